@@ -36,7 +36,8 @@ extern "C" {
 #define SEGTOPK_HIP_ERROR 3        /* a HIP runtime call or launch failed     */
 #define SEGTOPK_SCRATCH_TOO_SMALL 4 /* batched_topk_ex_noalloc: the request's
                                        plan needs more scratch than
-                                       SEGTOPK_STATIC_SCRATCH_BYTES          */
+                                       SEGTOPK_STATIC_SCRATCH_BYTES; operators
+                                       with a workspace: it is too small     */
 
 /* ---- key types ------------------------------------------------------- */
 /* Keys are compared by numeric value.  Floating-point keys: -0.0 and +0.0
@@ -248,6 +249,157 @@ int batched_topk_ex_noalloc(const segtopk_keys *keys, const segtopk_values *valu
                             int64_t num_segments, int64_t k, const int32_t *k_per_segment,
                             int64_t max_segment_size, int direction, int determinism,
                             int tie_break, int ordering, hipStream_t stream);
+
+/* ======================================================================
+ * Operators around the selection in a language model
+ *
+ * A router's top-k gives every token k experts: segtopk_sort_ids lists the
+ * (token, expert) slots expert by expert, segtopk_dispatch_rows copies the
+ * tokens into that order, segtopk_combine_rows brings the experts' results back
+ * with the gate weights applied.  A sampler's top-k gives the next token:
+ * segtopk_embedding_rows looks it up, and segtopk_policy_loss scores sampled
+ * tokens under the model's logits.  The *_backward functions, and
+ * segtopk_policy_loss with a gradient buffer, are their gradients.
+ *
+ * For all of them: pointers in the arguments are DEVICE pointers; the argument
+ * structs are host memory read during the call only.  A call validates, queues
+ * kernels on `stream` and returns without waiting; it allocates nothing, keeps
+ * nothing, copies nothing to the host, and may be captured into a graph.
+ * Element types are SEGTOPK_KEY_F32, _BF16 and _F16, id types SEGTOPK_KEY_I32
+ * and _I64.  Sums are held in 32 bits or more, in one fixed order, and rounded
+ * once: the same call gives the same bits every time.  Outputs must not overlap
+ * inputs unless stated.  Workspaces hold at least what the *_workspace function
+ * returns (bytes; 0 also for sizes that the call refuses), aligned to 256
+ * bytes; a smaller one is SEGTOPK_SCRATCH_TOO_SMALL, and NULL is allowed for 0
+ * bytes.  SEGTOPK_INVALID_ARGUMENT: a NULL or misaligned pointer, an unknown or
+ * unmatched type, a negative or too large size, a stride below the width; no
+ * work is queued then.
+ * ====================================================================== */
+
+/* Rows of a matrix: element c of row r is data[r * stride + c].  `stride` counts
+ * elements; rows need the alignment of one element only. */
+typedef struct segtopk_rows {
+    void *data;
+    int64_t stride;
+    int32_t type; /* a segtopk_key_type */
+} segtopk_rows;
+
+/*
+ * segtopk_sort_ids -- the stable sort of n ids into num_segments segments.
+ *
+ *   key_i = ids[i] if 0 <= ids[i] < num_segments, else num_segments (dropped)
+ *   order     [n] the slots i by key, equal keys by slot; dropped ones last
+ *   position  [n] its inverse: order[position[i]] = i
+ *   offsets   [num_segments + 1] segment s is order[offsets[s] .. offsets[s+1]);
+ *             offsets[num_segments] is the number of slots kept.  They serve as
+ *             batched_topk's segment_offsets.
+ * 0 <= n <= 2^31 - 1, 0 <= num_segments < 2^31 - 1.
+ */
+int64_t segtopk_sort_ids_workspace(int64_t n, int64_t num_segments);
+int segtopk_sort_ids(const void *ids, int32_t id_type, int64_t n, int64_t num_segments,
+                     int32_t *order, int32_t *position, int64_t *offsets, void *workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * segtopk_dispatch_rows -- tokens copied into expert order:
+ *   rows[position[t * k + j]] = x[t]
+ * x has `tokens` rows, `rows` tokens * k; both are `width` wide and of one type.
+ * A slot whose position is not below *kept is dropped and its row set to zero;
+ * `kept` is a device pointer (&offsets[num_segments] of the sort) or NULL: all
+ * are kept.  Slots whose position is outside [0, tokens * k) are skipped.
+ * `position` is a permutation; tokens * k <= 2^31 - 1.
+ */
+int segtopk_dispatch_rows(const segtopk_rows *x, const segtopk_rows *rows, int64_t tokens,
+                          int64_t k, int64_t width, const int32_t *position, const int64_t *kept,
+                          hipStream_t stream);
+
+/*
+ * segtopk_combine_rows -- rows in expert order summed into their tokens:
+ *   out[t] = sum_j weights[t * k + j] rows[position[t * k + j]]
+ * over the slots kept.  Rows of dropped slots are not read, whatever they hold.
+ * weights NULL: all one (the gradient of segtopk_dispatch_rows).  weight_type is
+ * SEGTOPK_KEY_F32 or the rows' type.
+ */
+int segtopk_combine_rows(const segtopk_rows *rows, const segtopk_rows *out, const void *weights,
+                         int32_t weight_type, int64_t tokens, int64_t k, int64_t width,
+                         const int32_t *position, const int64_t *kept, hipStream_t stream);
+
+/*
+ * segtopk_combine_rows_backward -- the gradient of segtopk_combine_rows:
+ *   drows[position[t * k + j]]  = weights[t * k + j] dout[t]
+ *   dweights[t * k + j] = <dout[t], rows[position[t * k + j]]>
+ * and zero for dropped slots.  dweights NULL: not wanted, and rows may be NULL.
+ * weights NULL: all one.  dweights is of weight_type.
+ */
+int segtopk_combine_rows_backward(const segtopk_rows *dout, const segtopk_rows *rows,
+                                  const segtopk_rows *drows, const void *weights, void *dweights,
+                                  int32_t weight_type, int64_t tokens, int64_t k, int64_t width,
+                                  const int32_t *position, const int64_t *kept,
+                                  hipStream_t stream);
+
+/*
+ * segtopk_embedding_rows -- out[i] = scale * table[ids[i]], rounded once; the
+ * row of an id outside [0, num_rows) is zero.
+ */
+int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_rows *out, const void *ids,
+                           int32_t id_type, int64_t n, int64_t num_rows, int64_t width,
+                           float scale, hipStream_t stream);
+
+/*
+ * segtopk_embedding_backward -- the gradient of the table:
+ *   dtable[v] = scale * sum over ids[i] = v of dout[i]
+ * All num_rows rows are written, most of them zero.  Ids outside [0, num_rows)
+ * add nothing, nor does padding_id (outside [0, num_rows): no padding).
+ * accumulate != 0: the sums are added to what dtable holds, and rows of ids that
+ * do not occur are neither read nor written.  dtable is of dout's type or
+ * SEGTOPK_KEY_F32.  SEGTOPK_NOT_SUPPORTED: more work than one launch holds
+ * (about n * width / 64 Ki + num_rows / 16 >= 2^24).
+ */
+int64_t segtopk_embedding_backward_workspace(int64_t n, int64_t num_rows, int64_t width);
+int segtopk_embedding_backward(const segtopk_rows *dout, const segtopk_rows *dtable,
+                               const void *ids, int32_t id_type, int64_t n, int64_t num_rows,
+                               int64_t width, float scale, int64_t padding_id, int32_t accumulate,
+                               void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * segtopk_policy_loss -- the clipped policy loss of sampled tokens with a KL
+ * term, and its gradient in the logits.
+ *
+ * Row t holds the logits that token_ids[t] was drawn from.  With
+ * z = logits[t] / temperature:
+ *   logp[t] = z[token] - log sum_c exp(z[c])
+ *   r = exp(logp - old_logp),  A = advantages[t]
+ *   term = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A)
+ *          + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1)
+ * Answer s is the rows segment_offsets[s] .. segment_offsets[s+1] (offsets do
+ * not decrease).  loss is the mean over the answers of the mean over each
+ * answer's live rows; an answer without one adds zero.  A row is live if its
+ * token is in [0, vocab) and it lies in an answer; the others, and rows whose
+ * logits are all -inf, have logp 0, no term and a gradient of zero, and what
+ * else they hold does not matter.  A logit of -inf is a token ruled out.
+ *
+ *   dlogits.data  NULL: no gradient.  Else grad_scale * d loss / d logits, of
+ *                 the logits' type; it may be the logits themselves (same
+ *                 data and stride).
+ *   ref_logp      may be NULL when kl_coef is 0
+ * 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0, temperature > 0;
+ * tokens < 2^22, num_segments < 2^24.
+ */
+typedef struct segtopk_policy_loss_args {
+    segtopk_rows logits, dlogits;
+    const void *token_ids;
+    int32_t id_type;
+    float clip_low, clip_high, kl_coef, temperature, grad_scale;
+    int64_t tokens, vocab, num_segments;
+    const int64_t *segment_offsets;
+    const float *old_logp, *ref_logp, *advantages;
+    float *loss; /* [1] */
+    float *logp; /* [tokens] */
+} segtopk_policy_loss_args;
+
+int64_t segtopk_policy_loss_workspace(int64_t tokens, int64_t vocab, int64_t num_segments);
+int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *workspace,
+                        int64_t workspace_bytes, hipStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *segtopk_status_string(int status);

@@ -6,6 +6,10 @@ tensors with torch when the caller does not pass them, and hands device
 pointers and the current HIP stream to ``batched_topk``.  Every step of the
 selection runs in the library's HIP kernels; there is no other code path, and
 the binding raises if the library is missing.
+
+The operators around the selection (expert sort, dispatch and combine, embedding
+rows, policy loss, and their gradients) are bound the same way in
+``model_ops`` and reached from here.
 """
 from __future__ import annotations
 
@@ -44,8 +48,8 @@ if hasattr(torch, "uint64"):
 
 
 class SegTopKError(RuntimeError):
-    def __init__(self, status: int):
-        super().__init__(f"batched_topk failed: {STATUS.get(status, 'unknown')} (status {status})")
+    def __init__(self, status: int, call: str = "batched_topk"):
+        super().__init__(f"{call} failed: {STATUS.get(status, 'unknown')} (status {status})")
         self.status = status
 
 
@@ -256,3 +260,7 @@ def batched_topk(keys: torch.Tensor, segment_offsets: torch.Tensor, k: int, *,
     if rc != 0:
         raise SegTopKError(rc)
     return out_keys, (out_values if values is not None else None)
+
+
+from .model_ops import (combine, combine_backward, dispatch, dispatch_backward,  # noqa: E402,F401
+                        embedding, embedding_backward, policy_loss, policy_loss_grad, sort_ids)

@@ -1,0 +1,259 @@
+// embedding_grad.hip -- the gradient of an embedding table:
+//   dtable[v] = scale * sum_{i : id_i = v} dout[i]      (v != padding)
+//
+// The tokens are sorted by id (sort_ids.hip); equal ids then lie in runs, and
+// the sorted tokens are cut into chunks of kChunk rows, so that a frequent
+// token costs no workgroup more than any other:
+//   sum_kernel     a workgroup adds up one chunk, 16 bytes of a row to a thread,
+//                  in 32 bits; a run inside the chunk goes to its row of the
+//                  table at once, a run that crosses the chunk's border leaves a
+//                  32-bit partial row.  Other workgroups of the same launch
+//                  write the zero rows of ids that no token has.
+//   finish_kernel  adds the partial rows of a run, chunk by chunk.
+// Every sum has one fixed order: results are the same every time.
+//
+// Bound by writing the table: most of its rows are zeros.
+#include "ops_common.h"
+
+namespace segtopk_ops {
+namespace {
+
+constexpr uint32_t kChunk = 32;
+constexpr uint32_t kZeroRows = 16;  // rows of the table that a workgroup looks up and clears
+
+struct GradArgs {
+    const int32_t *order;
+    const uint32_t *sorted;  // ids in order, num_rows for one outside the table
+    float *part;             // [chunks][2][width]: the run a chunk ends with, begins with
+    uint32_t n, chunks, num_rows, padding;  // padding >= num_rows: none
+    uint32_t pieces, units, cols;  // cols: workgroups side by side over a row
+    float scale;
+    uint32_t accumulate;
+    int64_t width, ds, ts;
+};
+
+// Whether the run at sorted place i goes into the table.
+__device__ inline bool counts(const GradArgs &a, uint32_t id) {
+    return id < a.num_rows && id != a.padding;
+}
+
+template <class O> __device__ inline void put(O *dst, float v, const GradArgs &a) {
+    v *= a.scale;
+    *dst = (O)(a.accumulate ? (float)*dst + v : v);
+}
+
+template <class T, class O>
+__device__ inline void put_piece(O *dst, typename Piece<T>::f32 v, const GradArgs &a) {
+    typedef O vec __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(O))));
+    vec *const d = reinterpret_cast<vec *>(dst);
+    v *= a.scale;
+    if (a.accumulate) v += __builtin_convertvector(*d, typename Piece<T>::f32);
+    *d = __builtin_convertvector(v, vec);
+}
+
+template <class T, class O>
+__global__ __launch_bounds__(kOpThreads) void sum_kernel(const T *__restrict__ dout, O *table,
+                                                         GradArgs a) {
+    using P = Piece<T>;
+    const uint32_t t = threadIdx.x;
+    if (blockIdx.x < a.chunks * a.cols) {
+        __shared__ uint32_t id[kChunk], row[kChunk];
+        const uint32_t chunk = blockIdx.x / a.cols, col = blockIdx.x % a.cols;
+        const uint32_t b = chunk * kChunk, m = min(kChunk, a.n - b);
+        if (t < m) {
+            id[t] = a.sorted[b + t];
+            row[t] = (uint32_t)a.order[b + t];
+        }
+        __syncthreads();
+        const bool joins = b && a.sorted[b - 1] == id[0];
+        const bool goes_on = b + m < a.n && a.sorted[b + m] == id[m - 1];
+        for (uint32_t u = col * kOpThreads + t; u < a.units; u += a.cols * kOpThreads) {
+            const bool whole = u < a.pieces;
+            const size_t at = whole ? (size_t)u * P::N : (size_t)a.pieces * P::N + (u - a.pieces);
+            typename P::f32 acc = 0.0f;
+            uint32_t first = 0;  // of the run that is being added
+            for (uint32_t i = 0; i < m; ++i) {
+                const T *src = dout + (int64_t)row[i] * a.ds + at;
+                if (counts(a, id[i])) {
+                    if (whole) acc += widen<T>(load_piece(src));
+                    else acc[0] += (float)*src;
+                }
+                if (i + 1 < m && id[i + 1] == id[i]) continue;
+                if (counts(a, id[i])) {
+                    const bool head = first == 0 && joins, tail = i + 1 == m && goes_on;
+                    if (head || tail) {
+                        float *dst = a.part + ((size_t)chunk * 2 + (head ? 1 : 0)) * a.width + at;
+                        typedef float mem
+                            __attribute__((ext_vector_type(16 / sizeof(T)), aligned(4)));
+                        if (whole) *reinterpret_cast<mem *>(dst) = acc;
+                        else *dst = acc[0];
+                    } else {
+                        O *dst = table + (int64_t)id[i] * a.ts + at;
+                        if (whole) put_piece<T>(dst, acc, a);
+                        else put(dst, acc[0], a);
+                    }
+                }
+                acc = 0.0f;
+                first = i + 1;
+            }
+        }
+        return;
+    }
+    // Rows of ids that no token has, and the padding's.
+    __shared__ uint32_t empty[kZeroRows];
+    const uint32_t v0 = (blockIdx.x - a.chunks * a.cols) * kZeroRows;
+    if (t < kZeroRows) {
+        const uint32_t v = v0 + t;
+        uint32_t lo = 0, hi = a.n;
+        while (lo < hi) {
+            const uint32_t mid = lo + ((hi - lo) >> 1);
+            if (a.sorted[mid] < v) lo = mid + 1;
+            else hi = mid;
+        }
+        empty[t] = v < a.num_rows && (lo >= a.n || a.sorted[lo] != v || v == a.padding);
+    }
+    __syncthreads();
+    using Q = Piece<O>;
+    const uint32_t pieces = (uint32_t)(a.width / Q::N);
+    for (uint32_t r = 0; r < kZeroRows; ++r) {
+        if (!empty[r]) continue;
+        O *dst = table + (int64_t)(v0 + r) * a.ts;
+        for (uint32_t u = t; u < pieces; u += kOpThreads)
+            store_piece(dst + (size_t)u * Q::N, (typename Q::vec)(O)0.0f);
+        for (size_t i = (size_t)pieces * Q::N + t; i < (size_t)a.width; i += kOpThreads)
+            dst[i] = (O)0.0f;
+    }
+}
+
+// One workgroup for a chunk that a run starts in and leaves: the partial rows
+// of that run, in the order of the chunks.
+template <class O>
+__global__ __launch_bounds__(kOpThreads) void finish_kernel(O *table, GradArgs a) {
+    const uint32_t chunk = blockIdx.x, b = chunk * kChunk;
+    const uint32_t e = b + kChunk;  // the next chunk is there: the grid leaves the last one out
+    const uint32_t id = a.sorted[e - 1];
+    if (!counts(a, id) || a.sorted[e] != id) return;
+    if (b && a.sorted[b - 1] == id) return;  // it started before this chunk
+    // How many chunks after this one the run reaches.
+    __shared__ uint32_t reach;
+    if (threadIdx.x == 0) {
+        uint32_t lo = e, hi = a.n;  // first place past the run
+        while (lo < hi) {
+            const uint32_t mid = lo + ((hi - lo) >> 1);
+            if (a.sorted[mid] <= id) lo = mid + 1;
+            else hi = mid;
+        }
+        reach = (lo - 1) / kChunk;
+    }
+    __syncthreads();
+    const uint32_t last = reach;
+    for (int64_t c = (int64_t)blockIdx.y * kOpThreads + threadIdx.x; c < a.width;
+         c += (int64_t)gridDim.y * kOpThreads) {
+        float acc = a.part[(size_t)chunk * 2 * a.width + c];
+        for (uint32_t i = chunk + 1; i <= last; ++i)
+            acc += a.part[((size_t)i * 2 + 1) * a.width + c];
+        put(table + (int64_t)id * a.ts + c, acc, a);
+    }
+}
+
+size_t round_up(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct GradPlan {
+    size_t sort_bytes, index_bytes, part_bytes, bytes;
+    uint32_t chunks;
+};
+
+GradPlan grad_plan(int64_t n, int64_t num_rows, int64_t width) {
+    GradPlan p;
+    p.chunks = (uint32_t)((n + kChunk - 1) / kChunk);
+    p.sort_bytes = round_up(sort_workspace(n, num_rows));
+    p.index_bytes = round_up((size_t)n * 4);
+    p.part_bytes = p.chunks > 1 ? (size_t)p.chunks * 2 * (size_t)width * 4 : 0;
+    p.bytes = p.sort_bytes + 2 * p.index_bytes + p.part_bytes;
+    return p;
+}
+
+template <class T, class O>
+hipError_t queue_grad(const segtopk_rows *dout, const segtopk_rows *dtable, GradArgs a,
+                      hipStream_t stream) {
+    const uint32_t zero = a.accumulate ? 0u : (a.num_rows + kZeroRows - 1) / kZeroRows;
+    const uint32_t grid = a.chunks * a.cols + zero;
+    if (!grid) return hipSuccess;
+    O *table = static_cast<O *>(dtable->data);
+    hipLaunchKernelGGL((sum_kernel<T, O>), dim3(grid), dim3(kOpThreads), 0, stream,
+                       static_cast<const T *>(dout ? dout->data : nullptr), table, a);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || a.chunks < 2) return err;
+    int64_t y = (a.width + kOpThreads - 1) / kOpThreads;
+    if (y > 65535) y = 65535;
+    hipLaunchKernelGGL(finish_kernel<O>, dim3(a.chunks - 1, (unsigned)y), dim3(kOpThreads), 0,
+                       stream, table, a);
+    return hipGetLastError();
+}
+
+bool good_sizes(int64_t n, int64_t num_rows, int64_t width) {
+    return n >= 0 && n <= INT32_MAX && num_rows >= 0 && num_rows < INT32_MAX && width >= 1 &&
+           width <= INT32_MAX;
+}
+
+}  // namespace
+}  // namespace segtopk_ops
+
+using namespace segtopk_ops;
+
+extern "C" int64_t segtopk_embedding_backward_workspace(int64_t n, int64_t num_rows,
+                                                        int64_t width) {
+    if (!good_sizes(n, num_rows, width)) return 0;
+    return (int64_t)grad_plan(n, num_rows, width).bytes;
+}
+
+extern "C" int segtopk_embedding_backward(const segtopk_rows *dout, const segtopk_rows *dtable,
+                                          const void *ids, int32_t id_type, int64_t n,
+                                          int64_t num_rows, int64_t width, float scale,
+                                          int64_t padding_id, int32_t accumulate, void *workspace,
+                                          int64_t workspace_bytes, hipStream_t stream) {
+    const int ib = index_bytes(id_type);
+    if (!ib || !good_sizes(n, num_rows, width)) return SEGTOPK_INVALID_ARGUMENT;
+    if (num_rows == 0) return SEGTOPK_OK;
+    if (!good_rows(dtable, width)) return SEGTOPK_INVALID_ARGUMENT;
+    if (n && (!ids || !aligned(ids, ib) || !good_rows(dout, width) ||
+              (dtable->type != dout->type && dtable->type != SEGTOPK_KEY_F32)))
+        return SEGTOPK_INVALID_ARGUMENT;
+    const GradPlan p = grad_plan(n, num_rows, width);
+    const int64_t per = 16 / element_bytes(n ? dout->type : dtable->type);
+    const int64_t units = width / per + width % per, cols = (units + kOpThreads - 1) / kOpThreads;
+    // A launch holds fewer than 2^32 threads.
+    if ((int64_t)p.chunks * cols + num_rows / kZeroRows >= (1 << 24) - 1)
+        return SEGTOPK_NOT_SUPPORTED;
+    if (p.bytes && (!workspace || !aligned(workspace, 256))) return SEGTOPK_INVALID_ARGUMENT;
+    if (workspace_bytes < 0 || (size_t)workspace_bytes < p.bytes) return SEGTOPK_SCRATCH_TOO_SMALL;
+
+    char *ws = static_cast<char *>(workspace);
+    int32_t *order = reinterpret_cast<int32_t *>(ws + p.sort_bytes);
+    uint32_t *sorted = reinterpret_cast<uint32_t *>(ws + p.sort_bytes + p.index_bytes);
+    if (n && queue_sort(ids, id_type, n, num_rows, order, nullptr, nullptr, sorted, workspace,
+                        stream) != hipSuccess)
+        return SEGTOPK_HIP_ERROR;
+    GradArgs a{};
+    a.order = order;
+    a.sorted = sorted;
+    a.part = reinterpret_cast<float *>(ws + p.sort_bytes + 2 * p.index_bytes);
+    a.n = (uint32_t)n;
+    a.chunks = p.chunks;
+    a.num_rows = (uint32_t)num_rows;
+    a.padding = padding_id >= 0 && padding_id < num_rows ? (uint32_t)padding_id : 0xFFFFFFFFu;
+    const int row_type = n ? dout->type : dtable->type;
+    a.pieces = (uint32_t)(width / per);
+    a.units = (uint32_t)units;
+    a.cols = (uint32_t)cols;
+    a.scale = scale;
+    a.accumulate = accumulate != 0;
+    a.width = width;
+    a.ds = n ? dout->stride : 0;
+    a.ts = dtable->stride;
+    return with_type(row_type, [&](auto t) {
+        using T = decltype(t);
+        return status(dtable->type == SEGTOPK_KEY_F32 ? queue_grad<T, float>(dout, dtable, a, stream)
+                                                      : queue_grad<T, T>(dout, dtable, a, stream));
+    });
+}

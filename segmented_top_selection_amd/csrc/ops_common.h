@@ -1,0 +1,84 @@
+// ops_common.h -- what the operators around the selection share: element
+// types, 16-byte pieces of rows that may start at any element, wave
+// reductions, and the host's checks and launch arithmetic.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "segtopk.h"
+
+namespace segtopk_ops {
+
+constexpr int kOpThreads = 256;
+
+// One 16-byte piece of a row.  Rows may start at any element (odd widths,
+// slices of wider rows), so the type claims the element's alignment only;
+// gfx950 serves such pieces with the same 16-byte memory instructions.
+template <class T> struct Piece {
+    static constexpr int N = 16 / (int)sizeof(T);
+    typedef T vec __attribute__((ext_vector_type(16 / sizeof(T))));
+    typedef T mem __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+    typedef float f32 __attribute__((ext_vector_type(16 / sizeof(T))));
+};
+
+template <class T> __device__ inline typename Piece<T>::vec load_piece(const T *p) {
+    return *reinterpret_cast<const typename Piece<T>::mem *>(p);
+}
+template <class T> __device__ inline void store_piece(T *p, typename Piece<T>::vec v) {
+    *reinterpret_cast<typename Piece<T>::mem *>(p) = v;
+}
+template <class T>
+__device__ inline typename Piece<T>::f32 widen(typename Piece<T>::vec v) {
+    return __builtin_convertvector(v, typename Piece<T>::f32);
+}
+// Rounds to nearest even.
+template <class T>
+__device__ inline typename Piece<T>::vec narrow(typename Piece<T>::f32 v) {
+    return __builtin_convertvector(v, typename Piece<T>::vec);
+}
+
+__device__ inline float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+// ---- host ---------------------------------------------------------------
+inline int element_bytes(int type) {
+    return type == SEGTOPK_KEY_F32 ? 4
+           : (type == SEGTOPK_KEY_BF16 || type == SEGTOPK_KEY_F16) ? 2 : 0;
+}
+inline int index_bytes(int type) {
+    return type == SEGTOPK_KEY_I32 ? 4 : type == SEGTOPK_KEY_I64 ? 8 : 0;
+}
+inline bool aligned(const void *p, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes) == 0;
+}
+// A matrix of at least one row that the call reads or writes.
+inline bool good_rows(const segtopk_rows *m, int64_t width) {
+    const int b = m ? element_bytes(m->type) : 0;
+    return b && m->data && aligned(m->data, b) && m->stride >= width;
+}
+inline int status(hipError_t e) { return e == hipSuccess ? SEGTOPK_OK : SEGTOPK_HIP_ERROR; }
+
+// Calls f with a value of the element type.
+template <class F> inline int with_type(int type, F f) {
+    switch (type) {
+    case SEGTOPK_KEY_F32: return f(float{});
+    case SEGTOPK_KEY_BF16: return f(__bf16{});
+    default: return f(_Float16{});
+    }
+}
+
+// The stable sort of n ids (sort_ids.hip), for the operators that need it
+// inside: any of `order`, `position`, `offsets` and `sorted` (the ids in order,
+// num_segments for a dropped one) may be nullptr.
+size_t sort_workspace(int64_t n, int64_t num_segments);
+hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t num_segments, int32_t *order,
+                      int32_t *position, int64_t *offsets, uint32_t *sorted, void *workspace,
+                      hipStream_t stream);
+
+}  // namespace segtopk_ops

@@ -1,0 +1,373 @@
+// rows.hip -- rows moved between token order and expert order, and rows looked
+// up in a table.
+//
+//   dispatch   rows[position[t, j]] = x[t]
+//   combine    out[t] = sum_j w[t, j] rows[position[t, j]]
+//   their gradients: dispatch's is combine without weights; combine's sends
+//   w[t, j] dout[t] to row position[t, j] and gives
+//   dw[t, j] = <dout[t], rows[position[t, j]]>
+//   embedding  out[i] = scale * table[id_i]
+//
+// A slot whose position is not below *kept is dropped: its packed row is
+// zero and it adds nothing.  Positions outside [0, tokens * k) are skipped.
+//
+// All are bound by memory: every row is read once and written once, because
+// the work is laid out by token.  A group of `lanes` threads takes one token;
+// a thread holds one 16-byte piece of it, so a token's row is read once for
+// its k copies (dispatch) or k gradients (combine backward), and a sum over k
+// rows stays in registers (32 bits).  Pieces past the last whole one are
+// single elements, one to a thread.
+#include "ops_common.h"
+
+namespace segtopk_ops {
+namespace {
+
+// How a row of `width` elements is cut up: `pieces` whole pieces, then
+// single elements, together `units`; a group of `lanes` (a power of two)
+// threads walks them.
+struct Cut {
+    uint32_t pieces, units, lanes;
+};
+
+struct Slots {
+    const int32_t *position;  // [tokens][k]
+    const int64_t *kept;      // or nullptr: all
+    uint32_t tokens, k, count;  // count = tokens * k
+};
+
+__device__ inline uint32_t kept_of(const Slots &s) {
+    if (!s.kept) return s.count;
+    const int64_t v = *s.kept;
+    return v < 0 ? 0u : v < (int64_t)s.count ? (uint32_t)v : s.count;
+}
+
+template <class T>
+__global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restrict__ x, int64_t xs,
+                                                              T *__restrict__ rows, int64_t rs,
+                                                              Slots s, Cut c) {
+    using P = Piece<T>;
+    const uint32_t kept = kept_of(s), per = kOpThreads / c.lanes;
+    for (uint32_t token = blockIdx.x * per + threadIdx.x / c.lanes; token < s.tokens;
+         token += gridDim.x * per) {
+        const int32_t *pos = s.position + (size_t)token * s.k;
+        const T *src = x + (int64_t)token * xs;
+        for (uint32_t u = blockIdx.y * c.lanes + (threadIdx.x & (c.lanes - 1u)); u < c.units;
+             u += gridDim.y * c.lanes) {
+            if (u < c.pieces) {
+                const typename P::vec v = load_piece(src + (size_t)u * P::N);
+                for (uint32_t j = 0; j < s.k; ++j) {
+                    const uint32_t p = (uint32_t)pos[j];
+                    if (p < s.count)
+                        store_piece(rows + (int64_t)p * rs + (size_t)u * P::N,
+                                    p < kept ? v : (typename P::vec)(T)0.0f);
+                }
+            } else {
+                const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
+                const T v = src[at];
+                for (uint32_t j = 0; j < s.k; ++j) {
+                    const uint32_t p = (uint32_t)pos[j];
+                    if (p < s.count) rows[(int64_t)p * rs + at] = p < kept ? v : (T)0.0f;
+                }
+            }
+        }
+    }
+}
+
+template <class T, class W>
+__global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict__ rows,
+                                                             int64_t rs, T *__restrict__ out,
+                                                             int64_t os,
+                                                             const W *__restrict__ weights,
+                                                             Slots s, Cut c) {
+    using P = Piece<T>;
+    const uint32_t kept = kept_of(s), per = kOpThreads / c.lanes;
+    for (uint32_t token = blockIdx.x * per + threadIdx.x / c.lanes; token < s.tokens;
+         token += gridDim.x * per) {
+        const int32_t *pos = s.position + (size_t)token * s.k;
+        const W *wt = weights ? weights + (size_t)token * s.k : nullptr;
+        T *dst = out + (int64_t)token * os;
+        for (uint32_t u = blockIdx.y * c.lanes + (threadIdx.x & (c.lanes - 1u)); u < c.units;
+             u += gridDim.y * c.lanes) {
+            if (u < c.pieces) {
+                typename P::f32 acc = 0.0f;
+    #pragma unroll 8
+                for (uint32_t j = 0; j < s.k; ++j) {
+                    const uint32_t p = (uint32_t)pos[j];
+                    if (p >= kept) continue;
+                    const float w = wt ? (float)wt[j] : 1.0f;
+                    acc += w * widen<T>(load_piece(rows + (int64_t)p * rs + (size_t)u * P::N));
+                }
+                store_piece(dst + (size_t)u * P::N, narrow<T>(acc));
+            } else {
+                const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
+                float acc = 0.0f;
+                for (uint32_t j = 0; j < s.k; ++j) {
+                    const uint32_t p = (uint32_t)pos[j];
+                    if (p >= kept) continue;
+                    acc += (wt ? (float)wt[j] : 1.0f) * (float)rows[(int64_t)p * rs + at];
+                }
+                dst[at] = (T)acc;
+            }
+        }
+    }
+}
+
+constexpr int kSlotsAtOnce = 8;  // dot products that a thread keeps in registers
+
+template <class T, class W>
+__global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
+    const T *__restrict__ dout, int64_t ds, const T *__restrict__ rows, int64_t rs,
+    T *__restrict__ drows, int64_t drs, const W *__restrict__ weights, W *__restrict__ dweights,
+    Slots s, Cut c) {
+    using P = Piece<T>;
+    __shared__ float part[kOpThreads / 64][kSlotsAtOnce];
+    const uint32_t lane = threadIdx.x & (c.lanes - 1u);  // lanes: 64 or all threads
+    const uint32_t kept = kept_of(s), per = kOpThreads / c.lanes;
+    for (uint32_t first = blockIdx.x * per; first < s.tokens; first += gridDim.x * per) {
+        const uint32_t token = first + threadIdx.x / c.lanes;
+        const bool live = token < s.tokens;
+        const T *g = dout + (int64_t)token * ds;
+        for (uint32_t j0 = 0; j0 < s.k; j0 += kSlotsAtOnce) {
+            const uint32_t m = min((uint32_t)kSlotsAtOnce, s.k - j0);
+            uint32_t p[kSlotsAtOnce];
+            float w[kSlotsAtOnce], dot[kSlotsAtOnce];
+    #pragma unroll
+            for (int j = 0; j < kSlotsAtOnce; ++j) {
+                const bool here = live && (uint32_t)j < m;
+                const size_t i = (size_t)token * s.k + j0 + j;
+                p[j] = here ? (uint32_t)s.position[i] : 0xFFFFFFFFu;
+                w[j] = here && weights ? (float)weights[i] : 1.0f;
+                if (p[j] >= kept) w[j] = 0.0f;
+                dot[j] = 0.0f;
+            }
+            if (live)
+                for (uint32_t u = lane; u < c.units; u += c.lanes) {
+                    if (u < c.pieces) {
+                        const size_t at = (size_t)u * P::N;
+                        const typename P::f32 d = widen<T>(load_piece(g + at));
+    #pragma unroll
+                        for (int j = 0; j < kSlotsAtOnce; ++j) {
+                            if (p[j] >= s.count) continue;
+                            if (p[j] < kept && dweights) {
+                                const typename P::f32 y =
+                                    widen<T>(load_piece(rows + (int64_t)p[j] * rs + at));
+    #pragma unroll
+                                for (int i = 0; i < P::N; ++i) dot[j] += d[i] * y[i];
+                            }
+                            typename P::f32 r = 0.0f;
+                            if (p[j] < kept) r = w[j] * d;
+                            store_piece(drows + (int64_t)p[j] * drs + at, narrow<T>(r));
+                        }
+                    } else {
+                        const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
+                        const float d = (float)g[at];
+    #pragma unroll
+                        for (int j = 0; j < kSlotsAtOnce; ++j) {
+                            if (p[j] >= s.count) continue;
+                            if (p[j] < kept && dweights)
+                                dot[j] += d * (float)rows[(int64_t)p[j] * rs + at];
+                            drows[(int64_t)p[j] * drs + at] = p[j] < kept ? (T)(w[j] * d) : (T)0.0f;
+                        }
+                    }
+                }
+            if (!dweights) continue;
+    #pragma unroll
+            for (int j = 0; j < kSlotsAtOnce; ++j) dot[j] = wave_sum(dot[j]);
+            if (c.lanes == 64u) {
+                if (live && lane == 0)
+    #pragma unroll
+                    for (int j = 0; j < kSlotsAtOnce; ++j)
+                        if ((uint32_t)j < m) dweights[(size_t)token * s.k + j0 + j] = (W)dot[j];
+            } else {
+                if ((threadIdx.x & 63u) == 0)
+    #pragma unroll
+                    for (int j = 0; j < kSlotsAtOnce; ++j) part[threadIdx.x >> 6][j] = dot[j];
+                __syncthreads();
+                if (threadIdx.x < m) {
+                    float v = 0.0f;
+                    for (int i = 0; i < kOpThreads / 64; ++i) v += part[i][threadIdx.x];
+                    dweights[(size_t)token * s.k + j0 + threadIdx.x] = (W)v;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+template <class T, class I>
+__global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restrict__ table,
+                                                               int64_t ts, T *__restrict__ out,
+                                                               int64_t os,
+                                                               const I *__restrict__ ids,
+                                                               uint32_t n, int64_t num_rows,
+                                                               float scale, Cut c) {
+    using P = Piece<T>;
+    const uint32_t per = kOpThreads / c.lanes;
+    for (uint32_t i = blockIdx.x * per + threadIdx.x / c.lanes; i < n; i += gridDim.x * per) {
+        const int64_t id = ids[i];
+        const bool there = id >= 0 && id < num_rows;
+        const T *src = table + (there ? id : 0) * ts;
+        T *dst = out + (int64_t)i * os;
+        for (uint32_t u = blockIdx.y * c.lanes + (threadIdx.x & (c.lanes - 1u)); u < c.units;
+             u += gridDim.y * c.lanes) {
+            if (u < c.pieces) {
+                typename P::f32 v = 0.0f;
+                if (there) v = scale * widen<T>(load_piece(src + (size_t)u * P::N));
+                store_piece(dst + (size_t)u * P::N, narrow<T>(v));
+            } else {
+                const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
+                dst[at] = there ? (T)(scale * (float)src[at]) : (T)0.0f;
+            }
+        }
+    }
+}
+
+Cut cut_of(int64_t width, int elem_bytes) {
+    const int64_t n = 16 / elem_bytes;
+    Cut c;
+    c.pieces = (uint32_t)(width / n);
+    c.units = (uint32_t)(width / n + width % n);
+    c.lanes = 8;
+    while (c.lanes < (uint32_t)kOpThreads && c.lanes < c.units) c.lanes <<= 1;
+    return c;
+}
+
+// A launch holds fewer than 2^32 threads in a direction; the kernels loop over
+// the tokens that are left.
+unsigned blocks_of(int64_t tokens, const Cut &c) {
+    const int64_t per = kOpThreads / c.lanes, most = 1 << 22;
+    const int64_t n = (tokens + per - 1) / per;
+    return (unsigned)(n < most ? n : most);
+}
+
+dim3 grid_of(int64_t tokens, const Cut &c) {
+    const uint32_t y = (c.units + c.lanes - 1) / c.lanes;
+    return dim3(blocks_of(tokens, c), y < 65535u ? y : 65535u);
+}
+
+bool good_slots(int64_t tokens, int64_t k, int64_t width, const int32_t *position,
+                const int64_t *kept) {
+    return tokens >= 0 && k >= 1 && width >= 1 && width <= INT32_MAX && k <= INT32_MAX &&
+           tokens <= INT32_MAX / k && (tokens == 0 || position) && aligned(position, 4) &&
+           aligned(kept, 8);
+}
+
+Slots slots_of(int64_t tokens, int64_t k, const int32_t *position, const int64_t *kept) {
+    return Slots{position, kept, (uint32_t)tokens, (uint32_t)k, (uint32_t)(tokens * k)};
+}
+
+// Weights are absent, of 32 bits, or of the rows' type.
+bool good_weights(const void *weights, int32_t weight_type, int row_type) {
+    if (!weights) return true;
+    return (weight_type == SEGTOPK_KEY_F32 || weight_type == row_type) &&
+           aligned(weights, element_bytes(weight_type));
+}
+
+}  // namespace
+}  // namespace segtopk_ops
+
+using namespace segtopk_ops;
+
+extern "C" int segtopk_dispatch_rows(const segtopk_rows *x, const segtopk_rows *rows,
+                                     int64_t tokens, int64_t k, int64_t width,
+                                     const int32_t *position, const int64_t *kept,
+                                     hipStream_t stream) {
+    if (!good_slots(tokens, k, width, position, kept)) return SEGTOPK_INVALID_ARGUMENT;
+    if (tokens == 0) return SEGTOPK_OK;
+    if (!good_rows(x, width) || !good_rows(rows, width) || x->type != rows->type)
+        return SEGTOPK_INVALID_ARGUMENT;
+    return with_type(x->type, [&](auto t) {
+        using T = decltype(t);
+        const Cut c = cut_of(width, sizeof(T));
+        hipLaunchKernelGGL(dispatch_kernel<T>, grid_of(tokens, c), dim3(kOpThreads), 0, stream,
+                           static_cast<const T *>(x->data), x->stride,
+                           static_cast<T *>(rows->data), rows->stride,
+                           slots_of(tokens, k, position, kept), c);
+        return status(hipGetLastError());
+    });
+}
+
+extern "C" int segtopk_combine_rows(const segtopk_rows *rows, const segtopk_rows *out,
+                                    const void *weights, int32_t weight_type, int64_t tokens,
+                                    int64_t k, int64_t width, const int32_t *position,
+                                    const int64_t *kept, hipStream_t stream) {
+    if (!good_slots(tokens, k, width, position, kept)) return SEGTOPK_INVALID_ARGUMENT;
+    if (tokens == 0) return SEGTOPK_OK;
+    if (!good_rows(rows, width) || !good_rows(out, width) || rows->type != out->type ||
+        !good_weights(weights, weight_type, rows->type))
+        return SEGTOPK_INVALID_ARGUMENT;
+    return with_type(rows->type, [&](auto t) {
+        using T = decltype(t);
+        const Cut c = cut_of(width, sizeof(T));
+        const auto go = [&](auto w) {
+            using W = decltype(w);
+            hipLaunchKernelGGL((combine_kernel<T, W>), grid_of(tokens, c), dim3(kOpThreads), 0,
+                               stream, static_cast<const T *>(rows->data), rows->stride,
+                               static_cast<T *>(out->data), out->stride,
+                               static_cast<const W *>(weights),
+                               slots_of(tokens, k, position, kept), c);
+            return status(hipGetLastError());
+        };
+        return weights && weight_type != SEGTOPK_KEY_F32 ? go(t) : go(float{});
+    });
+}
+
+extern "C" int segtopk_combine_rows_backward(const segtopk_rows *dout, const segtopk_rows *rows,
+                                             const segtopk_rows *drows, const void *weights,
+                                             void *dweights, int32_t weight_type, int64_t tokens,
+                                             int64_t k, int64_t width, const int32_t *position,
+                                             const int64_t *kept, hipStream_t stream) {
+    if (!good_slots(tokens, k, width, position, kept)) return SEGTOPK_INVALID_ARGUMENT;
+    if (tokens == 0) return SEGTOPK_OK;
+    if (!good_rows(dout, width) || !good_rows(drows, width) || dout->type != drows->type ||
+        !good_weights(weights, weight_type, dout->type) ||
+        !good_weights(dweights, weight_type, dout->type))
+        return SEGTOPK_INVALID_ARGUMENT;
+    // Without the weights' gradient the rows are not read.
+    if (dweights && (!good_rows(rows, width) || rows->type != dout->type))
+        return SEGTOPK_INVALID_ARGUMENT;
+    return with_type(dout->type, [&](auto t) {
+        using T = decltype(t);
+        Cut c = cut_of(width, sizeof(T));
+        c.lanes = c.units > 128u ? (uint32_t)kOpThreads : 64u;
+        const auto go = [&](auto w) {
+            using W = decltype(w);
+            hipLaunchKernelGGL((combine_backward_kernel<T, W>), dim3(blocks_of(tokens, c)), dim3(kOpThreads), 0,
+                               stream, static_cast<const T *>(dout->data), dout->stride,
+                               static_cast<const T *>(rows ? rows->data : nullptr),
+                               rows ? rows->stride : 0, static_cast<T *>(drows->data),
+                               drows->stride, static_cast<const W *>(weights),
+                               static_cast<W *>(dweights), slots_of(tokens, k, position, kept), c);
+            return status(hipGetLastError());
+        };
+        return (weights || dweights) && weight_type != SEGTOPK_KEY_F32 ? go(t) : go(float{});
+    });
+}
+
+extern "C" int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_rows *out,
+                                      const void *ids, int32_t id_type, int64_t n,
+                                      int64_t num_rows, int64_t width, float scale,
+                                      hipStream_t stream) {
+    const int ib = index_bytes(id_type);
+    if (!ib || n < 0 || n > INT32_MAX || num_rows < 0 || num_rows >= INT32_MAX || width < 1 ||
+        width > INT32_MAX)
+        return SEGTOPK_INVALID_ARGUMENT;
+    if (n == 0) return SEGTOPK_OK;
+    if (!ids || !aligned(ids, ib) || !good_rows(out, width)) return SEGTOPK_INVALID_ARGUMENT;
+    if (num_rows && (!good_rows(table, width) || table->type != out->type))
+        return SEGTOPK_INVALID_ARGUMENT;
+    return with_type(out->type, [&](auto t) {
+        using T = decltype(t);
+        const Cut c = cut_of(width, sizeof(T));
+        const auto go = [&](auto i) {
+            using I = decltype(i);
+            hipLaunchKernelGGL((embedding_kernel<T, I>), grid_of(n, c), dim3(kOpThreads), 0,
+                               stream, static_cast<const T *>(num_rows ? table->data : nullptr),
+                               num_rows ? table->stride : 0, static_cast<T *>(out->data),
+                               out->stride, static_cast<const I *>(ids), (uint32_t)n, num_rows,
+                               scale, c);
+            return status(hipGetLastError());
+        };
+        return id_type == SEGTOPK_KEY_I64 ? go(int64_t{}) : go(int32_t{});
+    });
+}

@@ -1,0 +1,179 @@
+"""CPU-side checks of the operators around the selection: every refusal fires
+before a HIP call or a dereference (the pointers below are not real), empty
+requests are no-ops, and workspace sizes are those of the documented sizes."""
+import ctypes
+
+import pytest
+import torch
+
+import segmented_top_selection_amd as st
+from segmented_top_selection_amd import model_ops as mo
+
+A, B, C, D, WS = 0x10000, 0x20000, 0x30000, 0x40000, 0x50000
+F32, BF16, I32, F16, I64 = 0, 1, 3, 4, 8
+OK, INVALID, NOT_SUPPORTED, TOO_SMALL = 0, 1, 2, 4
+
+
+def rows(data=A, stride=64, type=BF16):
+    return mo._Rows(data, stride, type)
+
+
+def sort_ids(ids=A, id_type=I32, n=100, segments=8, order=B, position=C, offsets=D, ws=WS,
+             ws_bytes=1 << 30):
+    return mo.entry("segtopk_sort_ids")(ids, id_type, n, segments, order, position, offsets, ws,
+                                        ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ids=None), dict(ids=A + 2), dict(id_type=F32), dict(id_type=-1), dict(id_type=I64, ids=A + 4),
+    dict(n=-1), dict(n=2 ** 31), dict(segments=-1), dict(segments=2 ** 31 - 1), dict(order=None),
+    dict(order=B + 1), dict(position=None), dict(position=C + 2), dict(offsets=None),
+    dict(offsets=D + 4), dict(n=5000, ws=None), dict(n=5000, ws=WS + 8),
+])
+def test_sort_ids_refusals(kw):
+    assert sort_ids(**kw) == INVALID
+
+
+def test_sort_ids_workspace():
+    need = mo.entry("segtopk_sort_ids_workspace")
+    assert need(100, 8) == 0  # one workgroup, one pass
+    assert need(-1, 8) == need(100, -1) == need(2 ** 31, 8) == 0
+    assert need(100000, 8) > 0 and need(100, 100000) > 0
+    assert need(100000, 200000) >= 4 * 4 * 100000
+    assert sort_ids(n=100000, ws_bytes=need(100000, 8) - 1) == TOO_SMALL
+    assert sort_ids(n=100000, ws_bytes=-1) == TOO_SMALL
+
+
+def dispatch(x=None, out=None, tokens=10, k=2, width=64, position=C, kept=D):
+    return mo.entry("segtopk_dispatch_rows")(x or rows(), out or rows(B), tokens, k, width,
+                                             position, kept, None)
+
+
+def combine(r=None, out=None, weights=WS, wtype=F32, tokens=10, k=2, width=64, position=C, kept=D):
+    return mo.entry("segtopk_combine_rows")(r or rows(), out or rows(B), weights, wtype, tokens, k,
+                                            width, position, kept, None)
+
+
+def backward(dout=None, r=None, dr=None, weights=WS, dweights=WS, wtype=F32, tokens=10, k=2,
+             width=64, position=C, kept=D):
+    return mo.entry("segtopk_combine_rows_backward")(
+        dout or rows(), r or rows(), dr or rows(B), weights, dweights, wtype, tokens, k, width,
+        position, kept, None)
+
+
+SLOTS = [dict(tokens=-1), dict(k=0), dict(k=-1), dict(width=0), dict(width=2 ** 31),
+         dict(position=None), dict(position=C + 2), dict(kept=D + 4), dict(tokens=2 ** 30, k=2),
+         dict(width=65)]
+
+
+@pytest.mark.parametrize("fn", [dispatch, combine, backward])
+@pytest.mark.parametrize("kw", SLOTS)
+def test_slot_refusals(fn, kw):
+    assert fn(**kw) == INVALID
+    assert fn(tokens=0) == OK
+
+
+def test_matrix_refusals():
+    for bad in (rows(None), rows(A + 1), rows(type=I32), rows(type=99), rows(stride=63)):
+        assert dispatch(x=bad) == dispatch(out=bad) == INVALID
+        assert combine(r=bad) == combine(out=bad) == INVALID
+        assert backward(dout=bad) == backward(dr=bad) == backward(r=bad) == INVALID
+    assert dispatch(out=rows(B, type=F16)) == combine(out=rows(B, type=F32)) == INVALID
+    assert backward(dr=rows(B, type=F16)) == backward(r=rows(type=F32)) == INVALID
+    for kw in (dict(wtype=F16), dict(wtype=I32), dict(weights=WS + 2), dict(wtype=BF16, weights=WS + 1)):
+        assert combine(**kw) == backward(**kw) == INVALID
+    assert backward(dweights=WS + 1, wtype=BF16) == INVALID
+
+
+def embed(table=None, out=None, ids=C, id_type=I64, n=10, num_rows=5, width=64):
+    return mo.entry("segtopk_embedding_rows")(table or rows(), out or rows(B), ids, id_type, n,
+                                              num_rows, width, 1.0, None)
+
+
+def embed_grad(dout=None, dtable=None, ids=C, id_type=I64, n=10, num_rows=5, width=64, ws=WS,
+               ws_bytes=1 << 30, padding=-1):
+    return mo.entry("segtopk_embedding_backward")(
+        dout or rows(), dtable or rows(B), ids, id_type, n, num_rows, width, 1.0, padding, 0, ws,
+        ws_bytes, None)
+
+
+@pytest.mark.parametrize("fn", [embed, embed_grad])
+@pytest.mark.parametrize("kw", [
+    dict(ids=None), dict(ids=C + 4), dict(id_type=BF16), dict(n=-1), dict(n=2 ** 31),
+    dict(num_rows=-1), dict(num_rows=2 ** 31 - 1), dict(width=0), dict(width=65),
+    dict(width=2 ** 31),
+])
+def test_embedding_refusals(fn, kw):
+    assert fn(**kw) == INVALID
+
+
+def test_embedding_matrix_refusals_and_empty_calls():
+    for bad in (rows(None), rows(A + 1), rows(type=I32), rows(stride=63), rows(type=F16)):
+        assert embed(table=bad) == embed_grad(dtable=bad) == INVALID
+    for bad in (rows(None), rows(A + 1), rows(type=I32), rows(stride=63)):
+        assert embed(out=bad) == embed_grad(dout=bad) == INVALID
+    assert embed(n=0) == OK and embed_grad(num_rows=0) == OK
+    need = mo.entry("segtopk_embedding_backward_workspace")
+    assert embed_grad(ws=None) == embed_grad(ws=WS + 4) == INVALID
+    assert embed_grad(ws_bytes=need(10, 5, 64) - 1) == TOO_SMALL
+    assert need(-1, 5, 64) == need(10, -5, 64) == need(10, 5, 0) == 0
+    # More work than one launch holds.
+    assert embed_grad(n=2 ** 30, ws_bytes=2 ** 62) == NOT_SUPPORTED
+    assert embed_grad(num_rows=2 ** 29, ws_bytes=2 ** 62) == NOT_SUPPORTED
+
+
+def policy(ws=WS, ws_bytes=1 << 30, **kw):
+    a = mo._PolicyLossArgs()
+    base = dict(logits=rows(), dlogits=rows(B), token_ids=C, id_type=I64, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.1, temperature=1.0, grad_scale=1.0, tokens=10, vocab=64,
+                num_segments=2, segment_offsets=D, old_logp=A, ref_logp=A, advantages=A, loss=A,
+                logp=B)
+    base.update(kw)
+    for name, v in base.items():
+        setattr(a, name, v)
+    return mo.entry("segtopk_policy_loss")(ctypes.byref(a), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(logits=rows(None)), dict(logits=rows(A + 1)), dict(logits=rows(stride=63)),
+    dict(logits=rows(type=I32)), dict(dlogits=rows(B, type=F32)), dict(dlogits=rows(B, stride=63)),
+    dict(dlogits=rows(B + 1)), dict(token_ids=None), dict(token_ids=C + 4), dict(id_type=F32),
+    dict(tokens=-1), dict(tokens=2 ** 22), dict(vocab=0), dict(vocab=65), dict(vocab=2 ** 31),
+    dict(num_segments=-1), dict(num_segments=2 ** 24), dict(segment_offsets=None),
+    dict(segment_offsets=D + 4), dict(old_logp=None), dict(old_logp=A + 2), dict(ref_logp=None),
+    dict(ref_logp=A + 1), dict(advantages=None), dict(advantages=A + 2), dict(loss=None),
+    dict(loss=A + 2), dict(logp=None), dict(logp=A + 2), dict(clip_low=-0.1), dict(clip_low=1.5),
+    dict(clip_low=float("nan")), dict(clip_high=-0.1), dict(clip_high=float("nan")),
+    dict(kl_coef=-1.0), dict(kl_coef=float("nan")), dict(kl_coef=float("inf")),
+    dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("nan")),
+    dict(temperature=float("inf")), dict(grad_scale=float("nan")),
+    dict(grad_scale=float("inf")), dict(ws=None), dict(ws=WS + 8),
+])
+def test_policy_refusals(kw):
+    assert policy(**kw) == INVALID
+
+
+def test_policy_null_struct_and_workspace():
+    assert mo.entry("segtopk_policy_loss")(None, None, 0, None) == INVALID
+    need = mo.entry("segtopk_policy_loss_workspace")
+    assert need(10, 64, 2) > 0
+    assert need(-1, 64, 2) == need(10, 0, 2) == need(10, 64, -1) == need(2 ** 22, 64, 2) == 0
+    assert policy(ws_bytes=need(10, 64, 2) - 1) == TOO_SMALL
+
+
+def test_binding_refuses_host_tensors_and_other_types():
+    x, pos = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    ids, off = torch.zeros(4, dtype=torch.int64), torch.zeros(3, dtype=torch.int64)
+    f = torch.zeros(4)
+    for call in (lambda: st.sort_ids(ids, 4), lambda: st.dispatch(x, pos, off),
+                 lambda: st.combine(x, pos, off), lambda: st.dispatch_backward(x, pos, off),
+                 lambda: st.combine_backward(x, x, pos, off), lambda: st.embedding(x, ids),
+                 lambda: st.embedding_backward(x, ids, 5),
+                 lambda: st.policy_loss(x, ids, f, f, off),
+                 lambda: st.policy_loss_grad(x, ids, f, f, off)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: st.sort_ids([1, 2], 4), lambda: st.dispatch(None, pos, off),
+                 lambda: st.embedding("t", ids), lambda: st.policy_loss(None, ids, f, f, off)):
+        with pytest.raises(TypeError):
+            call()
