@@ -2,7 +2,7 @@
 //   dtable[v] = scale * sum_{i : id_i = v} dout[i]      (v != padding)
 //
 // The tokens are sorted by id (sort_ids.hip); equal ids then lie in runs, and
-// the sorted tokens are cut into chunks of kChunk rows, so that a frequent
+// the sorted tokens are cut into chunks of 8 to 32 rows, so that a frequent
 // token costs no workgroup more than any other:
 //   sum_kernel     a workgroup adds up one chunk, 16 bytes of a row to a thread,
 //                  in 32 bits; a run inside the chunk goes to its row of the
@@ -18,14 +18,15 @@
 namespace segtopk_ops {
 namespace {
 
-constexpr uint32_t kChunk = 32;
+constexpr uint32_t kMaxChunk = 32;  // rows of dout that a workgroup adds up
+constexpr int kRowsAtOnce = 8;      // of which so many are in flight together
 constexpr uint32_t kZeroRows = 16;  // rows of the table that a workgroup looks up and clears
 
 struct GradArgs {
     const int32_t *order;
     const uint32_t *sorted;  // ids in order, num_rows for one outside the table
     float *part;             // [chunks][2][width]: the run a chunk ends with, begins with
-    uint32_t n, chunks, num_rows, padding;  // padding >= num_rows: none
+    uint32_t n, chunk, chunks, num_rows, padding;  // padding >= num_rows: none
     uint32_t pieces, units, cols;  // cols: workgroups side by side over a row
     float scale;
     uint32_t accumulate;
@@ -57,9 +58,9 @@ __global__ __launch_bounds__(kOpThreads) void sum_kernel(const T *__restrict__ d
     using P = Piece<T>;
     const uint32_t t = threadIdx.x;
     if (blockIdx.x < a.chunks * a.cols) {
-        __shared__ uint32_t id[kChunk], row[kChunk];
+        __shared__ uint32_t id[kMaxChunk], row[kMaxChunk];
         const uint32_t chunk = blockIdx.x / a.cols, col = blockIdx.x % a.cols;
-        const uint32_t b = chunk * kChunk, m = min(kChunk, a.n - b);
+        const uint32_t b = chunk * a.chunk, m = min(a.chunk, a.n - b);
         if (t < m) {
             id[t] = a.sorted[b + t];
             row[t] = (uint32_t)a.order[b + t];
@@ -72,29 +73,43 @@ __global__ __launch_bounds__(kOpThreads) void sum_kernel(const T *__restrict__ d
             const size_t at = whole ? (size_t)u * P::N : (size_t)a.pieces * P::N + (u - a.pieces);
             typename P::f32 acc = 0.0f;
             uint32_t first = 0;  // of the run that is being added
-            for (uint32_t i = 0; i < m; ++i) {
-                const T *src = dout + (int64_t)row[i] * a.ds + at;
-                if (counts(a, id[i])) {
-                    if (whole) acc += widen<T>(load_piece(src));
-                    else acc[0] += (float)*src;
+            for (uint32_t i0 = 0; i0 < m; i0 += kRowsAtOnce) {
+                uint32_t key[kRowsAtOnce + 1];
+                typename P::vec v[kRowsAtOnce];
+#pragma unroll
+                for (int r = 0; r <= kRowsAtOnce; ++r)  // past the chunk: no id
+                    key[r] = __builtin_amdgcn_readfirstlane(i0 + r < m ? id[i0 + r] : 0xFFFFFFFFu);
+#pragma unroll
+                for (int r = 0; r < kRowsAtOnce; ++r) {
+                    v[r] = (typename P::vec)(T)0.0f;
+                    if (!counts(a, key[r])) continue;
+                    const T *src = dout + (int64_t)row[i0 + r] * a.ds + at;
+                    if (whole) v[r] = load_piece(src);
+                    else v[r][0] = *src;
                 }
-                if (i + 1 < m && id[i + 1] == id[i]) continue;
-                if (counts(a, id[i])) {
-                    const bool head = first == 0 && joins, tail = i + 1 == m && goes_on;
-                    if (head || tail) {
-                        float *dst = a.part + ((size_t)chunk * 2 + (head ? 1 : 0)) * a.width + at;
-                        typedef float mem
-                            __attribute__((ext_vector_type(16 / sizeof(T)), aligned(4)));
-                        if (whole) *reinterpret_cast<mem *>(dst) = acc;
-                        else *dst = acc[0];
-                    } else {
-                        O *dst = table + (int64_t)id[i] * a.ts + at;
-                        if (whole) put_piece<T>(dst, acc, a);
-                        else put(dst, acc[0], a);
+#pragma unroll
+                for (int r = 0; r < kRowsAtOnce; ++r) {
+                    if (key[r] == 0xFFFFFFFFu) continue;
+                    acc += widen<T>(v[r]);
+                    if (key[r + 1] == key[r]) continue;
+                    const uint32_t i = i0 + r;
+                    if (counts(a, key[r])) {
+                        const bool head = first == 0 && joins, tail = i + 1 == m && goes_on;
+                        if (head || tail) {
+                            float *dst = a.part + ((size_t)chunk * 2 + (head ? 1 : 0)) * a.width + at;
+                            typedef float mem
+                                __attribute__((ext_vector_type(16 / sizeof(T)), aligned(4)));
+                            if (whole) *reinterpret_cast<mem *>(dst) = acc;
+                            else *dst = acc[0];
+                        } else {
+                            O *dst = table + (int64_t)key[r] * a.ts + at;
+                            if (whole) put_piece<T>(dst, acc, a);
+                            else put(dst, acc[0], a);
+                        }
                     }
+                    acc = 0.0f;
+                    first = i + 1;
                 }
-                acc = 0.0f;
-                first = i + 1;
             }
         }
         return;
@@ -125,34 +140,56 @@ __global__ __launch_bounds__(kOpThreads) void sum_kernel(const T *__restrict__ d
     }
 }
 
-// One workgroup for a chunk that a run starts in and leaves: the partial rows
-// of that run, in the order of the chunks.
+// A workgroup for a chunk that a run starts in and leaves adds the partial rows
+// of that run: 64 lanes side by side over the columns, four to a lane, and
+// four waves over the chunks, each with eight partial rows in flight.
 template <class O>
 __global__ __launch_bounds__(kOpThreads) void finish_kernel(O *table, GradArgs a) {
-    const uint32_t chunk = blockIdx.x, b = chunk * kChunk;
-    const uint32_t e = b + kChunk;  // the next chunk is there: the grid leaves the last one out
-    const uint32_t id = a.sorted[e - 1];
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    typedef float f4mem __attribute__((ext_vector_type(4), aligned(4)));
+    constexpr uint32_t kWaves = kOpThreads / 64;
+    const uint32_t chunk = blockIdx.x, b = chunk * a.chunk;
+    const uint32_t e = b + a.chunk;  // the next chunk is there: the grid leaves the last one out
+    const uint32_t id = a.sorted[e - 1], before = b ? a.sorted[b - 1] : 0xFFFFFFFFu;
     if (!counts(a, id) || a.sorted[e] != id) return;
-    if (b && a.sorted[b - 1] == id) return;  // it started before this chunk
-    // How many chunks after this one the run reaches.
-    __shared__ uint32_t reach;
-    if (threadIdx.x == 0) {
-        uint32_t lo = e, hi = a.n;  // first place past the run
-        while (lo < hi) {
-            const uint32_t mid = lo + ((hi - lo) >> 1);
-            if (a.sorted[mid] <= id) lo = mid + 1;
-            else hi = mid;
-        }
-        reach = (lo - 1) / kChunk;
+    if (before == id) return;  // the run started before this chunk
+    const uint32_t lane = threadIdx.x & 63u, w = threadIdx.x >> 6;
+    // The run reaches into the chunks whose first row is of the same id.
+    uint32_t last = chunk + 1;
+    while (true) {
+        const uint32_t c = last + 1 + lane;
+        const uint64_t same = __ballot(c < a.chunks && a.sorted[c * a.chunk] == id);
+        const uint32_t run = same == ~0ull ? 64u : (uint32_t)__builtin_ctzll(~same);
+        last += run;
+        if (run < 64u) break;
     }
-    __syncthreads();
-    const uint32_t last = reach;
-    for (int64_t c = (int64_t)blockIdx.y * kOpThreads + threadIdx.x; c < a.width;
-         c += (int64_t)gridDim.y * kOpThreads) {
-        float acc = a.part[(size_t)chunk * 2 * a.width + c];
-        for (uint32_t i = chunk + 1; i <= last; ++i)
-            acc += a.part[((size_t)i * 2 + 1) * a.width + c];
-        put(table + (int64_t)id * a.ts + c, acc, a);
+    __shared__ f4 part[kWaves][64];
+    for (int64_t c0 = (int64_t)blockIdx.y * 256; c0 < a.width; c0 += (int64_t)gridDim.y * 256) {
+        const int64_t c = c0 + lane * 4;
+        const bool whole = c + 4 <= a.width;
+        const uint32_t rest = c < a.width && !whole ? (uint32_t)(a.width - c) : 0u;
+        f4 acc = 0.0f;
+#pragma unroll 8
+        for (uint32_t i = chunk + w; i <= last; i += kWaves) {
+            const float *src = a.part + ((size_t)i * 2 + (i == chunk ? 0 : 1)) * a.width + c;
+            if (whole) acc += *reinterpret_cast<const f4mem *>(src);
+            else if (rest) {
+                acc[0] += src[0];
+                if (rest > 1) acc[1] += src[1];
+                if (rest > 2) acc[2] += src[2];
+            }
+        }
+        part[w][lane] = acc;
+        __syncthreads();
+        if (w == 0) {
+            for (uint32_t i = 1; i < kWaves; ++i) acc += part[i][lane];
+            O *dst = table + (int64_t)id * a.ts + c;
+            if (whole || rest) put(dst, acc[0], a);
+            if (whole || rest > 1) put(dst + 1, acc[1], a);
+            if (whole || rest > 2) put(dst + 2, acc[2], a);
+            if (whole) put(dst + 3, acc[3], a);
+        }
+        __syncthreads();
     }
 }
 
@@ -160,12 +197,15 @@ size_t round_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct GradPlan {
     size_t sort_bytes, index_bytes, part_bytes, bytes;
-    uint32_t chunks;
+    uint32_t chunk, chunks;
 };
 
 GradPlan grad_plan(int64_t n, int64_t num_rows, int64_t width) {
     GradPlan p;
-    p.chunks = (uint32_t)((n + kChunk - 1) / kChunk);
+    // Long chunks leave few partial rows; shorter ones fill the device where
+    // there are few tokens.
+    p.chunk = n >= 16384 ? kMaxChunk : n >= 8192 ? 16u : 8u;
+    p.chunks = (uint32_t)((n + p.chunk - 1) / p.chunk);
     p.sort_bytes = round_up(sort_workspace(n, num_rows));
     p.index_bytes = round_up((size_t)n * 4);
     p.part_bytes = p.chunks > 1 ? (size_t)p.chunks * 2 * (size_t)width * 4 : 0;
@@ -184,10 +224,9 @@ hipError_t queue_grad(const segtopk_rows *dout, const segtopk_rows *dtable, Grad
                        static_cast<const T *>(dout ? dout->data : nullptr), table, a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.chunks < 2) return err;
-    int64_t y = (a.width + kOpThreads - 1) / kOpThreads;
-    if (y > 65535) y = 65535;
-    hipLaunchKernelGGL(finish_kernel<O>, dim3(a.chunks - 1, (unsigned)y), dim3(kOpThreads), 0,
-                       stream, table, a);
+    const int64_t y = (a.width + 255) / 256;
+    hipLaunchKernelGGL(finish_kernel<O>, dim3(a.chunks - 1, (unsigned)(y < 64 ? y : 64)),
+                       dim3(kOpThreads), 0, stream, table, a);
     return hipGetLastError();
 }
 
@@ -239,6 +278,7 @@ extern "C" int segtopk_embedding_backward(const segtopk_rows *dout, const segtop
     a.sorted = sorted;
     a.part = reinterpret_cast<float *>(ws + p.sort_bytes + 2 * p.index_bytes);
     a.n = (uint32_t)n;
+    a.chunk = p.chunk;
     a.chunks = p.chunks;
     a.num_rows = (uint32_t)num_rows;
     a.padding = padding_id >= 0 && padding_id < num_rows ? (uint32_t)padding_id : 0xFFFFFFFFu;

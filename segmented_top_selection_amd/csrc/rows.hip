@@ -17,6 +17,8 @@
 // its k copies (dispatch) or k gradients (combine backward), and a sum over k
 // rows stays in registers (32 bits).  Pieces past the last whole one are
 // single elements, one to a thread.
+#include <type_traits>
+
 #include "ops_common.h"
 
 namespace segtopk_ops {
@@ -28,6 +30,8 @@ namespace {
 struct Cut {
     uint32_t pieces, units, lanes;
 };
+
+constexpr int kSlotsAtOnce = 8;  // a token's slots that a thread works on together
 
 struct Slots {
     const int32_t *position;  // [tokens][k]
@@ -41,13 +45,23 @@ __device__ inline uint32_t kept_of(const Slots &s) {
     return v < 0 ? 0u : v < (int64_t)s.count ? (uint32_t)v : s.count;
 }
 
-template <class T>
+// A value that all lanes of a wave share, in a scalar register.  Rows of 64
+// units or more have a wave to themselves (ONE): what belongs to the token is
+// the wave's then, which takes its addresses out of the vector registers.
+template <bool ONE> __device__ inline uint32_t shared(uint32_t v) {
+    return ONE ? (uint32_t)__builtin_amdgcn_readfirstlane((int)v) : v;
+}
+template <bool ONE> __device__ inline float shared(float v) {
+    return ONE ? __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))) : v;
+}
+
+template <class T, bool ONE>
 __global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restrict__ x, int64_t xs,
                                                               T *__restrict__ rows, int64_t rs,
                                                               Slots s, Cut c) {
     using P = Piece<T>;
     const uint32_t kept = kept_of(s), per = kOpThreads / c.lanes;
-    for (uint32_t token = blockIdx.x * per + threadIdx.x / c.lanes; token < s.tokens;
+    for (uint32_t token = blockIdx.x * per + shared<ONE>(threadIdx.x / c.lanes); token < s.tokens;
          token += gridDim.x * per) {
         const int32_t *pos = s.position + (size_t)token * s.k;
         const T *src = x + (int64_t)token * xs;
@@ -56,7 +70,7 @@ __global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restric
             if (u < c.pieces) {
                 const typename P::vec v = load_piece(src + (size_t)u * P::N);
                 for (uint32_t j = 0; j < s.k; ++j) {
-                    const uint32_t p = (uint32_t)pos[j];
+                    const uint32_t p = shared<ONE>((uint32_t)pos[j]);
                     if (p < s.count)
                         store_piece(rows + (int64_t)p * rs + (size_t)u * P::N,
                                     p < kept ? v : (typename P::vec)(T)0.0f);
@@ -65,7 +79,7 @@ __global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restric
                 const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
                 const T v = src[at];
                 for (uint32_t j = 0; j < s.k; ++j) {
-                    const uint32_t p = (uint32_t)pos[j];
+                    const uint32_t p = shared<ONE>((uint32_t)pos[j]);
                     if (p < s.count) rows[(int64_t)p * rs + at] = p < kept ? v : (T)0.0f;
                 }
             }
@@ -73,7 +87,7 @@ __global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restric
     }
 }
 
-template <class T, class W>
+template <class T, class W, bool ONE>
 __global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict__ rows,
                                                              int64_t rs, T *__restrict__ out,
                                                              int64_t os,
@@ -81,7 +95,7 @@ __global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict
                                                              Slots s, Cut c) {
     using P = Piece<T>;
     const uint32_t kept = kept_of(s), per = kOpThreads / c.lanes;
-    for (uint32_t token = blockIdx.x * per + threadIdx.x / c.lanes; token < s.tokens;
+    for (uint32_t token = blockIdx.x * per + shared<ONE>(threadIdx.x / c.lanes); token < s.tokens;
          token += gridDim.x * per) {
         const int32_t *pos = s.position + (size_t)token * s.k;
         const W *wt = weights ? weights + (size_t)token * s.k : nullptr;
@@ -90,19 +104,33 @@ __global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict
              u += gridDim.y * c.lanes) {
             if (u < c.pieces) {
                 typename P::f32 acc = 0.0f;
-    #pragma unroll 8
-                for (uint32_t j = 0; j < s.k; ++j) {
-                    const uint32_t p = (uint32_t)pos[j];
-                    if (p >= kept) continue;
-                    const float w = wt ? (float)wt[j] : 1.0f;
-                    acc += w * widen<T>(load_piece(rows + (int64_t)p * rs + (size_t)u * P::N));
+                // The rows of up to eight slots are in flight together.
+                for (uint32_t j0 = 0; j0 < s.k; j0 += kSlotsAtOnce) {
+                    uint32_t p[kSlotsAtOnce];
+                    float w[kSlotsAtOnce];
+                    typename P::vec v[kSlotsAtOnce];
+#pragma unroll
+                    for (int j = 0; j < kSlotsAtOnce; ++j) {
+                        const bool here = j0 + j < s.k;
+                        p[j] = shared<ONE>(here ? (uint32_t)pos[j0 + j] : 0xFFFFFFFFu);
+                        w[j] = shared<ONE>(here && wt ? (float)wt[j0 + j] : 1.0f);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kSlotsAtOnce; ++j) {
+                        v[j] = (typename P::vec)(T)0.0f;
+                        if (p[j] < kept)
+                            v[j] = load_piece(rows + (int64_t)p[j] * rs + (size_t)u * P::N);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kSlotsAtOnce; ++j)
+                        if (p[j] < kept) acc += w[j] * widen<T>(v[j]);
                 }
                 store_piece(dst + (size_t)u * P::N, narrow<T>(acc));
             } else {
                 const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
                 float acc = 0.0f;
                 for (uint32_t j = 0; j < s.k; ++j) {
-                    const uint32_t p = (uint32_t)pos[j];
+                    const uint32_t p = shared<ONE>((uint32_t)pos[j]);
                     if (p >= kept) continue;
                     acc += (wt ? (float)wt[j] : 1.0f) * (float)rows[(int64_t)p * rs + at];
                 }
@@ -111,8 +139,6 @@ __global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict
         }
     }
 }
-
-constexpr int kSlotsAtOnce = 8;  // dot products that a thread keeps in registers
 
 template <class T, class W>
 __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
@@ -124,19 +150,19 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
     const uint32_t lane = threadIdx.x & (c.lanes - 1u);  // lanes: 64 or all threads
     const uint32_t kept = kept_of(s), per = kOpThreads / c.lanes;
     for (uint32_t first = blockIdx.x * per; first < s.tokens; first += gridDim.x * per) {
-        const uint32_t token = first + threadIdx.x / c.lanes;
+        const uint32_t token = first + shared<true>(threadIdx.x / c.lanes);
         const bool live = token < s.tokens;
         const T *g = dout + (int64_t)token * ds;
         for (uint32_t j0 = 0; j0 < s.k; j0 += kSlotsAtOnce) {
             const uint32_t m = min((uint32_t)kSlotsAtOnce, s.k - j0);
             uint32_t p[kSlotsAtOnce];
             float w[kSlotsAtOnce], dot[kSlotsAtOnce];
-    #pragma unroll
+#pragma unroll
             for (int j = 0; j < kSlotsAtOnce; ++j) {
                 const bool here = live && (uint32_t)j < m;
                 const size_t i = (size_t)token * s.k + j0 + j;
-                p[j] = here ? (uint32_t)s.position[i] : 0xFFFFFFFFu;
-                w[j] = here && weights ? (float)weights[i] : 1.0f;
+                p[j] = shared<true>(here ? (uint32_t)s.position[i] : 0xFFFFFFFFu);
+                w[j] = shared<true>(here && weights ? (float)weights[i] : 1.0f);
                 if (p[j] >= kept) w[j] = 0.0f;
                 dot[j] = 0.0f;
             }
@@ -145,23 +171,31 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
                     if (u < c.pieces) {
                         const size_t at = (size_t)u * P::N;
                         const typename P::f32 d = widen<T>(load_piece(g + at));
-    #pragma unroll
+                        typename P::vec y[kSlotsAtOnce];
+#pragma unroll
+                        for (int j = 0; j < kSlotsAtOnce; ++j) {
+                            y[j] = (typename P::vec)(T)0.0f;
+                            if (p[j] < kept && dweights)
+                                y[j] = load_piece(rows + (int64_t)p[j] * rs + at);
+                        }
+#pragma unroll
                         for (int j = 0; j < kSlotsAtOnce; ++j) {
                             if (p[j] >= s.count) continue;
-                            if (p[j] < kept && dweights) {
-                                const typename P::f32 y =
-                                    widen<T>(load_piece(rows + (int64_t)p[j] * rs + at));
-    #pragma unroll
-                                for (int i = 0; i < P::N; ++i) dot[j] += d[i] * y[i];
-                            }
                             typename P::f32 r = 0.0f;
                             if (p[j] < kept) r = w[j] * d;
                             store_piece(drows + (int64_t)p[j] * drs + at, narrow<T>(r));
                         }
+#pragma unroll
+                        for (int j = 0; j < kSlotsAtOnce; ++j) {
+                            if (p[j] >= kept) continue;
+                            const typename P::f32 v = widen<T>(y[j]);
+#pragma unroll
+                            for (int i = 0; i < P::N; ++i) dot[j] += d[i] * v[i];
+                        }
                     } else {
                         const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
                         const float d = (float)g[at];
-    #pragma unroll
+#pragma unroll
                         for (int j = 0; j < kSlotsAtOnce; ++j) {
                             if (p[j] >= s.count) continue;
                             if (p[j] < kept && dweights)
@@ -171,16 +205,16 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
                     }
                 }
             if (!dweights) continue;
-    #pragma unroll
+#pragma unroll
             for (int j = 0; j < kSlotsAtOnce; ++j) dot[j] = wave_sum(dot[j]);
             if (c.lanes == 64u) {
                 if (live && lane == 0)
-    #pragma unroll
+#pragma unroll
                     for (int j = 0; j < kSlotsAtOnce; ++j)
                         if ((uint32_t)j < m) dweights[(size_t)token * s.k + j0 + j] = (W)dot[j];
             } else {
                 if ((threadIdx.x & 63u) == 0)
-    #pragma unroll
+#pragma unroll
                     for (int j = 0; j < kSlotsAtOnce; ++j) part[threadIdx.x >> 6][j] = dot[j];
                 __syncthreads();
                 if (threadIdx.x < m) {
@@ -194,7 +228,9 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
     }
 }
 
-template <class T, class I>
+// A group of threads takes ROWS rows, so that a thread has that many loads in
+// flight.
+template <class T, class I, int ROWS>
 __global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restrict__ table,
                                                                int64_t ts, T *__restrict__ out,
                                                                int64_t os,
@@ -203,24 +239,43 @@ __global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restri
                                                                float scale, Cut c) {
     using P = Piece<T>;
     const uint32_t per = kOpThreads / c.lanes;
-    for (uint32_t i = blockIdx.x * per + threadIdx.x / c.lanes; i < n; i += gridDim.x * per) {
-        const int64_t id = ids[i];
-        const bool there = id >= 0 && id < num_rows;
-        const T *src = table + (there ? id : 0) * ts;
-        T *dst = out + (int64_t)i * os;
+    for (uint32_t i0 = blockIdx.x * per * ROWS + threadIdx.x / c.lanes; i0 < n;
+         i0 += gridDim.x * per * ROWS) {
+        int64_t id[ROWS];  // -1: a row of zeros
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const uint32_t i = i0 + r * per;
+            id[r] = i < n ? (int64_t)ids[i] : -1;
+            if (id[r] >= num_rows) id[r] = -1;
+        }
         for (uint32_t u = blockIdx.y * c.lanes + (threadIdx.x & (c.lanes - 1u)); u < c.units;
              u += gridDim.y * c.lanes) {
             if (u < c.pieces) {
-                typename P::f32 v = 0.0f;
-                if (there) v = scale * widen<T>(load_piece(src + (size_t)u * P::N));
-                store_piece(dst + (size_t)u * P::N, narrow<T>(v));
+                const size_t at = (size_t)u * P::N;
+                typename P::vec v[ROWS];
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    v[r] = (typename P::vec)(T)0.0f;
+                    if (id[r] >= 0) v[r] = load_piece(table + id[r] * ts + at);
+                }
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r)
+                    if (i0 + r * per < n)
+                        store_piece(out + (int64_t)(i0 + r * per) * os + at,
+                                    id[r] >= 0 ? narrow<T>(scale * widen<T>(v[r])) : v[r]);
             } else {
                 const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
-                dst[at] = there ? (T)(scale * (float)src[at]) : (T)0.0f;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r)
+                    if (i0 + r * per < n)
+                        out[(int64_t)(i0 + r * per) * os + at] =
+                            id[r] >= 0 ? (T)(scale * (float)table[id[r] * ts + at]) : (T)0.0f;
             }
         }
     }
 }
+
+constexpr int64_t kManyPieces = 4 * 256 * 2048;  // four for each thread that 256 CUs hold
 
 Cut cut_of(int64_t width, int elem_bytes) {
     const int64_t n = 16 / elem_bytes;
@@ -279,7 +334,7 @@ extern "C" int segtopk_dispatch_rows(const segtopk_rows *x, const segtopk_rows *
     return with_type(x->type, [&](auto t) {
         using T = decltype(t);
         const Cut c = cut_of(width, sizeof(T));
-        hipLaunchKernelGGL(dispatch_kernel<T>, grid_of(tokens, c), dim3(kOpThreads), 0, stream,
+        hipLaunchKernelGGL((c.lanes >= 64u ? dispatch_kernel<T, true> : dispatch_kernel<T, false>), grid_of(tokens, c), dim3(kOpThreads), 0, stream,
                            static_cast<const T *>(x->data), x->stride,
                            static_cast<T *>(rows->data), rows->stride,
                            slots_of(tokens, k, position, kept), c);
@@ -301,8 +356,9 @@ extern "C" int segtopk_combine_rows(const segtopk_rows *rows, const segtopk_rows
         const Cut c = cut_of(width, sizeof(T));
         const auto go = [&](auto w) {
             using W = decltype(w);
-            hipLaunchKernelGGL((combine_kernel<T, W>), grid_of(tokens, c), dim3(kOpThreads), 0,
-                               stream, static_cast<const T *>(rows->data), rows->stride,
+            hipLaunchKernelGGL(
+                (c.lanes >= 64u ? combine_kernel<T, W, true> : combine_kernel<T, W, false>),
+                grid_of(tokens, c), dim3(kOpThreads), 0, stream, static_cast<const T *>(rows->data), rows->stride,
                                static_cast<T *>(out->data), out->stride,
                                static_cast<const W *>(weights),
                                slots_of(tokens, k, position, kept), c);
@@ -359,15 +415,23 @@ extern "C" int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_r
     return with_type(out->type, [&](auto t) {
         using T = decltype(t);
         const Cut c = cut_of(width, sizeof(T));
-        const auto go = [&](auto i) {
+        // Four rows a thread once there is work for every wave the device holds.
+        const bool many = n * c.units >= kManyPieces;
+        const dim3 grid = grid_of(many ? (n + 3) / 4 : n, c);
+        const auto go = [&](auto i, auto rows) {
             using I = decltype(i);
-            hipLaunchKernelGGL((embedding_kernel<T, I>), grid_of(n, c), dim3(kOpThreads), 0,
-                               stream, static_cast<const T *>(num_rows ? table->data : nullptr),
+            hipLaunchKernelGGL((embedding_kernel<T, I, decltype(rows)::value>), grid,
+                               dim3(kOpThreads), 0, stream,
+                               static_cast<const T *>(num_rows ? table->data : nullptr),
                                num_rows ? table->stride : 0, static_cast<T *>(out->data),
                                out->stride, static_cast<const I *>(ids), (uint32_t)n, num_rows,
                                scale, c);
             return status(hipGetLastError());
         };
-        return id_type == SEGTOPK_KEY_I64 ? go(int64_t{}) : go(int32_t{});
+        const auto by_rows = [&](auto i) {
+            return many ? go(i, std::integral_constant<int, 4>{})
+                        : go(i, std::integral_constant<int, 1>{});
+        };
+        return id_type == SEGTOPK_KEY_I64 ? by_rows(int64_t{}) : by_rows(int32_t{});
     });
 }

@@ -2,16 +2,19 @@
 // order = stable argsort of key_i, where key_i = id_i inside [0, S) and S
 // otherwise; position = its inverse; offsets[s] = #{i : key_i < s}.
 //
-// Least-significant-digit radix passes of at most 9 bits.  A pass splits the
-// items into consecutive chunks, one workgroup of 16 waves each, and a chunk
-// into 16 consecutive parts, one for each wave:
-//   count_kernel    digit histogram of each chunk
-//   scatter_kernel  where a chunk's items of digit d start: all items of smaller
-//                   digits, and those of d in earlier chunks and waves; then
-//                   each wave takes its items 64 at a time, ranks equal digits
-//                   by the lanes below (one ballot a bit) and writes them.
-// One chunk needs no count_kernel.  Up to 511 segments take one pass.  No atomic
-// decides an order, so results are the same every time.
+// Least-significant-digit radix passes of at most 9 bits, by workgroups of 16
+// waves.  A block of up to 8192 items stays in registers, eight to a lane, each
+// wave holding consecutive items.  A wave takes its items 64 at a time and
+// ranks equal digits by the lanes below (one ballot a bit) and the wave's own
+// counters in LDS; the counters of the 16 waves, summed digit by digit, then
+// say where each wave's items of a digit start.  No atomic decides an order, so
+// results are the same every time.
+//   block_sort_kernel  up to 8192 items: all passes in one launch, items
+//                      exchanged through LDS between them
+//   count_kernel       more: the digit histogram of each chunk of blocks,
+//   scatter_kernel     and the pass itself, every workgroup adding up the
+//                      histograms of the chunks before its own
+// Up to 511 segments take one pass, up to 262143 two.
 //
 // Bound by launches and by the latency of the dependent steps, not by its
 // bytes (16 to 20 an item).
@@ -20,11 +23,12 @@
 namespace segtopk_ops {
 namespace {
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxBits = 9;  // the waves' counters then take 37 KB of LDS
-constexpr int kMaxBins = 1 << kMaxBits;
-constexpr int64_t kOneChunk = 4096;   // items that one workgroup sorts alone
+constexpr uint32_t kSortThreads = 1024;
+constexpr uint32_t kSortWaves = kSortThreads / 64;
+constexpr int kItems = 8;  // of a lane
+constexpr uint32_t kBlock = kSortThreads * kItems;
+constexpr int kMaxBits = 9;
+constexpr uint32_t kMaxBins = 1u << kMaxBits;
 constexpr int64_t kMinChunk = 2048;
 constexpr int64_t kMaxChunks = 128;
 
@@ -37,7 +41,7 @@ struct SortArgs {
     int32_t *position;     // last pass, or nullptr
     int64_t *offsets;      // of a sort in one pass, or nullptr
     uint32_t *hist;        // [chunks][bins]
-    uint32_t n, segments, chunk, chunks, shift, bins, bits;
+    uint32_t n, segments, chunk, chunks, shift, bins, bits, passes;
     uint32_t wide;         // ids of 64 bits
 };
 
@@ -46,6 +50,125 @@ template <bool FIRST> __device__ inline uint32_t sort_key(const SortArgs &a, uin
     const int64_t id = a.wide ? static_cast<const int64_t *>(a.ids)[i]
                               : (int64_t) static_cast<const int32_t *>(a.ids)[i];
     return (id >= 0 && id < (int64_t)a.segments) ? (uint32_t)id : a.segments;
+}
+
+// The items of one block in registers: lane l of wave w holds items
+// w * 64 * items + r * 64 + l, r below `items`.
+struct Items {
+    uint32_t key[kItems], rank[kItems];
+    uint32_t first, items, count;  // of the block; item r is live below count
+    __device__ uint32_t at(int r) const { return first + (uint32_t)r * 64u; }
+    __device__ bool live(int r) const { return (uint32_t)r < items && at(r) < count; }
+};
+
+// Counts the wave's items by digit in `mine` (zero before), and ranks each among
+// those before it in the wave.
+__device__ inline void rank_items(Items &x, uint32_t shift, uint32_t bits, uint32_t *mine) {
+    const uint32_t lane = threadIdx.x & 63u, mask = (1u << bits) - 1u;
+    volatile uint32_t *const next = mine;
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) {
+        if ((uint32_t)r >= x.items) break;
+        const bool live = x.live(r);
+        const uint32_t digit = (x.key[r] >> shift) & mask;
+        uint64_t peers = __ballot(live);
+        for (uint32_t j = 0; j < bits; ++j) {
+            const uint64_t ones = __ballot((digit >> j) & 1u);
+            peers &= ((digit >> j) & 1u) ? ones : ~ones;
+        }
+        const uint32_t below = (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
+        uint32_t before = 0;
+        if (live) before = next[digit];
+        __builtin_amdgcn_wave_barrier();
+        if (live && below == 0) next[digit] = before + (uint32_t)__popcll(peers);
+        __builtin_amdgcn_wave_barrier();
+        x.rank[r] = before + below;
+    }
+}
+
+// Exclusive prefix over the digits, thread d holding digit d's count.
+__device__ inline uint32_t digit_prefix(uint32_t own, uint32_t *wave_total) {
+    const uint32_t lane = threadIdx.x & 63u, w = threadIdx.x >> 6;
+    uint32_t run = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t v = __shfl_up(run, d);
+        if (lane >= (uint32_t)d) run += v;
+    }
+    if (lane == 63u) wave_total[w] = run;
+    __syncthreads();
+    uint32_t base = run - own;
+    for (uint32_t i = 0; i < w; ++i) base += wave_total[i];
+    return base;
+}
+
+// Turns the waves' counts of digit d into the places where their items start,
+// from `base` on; returns where the next block's start.
+__device__ inline uint32_t wave_starts(uint32_t *whist, uint32_t bins, uint32_t d, uint32_t base) {
+#pragma unroll
+    for (uint32_t w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = whist[w * bins + d];
+        whist[w * bins + d] = base;
+        base += c;
+    }
+    return base;
+}
+
+// KEEP: room for the exchange between passes.
+template <bool KEEP>
+__global__ __launch_bounds__(kSortThreads) void block_sort_kernel(SortArgs a) {
+    __shared__ uint32_t whist[kSortWaves * kMaxBins], wave_total[kSortWaves];
+    __shared__ uint32_t keys[KEEP ? kBlock : 1], slots[KEEP ? kBlock : 1];
+    const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
+    Items x;
+    x.items = (a.n + kSortThreads - 1) / kSortThreads;
+    x.first = w * 64u * x.items + lane;
+    x.count = a.n;
+    uint32_t slot[kItems];
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) {
+        slot[r] = x.at(r);
+        x.key[r] = x.live(r) ? sort_key<true>(a, slot[r]) : 0u;
+    }
+    for (uint32_t pass = 0, shift = 0; pass < a.passes; ++pass, shift += a.bits) {
+        for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
+        __syncthreads();
+        rank_items(x, shift, a.bits, whist + w * a.bins);
+        __syncthreads();
+        uint32_t own = 0;
+        if (t < a.bins)
+#pragma unroll
+            for (uint32_t i = 0; i < kSortWaves; ++i) own += whist[i * a.bins + t];
+        const uint32_t base = digit_prefix(own, wave_total);
+        if (t < a.bins) {
+            if (a.offsets) a.offsets[t] = base;  // one pass: bins = segments + 1
+            wave_starts(whist, a.bins, t, base);
+        }
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+#pragma unroll
+        for (int r = 0; r < kItems; ++r) {
+            if (!x.live(r)) continue;
+            const uint32_t digit = (x.key[r] >> shift) & ((1u << a.bits) - 1u);
+            const uint32_t at = whist[w * a.bins + digit] + x.rank[r];
+            if (!last) {
+                keys[KEEP ? at : 0] = x.key[r];
+                slots[KEEP ? at : 0] = slot[r];
+            } else {
+                if (a.key_out) a.key_out[at] = x.key[r];
+                if (a.slot_out) a.slot_out[at] = slot[r];
+                if (a.position) a.position[slot[r]] = (int32_t)at;
+            }
+        }
+        if (!KEEP || last) break;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kItems; ++r)
+            if (x.live(r)) {
+                x.key[r] = keys[x.at(r)];
+                slot[r] = slots[x.at(r)];
+            }
+    }
 }
 
 template <bool FIRST>
@@ -64,25 +187,22 @@ __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a) {
 
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
-    extern __shared__ uint32_t lds[];
-    uint32_t *const whist = lds;                       // [waves][bins]
-    uint32_t *const wave_total = lds + kSortWaves * a.bins;  // [waves]
-    uint32_t *const total = wave_total + kSortWaves;   // [bins]
-    uint32_t *const before = total + a.bins;           // [bins]
+    __shared__ uint32_t whist[kSortWaves * kMaxBins], wave_total[kSortWaves];
+    __shared__ uint32_t total[kMaxBins], before[kMaxBins];
     const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
-    const uint32_t mask = (1u << a.bits) - 1u;
-    const uint32_t b = blockIdx.x * a.chunk;
-    const uint32_t e = min(a.n, b + a.chunk);
-    const uint32_t part = a.chunk / kSortWaves;  // a multiple of 64
-    const uint32_t wb = min(e, b + w * part), we = min(e, wb + part);
-
-    for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
+    const uint32_t b = blockIdx.x * a.chunk, e = min(a.n, b + a.chunk);
+    const uint32_t block = min(a.chunk, kBlock);
+    Items x;
+    x.items = block / kSortThreads;
+    const uint32_t in_block = w * 64u * x.items + lane;
+    x.first = b + in_block;
+    x.count = e;
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) x.key[r] = x.live(r) ? sort_key<FIRST>(a, x.at(r)) : 0u;
     if (t < a.bins) total[t] = before[t] = 0u;
+    for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
     __syncthreads();
-    for (uint32_t i = wb + lane; i < we; i += 64u)
-        atomicAdd(&whist[w * a.bins + ((sort_key<FIRST>(a, i) >> a.shift) & mask)], 1u);
-    // Rows of the histograms of all chunks, shared out among groups of threads.
-    if (a.chunks > 1) {
+    {   // Rows of the histograms of all chunks, shared out among groups of threads.
         uint32_t width = 64;
         while (width < a.bins) width <<= 1;
         const uint32_t d = t & (width - 1u), groups = kSortThreads / width;
@@ -98,59 +218,36 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
             atomicAdd(&before[d], mine);
         }
     }
+    rank_items(x, a.shift, a.bits, whist + w * a.bins);
     __syncthreads();
-    // Exclusive prefix of the totals over the digits, one thread a digit.
-    uint32_t own = 0;
+    uint32_t base = digit_prefix(t < a.bins ? total[t] : 0u, wave_total);
     if (t < a.bins) {
-        if (a.chunks > 1) own = total[t];
-        else
-            for (int i = 0; i < kSortWaves; ++i) own += whist[i * a.bins + t];
-    }
-    uint32_t run = own;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t v = __shfl_up(run, d);
-        if (lane >= (uint32_t)d) run += v;
-    }
-    if (lane == 63u) wave_total[w] = run;
-    __syncthreads();
-    if (t < a.bins) {
-        uint32_t base = run - own;
-        for (uint32_t i = 0; i < w; ++i) base += wave_total[i];
-        if (a.offsets && blockIdx.x == 0) a.offsets[t] = base;  // bins = segments + 1 then
+        if (a.offsets && blockIdx.x == 0) a.offsets[t] = base;  // one pass: bins = segments + 1
         base += before[t];
-        for (int i = 0; i < kSortWaves; ++i) {
-            const uint32_t c = whist[i * a.bins + t];
-            whist[i * a.bins + t] = base;
-            base += c;
-        }
     }
-    __syncthreads();
-    // A wave's items in order, 64 at a time; its counters are its own.
-    volatile uint32_t *const next = whist + w * a.bins;
-    for (uint32_t i0 = wb; i0 < we; i0 += 64u) {
-        const uint32_t i = i0 + lane;
-        const bool live = i < we;
-        const uint32_t key = live ? sort_key<FIRST>(a, i) : 0u;
-        const uint32_t digit = (key >> a.shift) & mask;
-        uint64_t peers = __ballot(live);
-        for (uint32_t j = 0; j < a.bits; ++j) {
-            const uint64_t ones = __ballot((digit >> j) & 1u);
-            peers &= ((digit >> j) & 1u) ? ones : ~ones;
-        }
-        const uint32_t rank = __popcll(peers & ((1ull << lane) - 1ull));
-        uint32_t at = 0;
-        if (live) at = next[digit];
-        __builtin_amdgcn_wave_barrier();
-        if (live && rank == 0) next[digit] = at + (uint32_t)__popcll(peers);
-        __builtin_amdgcn_wave_barrier();
-        if (live) {
-            const uint32_t slot = FIRST ? i : a.slot_in[i];
-            at += rank;
-            if (a.key_out) a.key_out[at] = key;
+    for (uint32_t b0 = b;;) {
+        if (t < a.bins) base = wave_starts(whist, a.bins, t, base);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kItems; ++r) {
+            if (!x.live(r)) continue;
+            const uint32_t digit = (x.key[r] >> a.shift) & ((1u << a.bits) - 1u);
+            const uint32_t at = whist[w * a.bins + digit] + x.rank[r];
+            const uint32_t slot = FIRST ? x.at(r) : a.slot_in[x.at(r)];
+            if (a.key_out) a.key_out[at] = x.key[r];
             if (a.slot_out) a.slot_out[at] = slot;
             if (a.position) a.position[slot] = (int32_t)at;
         }
+        if (e - b0 <= block) break;  // the next block of the chunk
+        b0 += block;
+        __syncthreads();
+        for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
+        x.first = b0 + in_block;
+#pragma unroll
+        for (int r = 0; r < kItems; ++r) x.key[r] = x.live(r) ? sort_key<FIRST>(a, x.at(r)) : 0u;
+        __syncthreads();
+        rank_items(x, a.shift, a.bits, whist + w * a.bins);
+        __syncthreads();
     }
 }
 
@@ -176,7 +273,7 @@ struct SortPlan {
 
 SortPlan sort_plan(int64_t n, int64_t segments) {
     SortPlan p{};
-    if (segments + 1 <= kMaxBins) {
+    if (segments + 1 <= (int64_t)kMaxBins) {
         p.passes = 1;
         p.bins = (uint32_t)(segments + 1);
         p.bits = 1;
@@ -188,20 +285,23 @@ SortPlan sort_plan(int64_t n, int64_t segments) {
         p.bits = (bits + p.passes - 1) / p.passes;
         p.bins = 1u << p.bits;
     }
-    int64_t chunk = n;
-    if (n > kOneChunk) {
+    // One block, or chunks of whole blocks (of part of one, where there are few
+    // items): few enough for a workgroup to add up all their histograms.
+    int64_t chunk = kBlock;
+    if (n > kBlock) {
         chunk = (n + kMaxChunks - 1) / kMaxChunks;
         if (chunk < kMinChunk) chunk = kMinChunk;
+        const int64_t unit = chunk > kBlock ? kBlock : kSortThreads;
+        chunk = (chunk + unit - 1) / unit * unit;
     }
-    chunk = (chunk + kSortThreads - 1) / kSortThreads * kSortThreads;
-    if (chunk < kSortThreads) chunk = kSortThreads;
     p.chunk = (uint32_t)chunk;
     p.chunks = n ? (uint32_t)((n + chunk - 1) / chunk) : 1u;
     p.hist_bytes = p.chunks > 1 ? ((size_t)p.chunks * p.bins * 4 + 255) & ~(size_t)255 : 0;
-    // Keys and slots between the passes, in two buffers taken in turn from
-    // three passes on, and the keys in order where offsets are searched in them.
+    // Of a sort in several passes, the keys in order, where offsets are searched;
+    // and of one in several chunks, keys and slots between the passes, in two
+    // buffers taken in turn.
     p.pair_bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
-    p.bytes = p.hist_bytes + (p.passes > 1 ? 5 : 0) * p.pair_bytes;
+    p.bytes = p.hist_bytes + (p.passes > 1 ? (p.chunks > 1 ? 5 : 1) : 0) * p.pair_bytes;
     return p;
 }
 
@@ -214,11 +314,12 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
                       hipStream_t stream) {
     const SortPlan p = sort_plan(n, segments);
     char *ws = static_cast<char *>(workspace);
-    uint32_t *pair[2][2];
-    for (int i = 0; i < 4; ++i)
-        pair[i >> 1][i & 1] = reinterpret_cast<uint32_t *>(ws + p.hist_bytes + i * p.pair_bytes);
-    if (p.passes > 1 && !sorted)
-        sorted = reinterpret_cast<uint32_t *>(ws + p.hist_bytes + 4 * p.pair_bytes);
+    uint32_t *pair[2][2] = {};
+    if (p.passes > 1 && !sorted) sorted = reinterpret_cast<uint32_t *>(ws + p.hist_bytes);
+    if (p.passes > 1 && p.chunks > 1)
+        for (int i = 0; i < 4; ++i)
+            pair[i >> 1][i & 1] =
+                reinterpret_cast<uint32_t *>(ws + p.hist_bytes + (i + 1) * p.pair_bytes);
     SortArgs a{};
     a.ids = ids;
     a.hist = reinterpret_cast<uint32_t *>(ws);
@@ -229,9 +330,18 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
     a.bins = p.bins;
     a.bits = (uint32_t)p.bits;
     a.wide = id_type == SEGTOPK_KEY_I64;
-    const size_t lds = 4 * ((size_t)(kSortWaves + 2) * p.bins + kSortWaves);
+    a.passes = (uint32_t)p.passes;
+    a.offsets = p.passes == 1 ? offsets : nullptr;
     hipError_t err;
-    for (int i = 0; i < p.passes; ++i) {
+    if (p.chunks == 1) {
+        a.key_out = sorted;
+        a.slot_out = reinterpret_cast<uint32_t *>(order);
+        a.position = position;
+        hipLaunchKernelGGL(p.passes > 1 ? block_sort_kernel<true> : block_sort_kernel<false>,
+                           dim3(1), dim3(kSortThreads), 0, stream, a);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    for (int i = 0; p.chunks > 1 && i < p.passes; ++i) {
         const bool last = i == p.passes - 1;
         a.shift = (uint32_t)(i * p.bits);
         a.key_in = i ? pair[(i - 1) & 1][0] : nullptr;
@@ -239,14 +349,11 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
         a.key_out = last ? sorted : pair[i & 1][0];
         a.slot_out = last ? reinterpret_cast<uint32_t *>(order) : pair[i & 1][1];
         a.position = last ? position : nullptr;
-        a.offsets = p.passes == 1 ? offsets : nullptr;
-        if (p.chunks > 1) {
-            hipLaunchKernelGGL(i ? count_kernel<false> : count_kernel<true>, dim3(p.chunks),
-                               dim3(kSortThreads), 0, stream, a);
-            if ((err = hipGetLastError()) != hipSuccess) return err;
-        }
+        hipLaunchKernelGGL(i ? count_kernel<false> : count_kernel<true>, dim3(p.chunks),
+                           dim3(kSortThreads), 0, stream, a);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
         hipLaunchKernelGGL(i ? scatter_kernel<false> : scatter_kernel<true>, dim3(p.chunks),
-                           dim3(kSortThreads), lds, stream, a);
+                           dim3(kSortThreads), 0, stream, a);
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
     if (p.passes > 1 && offsets) {

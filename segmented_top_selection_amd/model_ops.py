@@ -64,18 +64,44 @@ _SIGNATURES = {
 }
 
 
-@functools.lru_cache(maxsize=None)
+_entries = {}
+
+
 def entry(name: str):
     """The library's function of that name, with its argument types set."""
-    fn = getattr(library(), name)
-    fn.restype, fn.argtypes = _SIGNATURES[name]
+    fn = _entries.get(name)
+    if fn is None:
+        fn = getattr(library(), name)
+        fn.restype, fn.argtypes = _SIGNATURES[name]
+        _entries[name] = fn
     return fn
 
 
 def _call(name, *args):
-    rc = entry(name)(*args)
-    if rc != 0:
+    rc = (_entries.get(name) or entry(name))(*args)
+    if rc:
         raise SegTopKError(rc, name)
+
+
+# Sizes are pure functions of the arguments, and programs repeat few of them.
+@functools.lru_cache(maxsize=256)
+def _sort_workspace(n, num_segments):
+    return entry("segtopk_sort_ids_workspace")(n, num_segments)
+
+
+@functools.lru_cache(maxsize=256)
+def _grad_workspace(n, num_rows, width):
+    return entry("segtopk_embedding_backward_workspace")(n, num_rows, width)
+
+
+@functools.lru_cache(maxsize=256)
+def _loss_workspace(tokens, vocab, num_segments):
+    return entry("segtopk_policy_loss_workspace")(tokens, vocab, num_segments)
+
+
+# The current device without torch.cuda's checks; a device tensor is at hand
+# where it is asked for.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on_its_stream(fn):
@@ -83,7 +109,7 @@ def _on_its_stream(fn):
     @functools.wraps(fn)
     def wrapped(first, *args, stream=None, **kw):
         if isinstance(first, torch.Tensor) and first.is_cuda and (
-                stream is not None or first.device.index != torch.cuda.current_device()):
+                stream is not None or first.device.index != _current_device()):
             if stream is not None and stream.device != first.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors are on {first.device}")
             with torch.cuda.device(first.device), torch.cuda.stream(stream):
@@ -108,6 +134,9 @@ def _device_of(name, t):
 
 def _matrix(name, t, dev, shape=None, dtype=None):
     """t as rows with a unit inner stride that do not overlap."""
+    if isinstance(t, torch.Tensor) and t.device == dev and t.dtype in _FLOAT and t.dim() == 2 \
+            and t.is_contiguous() and t.shape[1] and shape is None and dtype is None:
+        return t
     _device_tensor(name, t, dev)
     if t.dtype not in _FLOAT:
         raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
@@ -142,7 +171,8 @@ def _result(name, t, dev, shape, dtype):
 
 def _rows(t):
     # The stride of a single row is never used, and torch may say anything.
-    return _Rows(t.data_ptr(), max(t.stride(0), t.shape[1]), _FLOAT[t.dtype])
+    stride, width = t.stride(0), t.shape[1]
+    return _Rows(t.data_ptr(), stride if stride > width else width, _FLOAT[t.dtype])
 
 
 def _ids(name, t, dev):
@@ -174,7 +204,7 @@ def _offsets(name, t, dev):
     _device_tensor(name, t, dev)
     if t.dtype != torch.int64:
         raise TypeError(f"{name} must be int64 (got {t.dtype})")
-    if t.dim() != 1 or t.shape[0] < 1:
+    if len(t.shape) != 1 or t.shape[0] < 1:
         raise ValueError(f"{name} must be 1-D with num_segments + 1 entries")
     return t if t.is_contiguous() else t.contiguous()
 
@@ -184,9 +214,10 @@ def _slots(position, offsets, dev):
     _device_tensor("position", position, dev)
     if position.dtype != torch.int32:
         raise TypeError(f"position must be int32 (got {position.dtype})")
-    if position.dim() not in (1, 2):
+    shape = position.shape
+    if len(shape) not in (1, 2):
         raise ValueError("position must have shape (tokens, k) or (tokens,)")
-    tokens, k = position.shape[0], position.shape[1] if position.dim() == 2 else 1
+    tokens, k = shape if len(shape) == 2 else (shape[0], 1)
     if k < 1:
         raise ValueError("position needs at least one slot a token")
     if not position.is_contiguous():
@@ -230,7 +261,7 @@ def sort_ids(ids: torch.Tensor, num_segments: int):
     order = torch.empty(n, dtype=torch.int32, device=dev)
     position = torch.empty(ids.shape, dtype=torch.int32, device=dev)
     offsets = torch.empty(num_segments + 1, dtype=torch.int64, device=dev)
-    need = entry("segtopk_sort_ids_workspace")(n, num_segments)
+    need = _sort_workspace(n, num_segments)
     ws = _workspace(need, dev)
     _call("segtopk_sort_ids", ids.data_ptr(), _INDEX[ids.dtype], n, num_segments,
           order.data_ptr(), position.data_ptr(), offsets.data_ptr(), _ptr(ws), need, _stream(dev))
@@ -370,7 +401,7 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, num_rows: int, *,
     if dtype not in (dout.dtype, torch.float32):
         raise TypeError(f"the gradient must be float32 or {dout.dtype} (got {dtype})")
     out = _result("out", out, dev, (num_rows, width), dtype)
-    need = entry("segtopk_embedding_backward_workspace")(n, num_rows, width)
+    need = _grad_workspace(n, num_rows, width)
     ws = _workspace(need, dev)
     _call("segtopk_embedding_backward", _rows(dout), _rows(out), ids.data_ptr(),
           _INDEX[ids.dtype], n, num_rows, width, float(scale),
@@ -415,7 +446,7 @@ def _policy(logits, token_ids, old_logp, advantages, segment_offsets, ref_logp, 
     a.old_logp, a.ref_logp = old_logp.data_ptr(), _ptr(ref_logp)
     a.advantages = advantages.data_ptr()
     a.loss, a.logp = loss.data_ptr(), logp.data_ptr()
-    need = entry("segtopk_policy_loss_workspace")(tokens, vocab, a.num_segments)
+    need = _loss_workspace(tokens, vocab, offsets.shape[0] - 1)
     ws = _workspace(need, dev)
     _call("segtopk_policy_loss", ctypes.byref(a), _ptr(ws), need, _stream(dev))
     return loss, logp, dlogits

@@ -28,7 +28,7 @@ def sort_ids(ids=A, id_type=I32, n=100, segments=8, order=B, position=C, offsets
     dict(ids=None), dict(ids=A + 2), dict(id_type=F32), dict(id_type=-1), dict(id_type=I64, ids=A + 4),
     dict(n=-1), dict(n=2 ** 31), dict(segments=-1), dict(segments=2 ** 31 - 1), dict(order=None),
     dict(order=B + 1), dict(position=None), dict(position=C + 2), dict(offsets=None),
-    dict(offsets=D + 4), dict(n=5000, ws=None), dict(n=5000, ws=WS + 8),
+    dict(offsets=D + 4), dict(n=9000, ws=None), dict(n=9000, ws=WS + 8),
 ])
 def test_sort_ids_refusals(kw):
     assert sort_ids(**kw) == INVALID
@@ -36,7 +36,7 @@ def test_sort_ids_refusals(kw):
 
 def test_sort_ids_workspace():
     need = mo.entry("segtopk_sort_ids_workspace")
-    assert need(100, 8) == 0  # one workgroup, one pass
+    assert need(100, 8) == need(8192, 511) == 0  # one workgroup, one pass
     assert need(-1, 8) == need(100, -1) == need(2 ** 31, 8) == 0
     assert need(100000, 8) > 0 and need(100, 100000) > 0
     assert need(100000, 200000) >= 4 * 4 * 100000

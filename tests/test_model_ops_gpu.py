@@ -72,7 +72,7 @@ def check_sort(ids, segments, **kw):
 
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64], ids=IDS.get)
 @pytest.mark.parametrize("segments", [1, 2, 37, 64, 128, 511, 512, 4099, 131072, 300001])
-@pytest.mark.parametrize("n", [0, 1, 63, 64, 65, 1000, 4096, 4097, 33333])
+@pytest.mark.parametrize("n", [0, 1, 63, 64, 65, 1000, 1025, 8191, 8192, 8193, 33333])
 def test_sort_ids(n, segments, dtype):
     g = gen(n * 7 + segments)
     ids = torch.randint(-2, segments + 2, (n,), generator=g, device=DEV).to(dtype)
@@ -80,7 +80,7 @@ def test_sort_ids(n, segments, dtype):
 
 
 @pytest.mark.parametrize("what", ["same", "last", "dropped", "descending", "skewed"])
-@pytest.mark.parametrize("n,segments", [(3000, 128), (300000, 128), (70001, 100000)])
+@pytest.mark.parametrize("n,segments", [(3000, 128), (8000, 5000), (300000, 128), (70001, 100000)])
 def test_sort_ids_orders(what, n, segments):
     i = torch.arange(n, device=DEV)
     ids = {"same": i * 0 + 3, "last": i * 0 + segments - 1, "dropped": i * 0 - 1,
@@ -91,7 +91,8 @@ def test_sort_ids_orders(what, n, segments):
 
 def test_sort_ids_large_and_far_ids():
     g = gen(3)
-    check_sort(torch.randint(0, 256, (1 << 20, 3), generator=g, device=DEV), 256)
+    check_sort(torch.randint(0, 256, (1 << 20, 3), generator=g, device=DEV), 256)  # blocks in turn
+    check_sort(torch.randint(0, 70000, (3 * (1 << 20) + 77,), generator=g, device=DEV), 70000)
     # 64-bit ids whose low 32 bits look like segments are outside.
     ids = torch.tensor([2 ** 32 + 1, 1, -2 ** 32 + 1, 2 ** 62, 0, 1, -2 ** 63], device=DEV)
     check_sort(ids, 4)
