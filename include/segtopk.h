@@ -389,7 +389,7 @@ typedef struct segtopk_policy_loss_args {
     segtopk_rows logits, dlogits;
     const void *token_ids;
     int32_t id_type;
-    float clip_low, clip_high, kl_coef, temperature, grad_scale;
+    double clip_low, clip_high, kl_coef, temperature, grad_scale;
     int64_t tokens, vocab, num_segments;
     const int64_t *segment_offsets;
     const float *old_logp, *ref_logp, *advantages;

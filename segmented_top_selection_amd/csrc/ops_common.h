@@ -24,11 +24,17 @@ template <class T> struct Piece {
     typedef float f32 __attribute__((ext_vector_type(16 / sizeof(T))));
 };
 
-template <class T> __device__ inline typename Piece<T>::vec load_piece(const T *p) {
-    return *reinterpret_cast<const typename Piece<T>::mem *>(p);
+// STREAM: past the caches, for what is not touched again soon.
+template <bool STREAM = false, class T>
+__device__ inline typename Piece<T>::vec load_piece(const T *p) {
+    const auto *q = reinterpret_cast<const typename Piece<T>::mem *>(p);
+    return STREAM ? __builtin_nontemporal_load(q) : *q;
 }
-template <class T> __device__ inline void store_piece(T *p, typename Piece<T>::vec v) {
-    *reinterpret_cast<typename Piece<T>::mem *>(p) = v;
+template <bool STREAM = false, class T>
+__device__ inline void store_piece(T *p, typename Piece<T>::vec v) {
+    auto *q = reinterpret_cast<typename Piece<T>::mem *>(p);
+    if (STREAM) __builtin_nontemporal_store((typename Piece<T>::mem)v, q);
+    else *q = v;
 }
 template <class T>
 __device__ inline typename Piece<T>::f32 widen(typename Piece<T>::vec v) {
@@ -62,6 +68,9 @@ inline bool good_rows(const segtopk_rows *m, int64_t width) {
     const int b = m ? element_bytes(m->type) : 0;
     return b && m->data && aligned(m->data, b) && m->stride >= width;
 }
+// Whether an output of so many bytes is stored past the caches: with the inputs it
+// no longer fits the 256 MB that the last of them holds.
+inline bool streams(int64_t bytes) { return bytes >= ((int64_t)128 << 20); }
 inline int status(hipError_t e) { return e == hipSuccess ? SEGTOPK_OK : SEGTOPK_HIP_ERROR; }
 
 // Calls f with a value of the element type.

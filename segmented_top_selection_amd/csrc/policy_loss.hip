@@ -2,7 +2,7 @@
 // sampled tokens, and its gradient.
 //
 // For a row t with sampled token y, z = logits / temperature:
-//   lse  = m + log sum exp(z - m),  m = max z;   lp = z[y] - lse
+//   lp   = z[y] - m - log sum exp(z - m),   m = max z
 //   r    = exp(lp - old),  A the advantage
 //   term = -min(r A, clamp(r, 1 - low, 1 + high) A)
 //          + kl (exp(ref - lp) - (ref - lp) - 1)
@@ -13,10 +13,20 @@
 // A row without a token in [0, vocab), or in no answer, counts for nothing: its
 // gradient is zero.
 //
-//   weight_kernel  one workgroup an answer: its live rows, and their weights
-//   row_kernel     one workgroup a row: maximum and sum in one pass (32 bits),
-//                  then, where asked for, the gradient in a second
-//   total_kernel   the sum of the rows' terms in 64 bits, in one fixed order
+//   count_kernel  one workgroup an answer: the number of its live rows
+//   row_kernel    one workgroup a row: maximum and sum in one pass, then, where
+//                 asked for, the gradient in a second that walks the row back
+//                 from its end, the last pieces of it still in registers.  The
+//                 last row to arrive adds up the terms, in one fixed order.
+//
+// The terms of a loss cancel, so each has to be better than the plain 32 bits
+// that its size suggests: exponents are taken from the row's maximum, with the
+// factor log2(e) / temperature in two parts, and everything after the sum, once a
+// row, is in 64 bits.
+#include <cfloat>
+#include <cmath>
+#include <type_traits>
+
 #include "ops_common.h"
 
 namespace segtopk_ops {
@@ -26,11 +36,13 @@ struct LossArgs {
     int64_t stride, dstride;
     const void *token_ids;
     const float *old_logp, *ref_logp, *advantages;
-    float *logp;
-    const float *weight;  // [tokens], 0 for a row that counts for nothing
-    double *term;         // [tokens]
+    float *logp, *loss;
+    const uint32_t *live;  // [tokens], 0 for a row that counts for nothing
+    double *term;          // [tokens]
+    uint32_t *arrived;
     uint32_t tokens, vocab, wide;
-    float clip_low, clip_high, kl_coef, inv_temperature, grad_scale;
+    double answers, clip_low, clip_high, kl_coef, temperature, grad_scale;
+    float factor, rest;  // log2(e) / temperature
 };
 
 __device__ inline int64_t token_of(const void *ids, uint32_t wide, uint32_t t) {
@@ -38,155 +50,250 @@ __device__ inline int64_t token_of(const void *ids, uint32_t wide, uint32_t t) {
                 : (int64_t) static_cast<const int32_t *>(ids)[t];
 }
 
-__global__ __launch_bounds__(kOpThreads) void weight_kernel(const void *ids, uint32_t wide,
-                                                            uint32_t tokens, uint32_t vocab,
-                                                            const int64_t *offsets,
-                                                            uint32_t segments, float *weight) {
-    __shared__ uint32_t live;
+constexpr uint32_t kCountThreads = 1024;
+
+// Rows arrive at one of 64 counters, and the last row of each at the counter
+// before them: additions to one word follow each other 14 ns apart, which took
+// 59 us of 4096 rows whatever their length.  Each has a cache line to itself.
+constexpr uint32_t kCounters = 64, kCounterWords = 32;
+__device__ inline uint32_t arrive(uint32_t *counter) {
+    return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ __launch_bounds__(kCountThreads) void count_kernel(const void *ids, uint32_t wide,
+                                                           uint32_t tokens, uint32_t vocab,
+                                                           const int64_t *offsets,
+                                                           uint32_t segments, uint32_t *live,
+                                                           uint32_t *arrived) {
+    __shared__ uint32_t total;
     const auto at = [&](uint32_t s) {  // offsets outside the rows are cut
         const int64_t v = offsets[s];
         return (uint32_t)(v < 0 ? 0 : v > (int64_t)tokens ? (int64_t)tokens : v);
     };
     const uint32_t s = blockIdx.x;
-    const uint32_t b = at(s), e = at(s + 1);
-    if (threadIdx.x == 0) live = 0u;
+    const uint32_t b = segments ? at(s) : tokens, e = segments ? at(s + 1) : tokens;
+    if (threadIdx.x == 0) total = 0u;
+    if (s == 0 && threadIdx.x <= kCounters) arrived[threadIdx.x * kCounterWords] = 0u;
     __syncthreads();
     uint32_t n = 0;
-    for (uint32_t t = b + threadIdx.x; t < e; t += kOpThreads) {
-        const int64_t y = token_of(ids, wide, t);
-        n += y >= 0 && y < (int64_t)vocab;
+    for (uint32_t t0 = b + threadIdx.x; t0 < e; t0 += 4u * kCountThreads) {
+        int64_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t t = t0 + j * kCountThreads;
+            y[j] = t < e ? token_of(ids, wide, t) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n += y[j] >= 0 && y[j] < (int64_t)vocab;
     }
-    if (n) atomicAdd(&live, n);
+    if (n) atomicAdd(&total, n);
     __syncthreads();
-    const float w = 1.0f / ((float)segments * (float)live);
-    for (uint32_t t = b + threadIdx.x; t < e; t += kOpThreads) {
+    n = total;
+    for (uint32_t t = b + threadIdx.x; t < e; t += kCountThreads) {
         const int64_t y = token_of(ids, wide, t);
-        weight[t] = y >= 0 && y < (int64_t)vocab ? w : 0.0f;
+        live[t] = y >= 0 && y < (int64_t)vocab ? n : 0u;
     }
     if (s == 0)
-        for (uint32_t t = threadIdx.x; t < b; t += kOpThreads) weight[t] = 0.0f;
-    if (s == segments - 1)
-        for (uint32_t t = e + threadIdx.x; t < tokens; t += kOpThreads) weight[t] = 0.0f;
+        for (uint32_t t = threadIdx.x; t < b; t += kCountThreads) live[t] = 0u;
+    if (segments && s == segments - 1)
+        for (uint32_t t = e + threadIdx.x; t < tokens; t += kCountThreads) live[t] = 0u;
 }
 
-constexpr int kRowThreads = 1024;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
+constexpr double kLog2e = 1.44269504088896340736;
+constexpr int kAtOnce = 4;  // pieces of a thread that are in flight together
 
-// Running maximum m (of the scaled logits, base 2) and sum of 2^(z - m).
+// Running maximum m and sum of 2^((x - m) factor).
 struct Stat {
     float m, s;
 };
 __device__ inline float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
-__device__ inline Stat join(Stat a, Stat b) {
-    const float m = fmaxf(a.m, b.m), o = shift_of(m);
-    return {m, a.s * exp2f(a.m - o) + b.s * exp2f(b.m - o)};
+
+// 2^(d log2(e) / temperature) for d <= 0.  `rest` is positive, so -inf gives 0.
+// The hardware's exponential takes what is below 2^-126 to zero, next to a sum of
+// at least one.
+__device__ inline float power(float d, const LossArgs &a) {
+    return __builtin_amdgcn_exp2f(fmaf(d, a.rest, d * a.factor));
 }
 
-template <class T, bool GRAD>
-__global__ __launch_bounds__(kRowThreads) void row_kernel(const T *logits, T *dlogits,
-                                                          LossArgs a) {
+// The statistics of 16 lanes or a whole wave as one.
+template <int LANES> __device__ inline Stat join_lanes(Stat x, const LossArgs &a) {
+    float m = x.m;
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    float s = x.s * power(x.m - shift_of(m), a);
+#pragma unroll
+    for (int d = LANES / 2; d; d >>= 1) s += __shfl_xor(s, d);
+    return {m, s};
+}
+
+struct RowTail {
+    float m, log2_sum, slope;
+};
+
+template <class T, bool GRAD, bool STREAM, int THREADS>
+__global__ __launch_bounds__(THREADS) void row_kernel(const T *logits, T *dlogits, LossArgs a) {
     using P = Piece<T>;
+    constexpr int kWaves = THREADS / 64;
+    constexpr uint32_t kGroup = THREADS * kAtOnce;  // pieces
+    __shared__ Stat part[16];
+    __shared__ RowTail tail;
+    __shared__ uint32_t arrival;
+    __shared__ double sums[kWaves];
     const uint32_t t = blockIdx.x, i = threadIdx.x;
-    const float weight = a.weight[t];
+    const uint32_t live = a.live[t], token = (uint32_t)token_of(a.token_ids, a.wide, t);
+    const float adv32 = a.advantages[t], old = a.old_logp[t];
+    const float ref = a.kl_coef != 0.0 ? a.ref_logp[t] : 0.0f;
     const T *row = logits + (int64_t)t * a.stride;
     T *grad = GRAD ? dlogits + (int64_t)t * a.dstride : nullptr;
-    const uint32_t pieces = a.vocab / P::N;
-    const float scale = a.inv_temperature * kLog2e;
-    float slope = 0.0f, lse = 0.0f;
-    uint32_t token = 0;
-    if (weight != 0.0f) {
-        token = (uint32_t)token_of(a.token_ids, a.wide, t);
-        const float zy = (float)row[token] * scale;  // read before the gradient may overwrite it
+    const uint32_t pieces = a.vocab / P::N, groups = (pieces + kGroup - 1) / kGroup;
+    const uint32_t single = pieces * P::N + i;  // the element past the pieces that is this thread's
+    const T none = (T)-INFINITY;
+    typename P::vec v[kAtOnce];
+    T x1 = none;
+    uint32_t mine = 0;
+    double lp = 0.0, term = 0.0;  // of thread 0
+    if (live) {
+        const float xy = (float)row[token];  // read before the gradient may overwrite it
+        if (single < a.vocab) x1 = row[single];
         Stat st{-INFINITY, 0.0f};
-        for (uint32_t u = i; u < pieces; u += kRowThreads) {
-            const typename P::f32 z = widen<T>(load_piece(row + (size_t)u * P::N)) * scale;
+        for (uint32_t g = 0; g < groups; ++g) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const uint32_t u = g * kGroup + j * THREADS + i;
+                v[j] = (typename P::vec)none;
+                if (u < pieces) v[j] = load_piece(row + (size_t)u * P::N);
+            }
             float m = st.m;
 #pragma unroll
-            for (int j = 0; j < P::N; ++j) m = fmaxf(m, z[j]);
-            const float o = shift_of(m);
-            st.s *= exp2f(st.m - o);
+            for (int j = 0; j < kAtOnce; ++j) {
+                const typename P::f32 x = widen<T>(v[j]);
 #pragma unroll
-            for (int j = 0; j < P::N; ++j) st.s += exp2f(z[j] - o);
+                for (int k = 0; k < P::N; ++k) m = fmaxf(m, x[k]);
+            }
+            const float o = shift_of(m);
+            st.s *= power(st.m - o, a);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const typename P::f32 x = widen<T>(v[j]);
+#pragma unroll
+                for (int k = 0; k < P::N; ++k) st.s += power(x[k] - o, a);
+            }
             st.m = m;
         }
-        for (uint32_t c = pieces * P::N + i; c < a.vocab; c += kRowThreads)
-            st = join(st, Stat{(float)row[c] * scale, 1.0f});
-#pragma unroll
-        for (int d = 32; d; d >>= 1)
-            st = join(st, Stat{__shfl_xor(st.m, d), __shfl_xor(st.s, d)});
-        __shared__ Stat part[kRowThreads / 64];
+        {
+            const float x = (float)x1, m = fmaxf(st.m, x), o = shift_of(m);
+            st.s = st.s * power(st.m - o, a) + power(x - o, a);
+            st.m = m;
+        }
+        st = join_lanes<64>(st, a);
         if ((i & 63u) == 0) part[i >> 6] = st;
         __syncthreads();
-        st = part[0];
-        for (int w = 1; w < kRowThreads / 64; ++w) st = join(st, part[w]);
-        if (st.m != -INFINITY) {
-            lse = st.m + log2f(st.s);
-            const float lp = (zy - lse) * kLn2;
-            const float adv = a.advantages[t], ratio = expf(lp - a.old_logp[t]);
-            const float clipped = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
-            const bool free = ratio * adv <= clipped * adv;
-            float term = -(free ? ratio : clipped) * adv;
-            slope = free ? -ratio * adv : 0.0f;
-            if (a.kl_coef != 0.0f) {
-                const float apart = a.ref_logp[t] - lp, e = expf(apart);
-                term += a.kl_coef * (e - apart - 1.0f);
-                slope += a.kl_coef * (1.0f - e);
-            }
-            slope *= weight * a.inv_temperature * a.grad_scale;
+        if (i < 64u) {
+            st = part[i % kWaves];
+            st = join_lanes<kWaves>(st, a);
             if (i == 0) {
-                a.logp[t] = lp;
-                a.term[t] = (double)term * (double)weight;
+                double d = 0.0;
+                // Nothing but -inf: no distribution, and no loss.
+                if (st.m != -INFINITY || st.s != 0.0f) {
+                    lp = ((double)xy - (double)st.m) / a.temperature - log((double)st.s);
+                    const double adv = adv32, ratio = exp(lp - (double)old);
+                    const double clipped = fmin(fmax(ratio, 1.0 - a.clip_low), 1.0 + a.clip_high);
+                    const bool free = ratio * adv <= clipped * adv;
+                    term = -(free ? ratio : clipped) * adv;
+                    d = free ? -ratio * adv : 0.0;
+                    if (a.kl_coef != 0.0) {
+                        const double apart = (double)ref - lp, e = exp(apart);
+                        term += a.kl_coef * (e - apart - 1.0);
+                        d += a.kl_coef * (1.0 - e);
+                    }
+                    const double weight = 1.0 / (a.answers * (double)live);
+                    term *= weight;
+                    d *= weight / a.temperature * a.grad_scale;
+                }
+                tail = {shift_of(st.m), log2f(st.s), (float)d};
             }
-        } else if (i == 0) {  // nothing but -inf: no distribution, and no loss
-            a.logp[t] = 0.0f;
-            a.term[t] = 0.0;
         }
-    } else if (i == 0) {
-        a.logp[t] = 0.0f;
-        a.term[t] = 0.0;
     }
-    if (!GRAD) return;
-    if (slope == 0.0f) {
-        for (uint32_t u = i; u < pieces; u += kRowThreads)
-            store_piece(grad + (size_t)u * P::N, (typename P::vec)(T)0.0f);
-        for (uint32_t c = pieces * P::N + i; c < a.vocab; c += kRowThreads) grad[c] = (T)0.0f;
-        return;
+    if (GRAD) __syncthreads();
+    if (i == 0) {
+        a.logp[t] = (float)lp;
+        __hip_atomic_store(&a.term[t], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // The term is stored past this XCD's cache, and has arrived where every
+        // XCD sees it before the row counts as arrived.  A release at device
+        // scope would do so by writing the whole cache back, the gradient with
+        // it, once a row: 638 us for 4096 x 131072 bf16 where this takes 368.
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        mine = arrive(a.arrived + (1u + t % kCounters) * kCounterWords);
     }
-    for (uint32_t u = i; u < pieces; u += kRowThreads) {
-        const typename P::f32 z = widen<T>(load_piece(row + (size_t)u * P::N)) * scale;
-        typename P::f32 g;
+    if (GRAD) {
+        const float slope = live ? tail.slope : 0.0f, m = tail.m, l = tail.log2_sum;
+        if (slope == 0.0f) {
+            for (uint32_t u = i; u < pieces; u += THREADS)
+                store_piece<STREAM>(grad + (size_t)u * P::N, (typename P::vec)(T)0.0f);
+            if (single < a.vocab) grad[single] = (T)0.0f;
+        } else {
+            const uint32_t hot = token / P::N, place = token % P::N;
+            for (uint32_t g = groups; g-- > 0;) {
+                if (g + 1 < groups) {
 #pragma unroll
-        for (int j = 0; j < P::N; ++j) {
-            const float p = exp2f(z[j] - lse);
-            g[j] = slope * ((u * P::N + j == token ? 1.0f : 0.0f) - p);
+                    for (int j = 0; j < kAtOnce; ++j) {
+                        const uint32_t u = g * kGroup + j * THREADS + i;  // below pieces
+                        v[j] = load_piece<STREAM>(row + (size_t)u * P::N);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const uint32_t u = g * kGroup + j * THREADS + i;
+                    if (u >= pieces) continue;
+                    const typename P::f32 x = widen<T>(v[j]);
+                    typename P::f32 d;
+#pragma unroll
+                    for (int k = 0; k < P::N; ++k)
+                        d[k] = -slope * __builtin_amdgcn_exp2f(fmaf(x[k] - m, a.factor, -l));
+                    if (u == hot)
+#pragma unroll
+                        for (int k = 0; k < P::N; ++k)
+                            if ((uint32_t)k == place) d[k] += slope;
+                    store_piece<STREAM>(grad + (size_t)u * P::N, narrow<T>(d));
+                }
+            }
+            if (single < a.vocab) {
+                const float p = __builtin_amdgcn_exp2f(fmaf((float)x1 - m, a.factor, -l));
+                grad[single] = (T)(slope * ((single == token ? 1.0f : 0.0f) - p));
+            }
         }
-        store_piece(grad + (size_t)u * P::N, narrow<T>(g));
     }
-    for (uint32_t c = pieces * P::N + i; c < a.vocab; c += kRowThreads)
-        grad[c] = (T)(slope * ((c == token ? 1.0f : 0.0f) - exp2f((float)row[c] * scale - lse)));
-}
-
-__global__ __launch_bounds__(1024) void total_kernel(const double *term, uint32_t n, float *loss) {
-    __shared__ double part[16];
-    double v = 0.0;
-    for (uint32_t t = threadIdx.x; t < n; t += 1024u) v += term[t];
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    if ((threadIdx.x & 63u) == 0) part[threadIdx.x >> 6] = v;
+    if (i == 0) {
+        const uint32_t of_its_counter = (a.tokens - 1u - t % kCounters) / kCounters + 1u;
+        arrival = mine + 1u == of_its_counter ? arrive(a.arrived) : kCounters;
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 16; ++w) v += part[w];
-        *loss = (float)v;
+    if (arrival + 1u != min(a.tokens, kCounters)) return;
+    // Every other row's term is there.
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    double sum = 0.0;
+    for (uint32_t r = i; r < a.tokens; r += THREADS)
+        sum += __hip_atomic_load(&a.term[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if ((i & 63u) == 0) sums[i >> 6] = sum;
+    __syncthreads();
+    if (i == 0) {
+        for (int w = 1; w < kWaves; ++w) sum += sums[w];
+        *a.loss = (float)sum;
     }
 }
 
-__global__ void no_answers_kernel(float *weight, uint32_t n) {
-    for (uint32_t t = blockIdx.x * blockDim.x + threadIdx.x; t < n; t += gridDim.x * blockDim.x)
-        weight[t] = 0.0f;
-}
+__global__ void no_rows_kernel(float *loss) { *loss = 0.0f; }
 
 size_t term_bytes(int64_t tokens) { return ((size_t)tokens * 8 + 255) & ~(size_t)255; }
+
+size_t live_bytes(int64_t tokens) { return ((size_t)tokens * 4 + 255) & ~(size_t)255; }
+
+// The terms, the live counts, and the counters of arrivals.
+size_t loss_workspace(int64_t tokens) {
+    return tokens ? term_bytes(tokens) + live_bytes(tokens) + (1 + kCounters) * kCounterWords * 4 : 0;
+}
 
 bool good_loss_sizes(int64_t tokens, int64_t vocab, int64_t segments) {
     // One workgroup of 1024 threads a row, fewer than 2^32 threads in all.
@@ -202,7 +309,7 @@ using namespace segtopk_ops;
 extern "C" int64_t segtopk_policy_loss_workspace(int64_t tokens, int64_t vocab,
                                                  int64_t num_segments) {
     if (!good_loss_sizes(tokens, vocab, num_segments)) return 0;
-    return (int64_t)(term_bytes(tokens) + (size_t)tokens * 4);
+    return (int64_t)loss_workspace(tokens);
 }
 
 extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *workspace,
@@ -213,9 +320,9 @@ extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *w
     const bool grad = q.dlogits.data != nullptr;
     const int ib = index_bytes(q.id_type);
     // The comparisons are false for NaN, which is refused with the rest.
-    if (!(q.clip_low >= 0.0f && q.clip_low <= 1.0f) || !(q.clip_high >= 0.0f) ||
-        !(q.kl_coef >= 0.0f) || !(q.temperature > 0.0f) || !(q.temperature < INFINITY) ||
-        !(q.grad_scale - q.grad_scale == 0.0f) || !(q.kl_coef < INFINITY) || !ib)
+    if (!(q.clip_low >= 0.0 && q.clip_low <= 1.0) || !(q.clip_high >= 0.0) ||
+        !(q.kl_coef >= 0.0) || !(q.temperature > 0.0) || !(q.temperature < INFINITY) ||
+        !(q.grad_scale - q.grad_scale == 0.0) || !(q.kl_coef < INFINITY) || !ib)
         return SEGTOPK_INVALID_ARGUMENT;
     if (!q.loss || !aligned(q.loss, 4)) return SEGTOPK_INVALID_ARGUMENT;
     if (q.num_segments && (!q.segment_offsets || !aligned(q.segment_offsets, 8)))
@@ -224,17 +331,19 @@ extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *w
         if (!good_rows(&q.logits, q.vocab) || !q.token_ids || !aligned(q.token_ids, ib) ||
             !q.old_logp || !aligned(q.old_logp, 4) || !q.advantages || !aligned(q.advantages, 4) ||
             !q.logp || !aligned(q.logp, 4) || !aligned(q.ref_logp, 4) ||
-            (q.kl_coef != 0.0f && !q.ref_logp))
+            (q.kl_coef != 0.0 && !q.ref_logp))
             return SEGTOPK_INVALID_ARGUMENT;
         if (grad && (!good_rows(&q.dlogits, q.vocab) || q.dlogits.type != q.logits.type))
             return SEGTOPK_INVALID_ARGUMENT;
     }
-    const size_t need = term_bytes(q.tokens) + (size_t)q.tokens * 4;
+    const size_t need = loss_workspace(q.tokens);
     if (need && (!workspace || !aligned(workspace, 256))) return SEGTOPK_INVALID_ARGUMENT;
     if (workspace_bytes < 0 || (size_t)workspace_bytes < need) return SEGTOPK_SCRATCH_TOO_SMALL;
 
-    double *term = static_cast<double *>(workspace);
-    float *weight = reinterpret_cast<float *>(static_cast<char *>(workspace) + term_bytes(q.tokens));
+    if (!q.tokens) {
+        hipLaunchKernelGGL(no_rows_kernel, dim3(1), dim3(1), 0, stream, q.loss);
+        return status(hipGetLastError());
+    }
     LossArgs a{};
     a.stride = q.logits.stride;
     a.dstride = q.dlogits.stride;
@@ -243,40 +352,56 @@ extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *w
     a.ref_logp = q.ref_logp;
     a.advantages = q.advantages;
     a.logp = q.logp;
-    a.weight = weight;
-    a.term = term;
+    a.loss = q.loss;
+    a.term = static_cast<double *>(workspace);
+    uint32_t *live = reinterpret_cast<uint32_t *>(a.term + term_bytes(q.tokens) / 8);
+    a.live = live;
+    a.arrived = live + live_bytes(q.tokens) / 4;
     a.tokens = (uint32_t)q.tokens;
     a.vocab = (uint32_t)q.vocab;
     a.wide = q.id_type == SEGTOPK_KEY_I64;
+    a.answers = (double)q.num_segments;
     a.clip_low = q.clip_low;
     a.clip_high = q.clip_high;
     a.kl_coef = q.kl_coef;
-    a.inv_temperature = 1.0f / q.temperature;
+    a.temperature = q.temperature;
     a.grad_scale = q.grad_scale;
-    hipError_t err;
-    if (q.tokens) {
-        if (q.num_segments)
-            hipLaunchKernelGGL(weight_kernel, dim3((unsigned)q.num_segments), dim3(kOpThreads), 0,
-                               stream, q.token_ids, a.wide, a.tokens, a.vocab, q.segment_offsets,
-                               (uint32_t)q.num_segments, weight);
-        else
-            hipLaunchKernelGGL(no_answers_kernel, dim3(64), dim3(kOpThreads), 0, stream, weight,
-                               a.tokens);
-        if ((err = hipGetLastError()) != hipSuccess) return SEGTOPK_HIP_ERROR;
-        const int st = with_type(q.logits.type, [&](auto v) {
-            using T = decltype(v);
-            const T *in = static_cast<const T *>(q.logits.data);
-            T *out = static_cast<T *>(q.dlogits.data);
-            if (grad)
-                hipLaunchKernelGGL((row_kernel<T, true>), dim3(a.tokens), dim3(kRowThreads), 0,
-                                   stream, in, out, a);
-            else
-                hipLaunchKernelGGL((row_kernel<T, false>), dim3(a.tokens), dim3(kRowThreads), 0,
-                                   stream, in, out, a);
+    // The first part rounded down, so that the rest is positive; both within the
+    // normal range, at the temperatures next to zero and infinity too.
+    const double factor =
+        std::fmin(std::fmax(kLog2e / q.temperature, 2.0 * (double)FLT_MIN), (double)FLT_MAX);
+    a.factor = (float)factor;
+    if ((double)a.factor >= factor) a.factor = std::nextafter(a.factor, 0.0f);
+    a.rest = std::fmax((float)(factor - (double)a.factor), FLT_MIN);
+    hipLaunchKernelGGL(count_kernel, dim3(q.num_segments ? (unsigned)q.num_segments : 1u),
+                       dim3(kCountThreads), 0, stream, q.token_ids, a.wide, a.tokens, a.vocab,
+                       q.segment_offsets, (uint32_t)q.num_segments, live, a.arrived);
+    if (hipGetLastError() != hipSuccess) return SEGTOPK_HIP_ERROR;
+    return with_type(q.logits.type, [&](auto v) {
+        using T = decltype(v);
+        const T *in = static_cast<const T *>(q.logits.data);
+        T *out = static_cast<T *>(q.dlogits.data);
+        const auto go = [&](auto with_grad, auto stream_stores, auto threads) {
+            constexpr int kThreads = decltype(threads)::value;
+            hipLaunchKernelGGL(
+                (row_kernel<T, decltype(with_grad)::value, decltype(stream_stores)::value, kThreads>),
+                dim3(a.tokens), dim3(kThreads), 0, stream, in, out, a);
             return status(hipGetLastError());
-        });
-        if (st != SEGTOPK_OK) return st;
-    }
-    hipLaunchKernelGGL(total_kernel, dim3(1), dim3(1024), 0, stream, term, a.tokens, q.loss);
-    return status(hipGetLastError());
+        };
+        const auto by_length = [&](auto with_grad, auto stream_stores) {
+            // The smallest workgroup that holds a row in registers.  4096 rows of
+            // bf16, by 256, 512 and 1024 threads: 1000 logits 24, 32, 53 us; 8000
+            // 32, 37, 58; 16000 53, 45, 63; 32000 105, 88, 78.
+            const int64_t bytes = q.vocab * (int64_t)sizeof(T);
+            return bytes <= 256 * kAtOnce * 16
+                       ? go(with_grad, stream_stores, std::integral_constant<int, 256>{})
+                   : bytes <= 512 * kAtOnce * 16
+                       ? go(with_grad, stream_stores, std::integral_constant<int, 512>{})
+                       : go(with_grad, stream_stores, std::integral_constant<int, 1024>{});
+        };
+        if (!grad) return by_length(std::false_type{}, std::false_type{});
+        return streams(q.tokens * q.vocab * (int64_t)sizeof(T))
+                   ? by_length(std::true_type{}, std::true_type{})
+                   : by_length(std::true_type{}, std::false_type{});
+    });
 }

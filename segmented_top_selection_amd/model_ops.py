@@ -36,9 +36,9 @@ class _Rows(ctypes.Structure):
 
 class _PolicyLossArgs(ctypes.Structure):
     _fields_ = [("logits", _Rows), ("dlogits", _Rows), ("token_ids", ctypes.c_void_p),
-                ("id_type", ctypes.c_int32), ("clip_low", ctypes.c_float),
-                ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
-                ("temperature", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("id_type", ctypes.c_int32), ("clip_low", ctypes.c_double),
+                ("clip_high", ctypes.c_double), ("kl_coef", ctypes.c_double),
+                ("temperature", ctypes.c_double), ("grad_scale", ctypes.c_double),
                 ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64),
                 ("num_segments", ctypes.c_int64), ("segment_offsets", ctypes.c_void_p),
                 ("old_logp", ctypes.c_void_p), ("ref_logp", ctypes.c_void_p),
