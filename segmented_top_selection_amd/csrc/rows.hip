@@ -55,7 +55,7 @@ template <bool ONE> __device__ inline float shared(float v) {
     return ONE ? __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))) : v;
 }
 
-template <class T, bool ONE>
+template <class T, bool ONE, bool STREAM>
 __global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restrict__ x, int64_t xs,
                                                               T *__restrict__ rows, int64_t rs,
                                                               Slots s, Cut c) {
@@ -67,20 +67,23 @@ __global__ __launch_bounds__(kOpThreads) void dispatch_kernel(const T *__restric
         const T *src = x + (int64_t)token * xs;
         for (uint32_t u = blockIdx.y * c.lanes + (threadIdx.x & (c.lanes - 1u)); u < c.units;
              u += gridDim.y * c.lanes) {
-            if (u < c.pieces) {
-                const typename P::vec v = load_piece(src + (size_t)u * P::N);
-                for (uint32_t j = 0; j < s.k; ++j) {
-                    const uint32_t p = shared<ONE>((uint32_t)pos[j]);
-                    if (p < s.count)
-                        store_piece(rows + (int64_t)p * rs + (size_t)u * P::N,
-                                    p < kept ? v : (typename P::vec)(T)0.0f);
-                }
-            } else {
-                const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
-                const T v = src[at];
-                for (uint32_t j = 0; j < s.k; ++j) {
-                    const uint32_t p = shared<ONE>((uint32_t)pos[j]);
-                    if (p < s.count) rows[(int64_t)p * rs + at] = p < kept ? v : (T)0.0f;
+            const bool whole = u < c.pieces;
+            const size_t at = whole ? (size_t)u * P::N : (size_t)c.pieces * P::N + (u - c.pieces);
+            typename P::vec v = (typename P::vec)(T)0.0f;
+            if (whole) v = load_piece(src + at);
+            else v[0] = src[at];
+            for (uint32_t j0 = 0; j0 < s.k; j0 += kSlotsAtOnce) {
+                uint32_t p[kSlotsAtOnce];
+#pragma unroll
+                for (int j = 0; j < kSlotsAtOnce; ++j)
+                    p[j] = shared<ONE>(j0 + j < s.k ? (uint32_t)pos[j0 + j] : 0xFFFFFFFFu);
+#pragma unroll
+                for (int j = 0; j < kSlotsAtOnce; ++j) {
+                    if (p[j] >= s.count) continue;
+                    T *dst = rows + (int64_t)p[j] * rs + at;
+                    const typename P::vec o = p[j] < kept ? v : (typename P::vec)(T)0.0f;
+                    if (whole) store_piece<STREAM>(dst, o);
+                    else *dst = o[0];
                 }
             }
         }
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict
                     for (int j = 0; j < kSlotsAtOnce; ++j) {
                         v[j] = (typename P::vec)(T)0.0f;
                         if (p[j] < kept)
-                            v[j] = load_piece(rows + (int64_t)p[j] * rs + (size_t)u * P::N);
+                            v[j] = load_piece<true>(rows + (int64_t)p[j] * rs + (size_t)u * P::N);
                     }
 #pragma unroll
                     for (int j = 0; j < kSlotsAtOnce; ++j)
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(kOpThreads) void combine_kernel(const T *__restrict
     }
 }
 
-template <class T, class W>
+template <class T, class W, bool STREAM>
 __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
     const T *__restrict__ dout, int64_t ds, const T *__restrict__ rows, int64_t rs,
     T *__restrict__ drows, int64_t drs, const W *__restrict__ weights, W *__restrict__ dweights,
@@ -176,14 +179,14 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
                         for (int j = 0; j < kSlotsAtOnce; ++j) {
                             y[j] = (typename P::vec)(T)0.0f;
                             if (p[j] < kept && dweights)
-                                y[j] = load_piece(rows + (int64_t)p[j] * rs + at);
+                                y[j] = load_piece<true>(rows + (int64_t)p[j] * rs + at);
                         }
 #pragma unroll
                         for (int j = 0; j < kSlotsAtOnce; ++j) {
                             if (p[j] >= s.count) continue;
                             typename P::f32 r = 0.0f;
                             if (p[j] < kept) r = w[j] * d;
-                            store_piece(drows + (int64_t)p[j] * drs + at, narrow<T>(r));
+                            store_piece<STREAM>(drows + (int64_t)p[j] * drs + at, narrow<T>(r));
                         }
 #pragma unroll
                         for (int j = 0; j < kSlotsAtOnce; ++j) {
@@ -230,7 +233,7 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
 
 // A group of threads takes ROWS rows, so that a thread has that many loads in
 // flight.
-template <class T, class I, int ROWS>
+template <class T, class I, int ROWS, bool STREAM>
 __global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restrict__ table,
                                                                int64_t ts, T *__restrict__ out,
                                                                int64_t os,
@@ -261,8 +264,9 @@ __global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restri
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r)
                     if (i0 + r * per < n)
-                        store_piece(out + (int64_t)(i0 + r * per) * os + at,
-                                    id[r] >= 0 ? narrow<T>(scale * widen<T>(v[r])) : v[r]);
+                        store_piece<STREAM>(
+                            out + (int64_t)(i0 + r * per) * os + at,
+                            id[r] >= 0 ? narrow<T>(scale * widen<T>(v[r])) : v[r]);
             } else {
                 const size_t at = (size_t)c.pieces * P::N + (u - c.pieces);
 #pragma unroll
@@ -334,11 +338,16 @@ extern "C" int segtopk_dispatch_rows(const segtopk_rows *x, const segtopk_rows *
     return with_type(x->type, [&](auto t) {
         using T = decltype(t);
         const Cut c = cut_of(width, sizeof(T));
-        hipLaunchKernelGGL((c.lanes >= 64u ? dispatch_kernel<T, true> : dispatch_kernel<T, false>), grid_of(tokens, c), dim3(kOpThreads), 0, stream,
-                           static_cast<const T *>(x->data), x->stride,
-                           static_cast<T *>(rows->data), rows->stride,
-                           slots_of(tokens, k, position, kept), c);
-        return status(hipGetLastError());
+        const auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid_of(tokens, c), dim3(kOpThreads), 0, stream,
+                               static_cast<const T *>(x->data), x->stride,
+                               static_cast<T *>(rows->data), rows->stride,
+                               slots_of(tokens, k, position, kept), c);
+            return status(hipGetLastError());
+        };
+        if (c.lanes < 64u) return go(dispatch_kernel<T, false, false>);
+        return streams(tokens * k * width * (int64_t)sizeof(T)) ? go(dispatch_kernel<T, true, true>)
+                                                                : go(dispatch_kernel<T, true, false>);
     });
 }
 
@@ -358,10 +367,9 @@ extern "C" int segtopk_combine_rows(const segtopk_rows *rows, const segtopk_rows
             using W = decltype(w);
             hipLaunchKernelGGL(
                 (c.lanes >= 64u ? combine_kernel<T, W, true> : combine_kernel<T, W, false>),
-                grid_of(tokens, c), dim3(kOpThreads), 0, stream, static_cast<const T *>(rows->data), rows->stride,
-                               static_cast<T *>(out->data), out->stride,
-                               static_cast<const W *>(weights),
-                               slots_of(tokens, k, position, kept), c);
+                grid_of(tokens, c), dim3(kOpThreads), 0, stream,
+                static_cast<const T *>(rows->data), rows->stride, static_cast<T *>(out->data),
+                out->stride, static_cast<const W *>(weights), slots_of(tokens, k, position, kept), c);
             return status(hipGetLastError());
         };
         return weights && weight_type != SEGTOPK_KEY_F32 ? go(t) : go(float{});
@@ -388,8 +396,11 @@ extern "C" int segtopk_combine_rows_backward(const segtopk_rows *dout, const seg
         c.lanes = c.units > 128u ? (uint32_t)kOpThreads : 64u;
         const auto go = [&](auto w) {
             using W = decltype(w);
-            hipLaunchKernelGGL((combine_backward_kernel<T, W>), dim3(blocks_of(tokens, c)), dim3(kOpThreads), 0,
-                               stream, static_cast<const T *>(dout->data), dout->stride,
+            const bool past = streams(tokens * k * width * (int64_t)sizeof(T));
+            hipLaunchKernelGGL((past ? combine_backward_kernel<T, W, true>
+                                     : combine_backward_kernel<T, W, false>),
+                               dim3(blocks_of(tokens, c)), dim3(kOpThreads), 0, stream,
+                               static_cast<const T *>(dout->data), dout->stride,
                                static_cast<const T *>(rows ? rows->data : nullptr),
                                rows ? rows->stride : 0, static_cast<T *>(drows->data),
                                drows->stride, static_cast<const W *>(weights),
@@ -420,8 +431,11 @@ extern "C" int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_r
         const dim3 grid = grid_of(many ? (n + 3) / 4 : n, c);
         const auto go = [&](auto i, auto rows) {
             using I = decltype(i);
-            hipLaunchKernelGGL((embedding_kernel<T, I, decltype(rows)::value>), grid,
-                               dim3(kOpThreads), 0, stream,
+            constexpr int kRows = decltype(rows)::value;
+            const bool past = kRows > 1 && streams(n * width * (int64_t)sizeof(T));
+            hipLaunchKernelGGL((past ? embedding_kernel<T, I, kRows, (kRows > 1)>
+                                     : embedding_kernel<T, I, kRows, false>),
+                               grid, dim3(kOpThreads), 0, stream,
                                static_cast<const T *>(num_rows ? table->data : nullptr),
                                num_rows ? table->stride : 0, static_cast<T *>(out->data),
                                out->stride, static_cast<const I *>(ids), (uint32_t)n, num_rows,
