@@ -353,7 +353,7 @@ int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_rows *out, c
  * accumulate != 0: the sums are added to what dtable holds, and rows of ids that
  * do not occur are neither read nor written.  dtable is of dout's type or
  * SEGTOPK_KEY_F32.  SEGTOPK_NOT_SUPPORTED: more work than one launch holds
- * (about n * width / 64 Ki + num_rows / 16 >= 2^24).
+ * (about n * width / 64 Ki >= 2^24).
  */
 int64_t segtopk_embedding_backward_workspace(int64_t n, int64_t num_rows, int64_t width);
 int segtopk_embedding_backward(const segtopk_rows *dout, const segtopk_rows *dtable,

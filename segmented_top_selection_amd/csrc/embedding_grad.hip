@@ -1,26 +1,25 @@
 // embedding_grad.hip -- the gradient of an embedding table:
 //   dtable[v] = scale * sum_{i : id_i = v} dout[i]      (v != padding)
 //
-// The tokens are sorted by id (sort_ids.hip); equal ids then lie in runs, and
-// the sorted tokens are cut into chunks of 8 to 32 rows, so that a frequent
-// token costs no workgroup more than any other:
+// The table is cleared beside the sort of the tokens by id (sort_ids.hip), which
+// leaves most of the device idle.  Equal ids then lie in runs, and the sorted
+// tokens are cut into chunks of 8 to 64 rows, so that a frequent token costs no
+// workgroup more than any other:
 //   sum_kernel     a workgroup adds up one chunk, 16 bytes of a row to a thread,
 //                  in 32 bits; a run inside the chunk goes to its row of the
 //                  table at once, a run that crosses the chunk's border leaves a
-//                  32-bit partial row.  Other workgroups of the same launch
-//                  write the zero rows of ids that no token has.
-//   finish_kernel  adds the partial rows of a run, chunk by chunk.
+//                  32-bit partial row
+//   finish_kernel  adds the partial rows of a run, chunk by chunk
 // Every sum has one fixed order: results are the same every time.
 //
-// Bound by writing the table: most of its rows are zeros.
+// Bound by writing the table, most of whose rows are zeros, and reading dout.
 #include "ops_common.h"
 
 namespace segtopk_ops {
 namespace {
 
-constexpr uint32_t kMaxChunk = 32;  // rows of dout that a workgroup adds up
+constexpr uint32_t kMaxChunk = 64;  // rows of dout that a workgroup adds up
 constexpr int kRowsAtOnce = 8;      // of which so many are in flight together
-constexpr uint32_t kZeroRows = 16;  // rows of the table that a workgroup looks up and clears
 
 struct GradArgs {
     const int32_t *order;
@@ -52,91 +51,78 @@ __device__ inline void put_piece(O *dst, typename Piece<T>::f32 v, const GradArg
     *d = __builtin_convertvector(v, vec);
 }
 
+// Clears rows that are not one piece of memory, or where there is no sort.
+template <class O>
+__global__ __launch_bounds__(kOpThreads) void clear_kernel(O *table, uint32_t num_rows,
+                                                           int64_t width, int64_t ts) {
+    using Q = Piece<O>;
+    const int64_t pieces = width / Q::N;
+    for (uint32_t v = blockIdx.x; v < num_rows; v += gridDim.x) {
+        O *dst = table + (int64_t)v * ts;
+        for (int64_t u = threadIdx.x; u < pieces; u += kOpThreads)
+            store_piece(dst + u * Q::N, (typename Q::vec)(O)0.0f);
+        for (int64_t i = pieces * Q::N + threadIdx.x; i < width; i += kOpThreads) dst[i] = (O)0.0f;
+    }
+}
+
 template <class T, class O>
 __global__ __launch_bounds__(kOpThreads) void sum_kernel(const T *__restrict__ dout, O *table,
                                                          GradArgs a) {
     using P = Piece<T>;
     const uint32_t t = threadIdx.x;
-    if (blockIdx.x < a.chunks * a.cols) {
-        __shared__ uint32_t id[kMaxChunk], row[kMaxChunk];
-        const uint32_t chunk = blockIdx.x / a.cols, col = blockIdx.x % a.cols;
-        const uint32_t b = chunk * a.chunk, m = min(a.chunk, a.n - b);
-        if (t < m) {
-            id[t] = a.sorted[b + t];
-            row[t] = (uint32_t)a.order[b + t];
-        }
-        __syncthreads();
-        const bool joins = b && a.sorted[b - 1] == id[0];
-        const bool goes_on = b + m < a.n && a.sorted[b + m] == id[m - 1];
-        for (uint32_t u = col * kOpThreads + t; u < a.units; u += a.cols * kOpThreads) {
-            const bool whole = u < a.pieces;
-            const size_t at = whole ? (size_t)u * P::N : (size_t)a.pieces * P::N + (u - a.pieces);
-            typename P::f32 acc = 0.0f;
-            uint32_t first = 0;  // of the run that is being added
-            for (uint32_t i0 = 0; i0 < m; i0 += kRowsAtOnce) {
-                uint32_t key[kRowsAtOnce + 1];
-                typename P::vec v[kRowsAtOnce];
-#pragma unroll
-                for (int r = 0; r <= kRowsAtOnce; ++r)  // past the chunk: no id
-                    key[r] = __builtin_amdgcn_readfirstlane(i0 + r < m ? id[i0 + r] : 0xFFFFFFFFu);
-#pragma unroll
-                for (int r = 0; r < kRowsAtOnce; ++r) {
-                    v[r] = (typename P::vec)(T)0.0f;
-                    if (!counts(a, key[r])) continue;
-                    const T *src = dout + (int64_t)row[i0 + r] * a.ds + at;
-                    if (whole) v[r] = load_piece(src);
-                    else v[r][0] = *src;
-                }
-#pragma unroll
-                for (int r = 0; r < kRowsAtOnce; ++r) {
-                    if (key[r] == 0xFFFFFFFFu) continue;
-                    acc += widen<T>(v[r]);
-                    if (key[r + 1] == key[r]) continue;
-                    const uint32_t i = i0 + r;
-                    if (counts(a, key[r])) {
-                        const bool head = first == 0 && joins, tail = i + 1 == m && goes_on;
-                        if (head || tail) {
-                            float *dst = a.part + ((size_t)chunk * 2 + (head ? 1 : 0)) * a.width + at;
-                            typedef float mem
-                                __attribute__((ext_vector_type(16 / sizeof(T)), aligned(4)));
-                            if (whole) *reinterpret_cast<mem *>(dst) = acc;
-                            else *dst = acc[0];
-                        } else {
-                            O *dst = table + (int64_t)key[r] * a.ts + at;
-                            if (whole) put_piece<T>(dst, acc, a);
-                            else put(dst, acc[0], a);
-                        }
-                    }
-                    acc = 0.0f;
-                    first = i + 1;
-                }
-            }
-        }
-        return;
-    }
-    // Rows of ids that no token has, and the padding's.
-    __shared__ uint32_t empty[kZeroRows];
-    const uint32_t v0 = (blockIdx.x - a.chunks * a.cols) * kZeroRows;
-    if (t < kZeroRows) {
-        const uint32_t v = v0 + t;
-        uint32_t lo = 0, hi = a.n;
-        while (lo < hi) {
-            const uint32_t mid = lo + ((hi - lo) >> 1);
-            if (a.sorted[mid] < v) lo = mid + 1;
-            else hi = mid;
-        }
-        empty[t] = v < a.num_rows && (lo >= a.n || a.sorted[lo] != v || v == a.padding);
+    __shared__ uint32_t id[kMaxChunk], row[kMaxChunk];
+    const uint32_t chunk = blockIdx.x / a.cols, col = blockIdx.x % a.cols;
+    const uint32_t b = chunk * a.chunk, m = min(a.chunk, a.n - b);
+    if (t < m) {
+        id[t] = a.sorted[b + t];
+        row[t] = (uint32_t)a.order[b + t];
     }
     __syncthreads();
-    using Q = Piece<O>;
-    const uint32_t pieces = (uint32_t)(a.width / Q::N);
-    for (uint32_t r = 0; r < kZeroRows; ++r) {
-        if (!empty[r]) continue;
-        O *dst = table + (int64_t)(v0 + r) * a.ts;
-        for (uint32_t u = t; u < pieces; u += kOpThreads)
-            store_piece(dst + (size_t)u * Q::N, (typename Q::vec)(O)0.0f);
-        for (size_t i = (size_t)pieces * Q::N + t; i < (size_t)a.width; i += kOpThreads)
-            dst[i] = (O)0.0f;
+    const bool joins = b && a.sorted[b - 1] == id[0];
+    const bool goes_on = b + m < a.n && a.sorted[b + m] == id[m - 1];
+    for (uint32_t u = col * kOpThreads + t; u < a.units; u += a.cols * kOpThreads) {
+        const bool whole = u < a.pieces;
+        const size_t at = whole ? (size_t)u * P::N : (size_t)a.pieces * P::N + (u - a.pieces);
+        typename P::f32 acc = 0.0f;
+        uint32_t first = 0;  // of the run that is being added
+        for (uint32_t i0 = 0; i0 < m; i0 += kRowsAtOnce) {
+            uint32_t key[kRowsAtOnce + 1];
+            typename P::vec v[kRowsAtOnce];
+#pragma unroll
+            for (int r = 0; r <= kRowsAtOnce; ++r)  // past the chunk: no id
+                key[r] = __builtin_amdgcn_readfirstlane(i0 + r < m ? id[i0 + r] : 0xFFFFFFFFu);
+#pragma unroll
+            for (int r = 0; r < kRowsAtOnce; ++r) {
+                v[r] = (typename P::vec)(T)0.0f;
+                if (!counts(a, key[r])) continue;
+                const T *src = dout + (int64_t)row[i0 + r] * a.ds + at;
+                if (whole) v[r] = load_piece<true>(src);
+                else v[r][0] = *src;
+            }
+#pragma unroll
+            for (int r = 0; r < kRowsAtOnce; ++r) {
+                if (key[r] == 0xFFFFFFFFu) continue;
+                acc += widen<T>(v[r]);
+                if (key[r + 1] == key[r]) continue;
+                const uint32_t i = i0 + r;
+                if (counts(a, key[r])) {
+                    const bool head = first == 0 && joins, tail = i + 1 == m && goes_on;
+                    if (head || tail) {
+                        float *dst = a.part + ((size_t)chunk * 2 + (head ? 1 : 0)) * a.width + at;
+                        typedef float mem
+                            __attribute__((ext_vector_type(16 / sizeof(T)), aligned(4)));
+                        if (whole) *reinterpret_cast<mem *>(dst) = acc;
+                        else *dst = acc[0];
+                    } else {
+                        O *dst = table + (int64_t)key[r] * a.ts + at;
+                        if (whole) put_piece<T>(dst, acc, a);
+                        else put(dst, acc[0], a);
+                    }
+                }
+                acc = 0.0f;
+                first = i + 1;
+            }
+        }
     }
 }
 
@@ -169,15 +155,23 @@ __global__ __launch_bounds__(kOpThreads) void finish_kernel(O *table, GradArgs a
         const bool whole = c + 4 <= a.width;
         const uint32_t rest = c < a.width && !whole ? (uint32_t)(a.width - c) : 0u;
         f4 acc = 0.0f;
-#pragma unroll 8
-        for (uint32_t i = chunk + w; i <= last; i += kWaves) {
-            const float *src = a.part + ((size_t)i * 2 + (i == chunk ? 0 : 1)) * a.width + c;
-            if (whole) acc += *reinterpret_cast<const f4mem *>(src);
-            else if (rest) {
-                acc[0] += src[0];
-                if (rest > 1) acc[1] += src[1];
-                if (rest > 2) acc[2] += src[2];
+        for (uint32_t i0 = chunk + w; i0 <= last; i0 += kWaves * kRowsAtOnce) {
+            f4 v[kRowsAtOnce];
+#pragma unroll
+            for (int r = 0; r < kRowsAtOnce; ++r) {
+                const uint32_t i = i0 + r * kWaves;
+                v[r] = 0.0f;
+                if (i > last) continue;
+                const float *src = a.part + ((size_t)i * 2 + (i == chunk ? 0 : 1)) * a.width + c;
+                if (whole) v[r] = *reinterpret_cast<const f4mem *>(src);
+                else if (rest) {
+                    v[r][0] = src[0];
+                    if (rest > 1) v[r][1] = src[1];
+                    if (rest > 2) v[r][2] = src[2];
+                }
             }
+#pragma unroll
+            for (int r = 0; r < kRowsAtOnce; ++r) acc += v[r];
         }
         part[w][lane] = acc;
         __syncthreads();
@@ -202,9 +196,11 @@ struct GradPlan {
 
 GradPlan grad_plan(int64_t n, int64_t num_rows, int64_t width) {
     GradPlan p;
-    // Long chunks leave few partial rows; shorter ones fill the device where
-    // there are few tokens.
-    p.chunk = n >= 16384 ? kMaxChunk : n >= 8192 ? 16u : 8u;
+    // Long chunks leave few partial rows; shorter ones make two workgroups for every
+    // CU where there are few tokens.
+    const int64_t cols = (width + 2047) / 2048;
+    p.chunk = kMaxChunk;
+    while (p.chunk > 8 && n * cols / p.chunk < 512) p.chunk /= 2;
     p.chunks = (uint32_t)((n + p.chunk - 1) / p.chunk);
     p.sort_bytes = round_up(sort_workspace(n, num_rows));
     p.index_bytes = round_up((size_t)n * 4);
@@ -214,15 +210,12 @@ GradPlan grad_plan(int64_t n, int64_t num_rows, int64_t width) {
 }
 
 template <class T, class O>
-hipError_t queue_grad(const segtopk_rows *dout, const segtopk_rows *dtable, GradArgs a,
+hipError_t queue_grad(const segtopk_rows *dout, const segtopk_rows *dtable, const GradArgs &a,
                       hipStream_t stream) {
-    const uint32_t zero = a.accumulate ? 0u : (a.num_rows + kZeroRows - 1) / kZeroRows;
-    const uint32_t grid = a.chunks * a.cols + zero;
-    if (!grid) return hipSuccess;
     O *table = static_cast<O *>(dtable->data);
-    hipLaunchKernelGGL((sum_kernel<T, O>), dim3(grid), dim3(kOpThreads), 0, stream,
-                       static_cast<const T *>(dout ? dout->data : nullptr), table, a);
-    hipError_t err = hipGetLastError();
+    hipLaunchKernelGGL((sum_kernel<T, O>), dim3(a.chunks * a.cols), dim3(kOpThreads), 0, stream,
+                       static_cast<const T *>(dout->data), table, a);
+    const hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.chunks < 2) return err;
     const int64_t y = (a.width + 255) / 256;
     hipLaunchKernelGGL(finish_kernel<O>, dim3(a.chunks - 1, (unsigned)(y < 64 ? y : 64)),
@@ -262,16 +255,32 @@ extern "C" int segtopk_embedding_backward(const segtopk_rows *dout, const segtop
     const int64_t per = 16 / element_bytes(n ? dout->type : dtable->type);
     const int64_t units = width / per + width % per, cols = (units + kOpThreads - 1) / kOpThreads;
     // A launch holds fewer than 2^32 threads.
-    if ((int64_t)p.chunks * cols + num_rows / kZeroRows >= (1 << 24) - 1)
-        return SEGTOPK_NOT_SUPPORTED;
+    if ((int64_t)p.chunks * cols >= (1 << 24) - 1) return SEGTOPK_NOT_SUPPORTED;
     if (p.bytes && (!workspace || !aligned(workspace, 256))) return SEGTOPK_INVALID_ARGUMENT;
     if (workspace_bytes < 0 || (size_t)workspace_bytes < p.bytes) return SEGTOPK_SCRATCH_TOO_SMALL;
 
     char *ws = static_cast<char *>(workspace);
     int32_t *order = reinterpret_cast<int32_t *>(ws + p.sort_bytes);
     uint32_t *sorted = reinterpret_cast<uint32_t *>(ws + p.sort_bytes + p.index_bytes);
-    if (n && queue_sort(ids, id_type, n, num_rows, order, nullptr, nullptr, sorted, workspace,
-                        stream) != hipSuccess)
+    // A table in one piece is cleared beside the sort, before it is known which of
+    // its rows are used: at most one more row is written for each of dout's.
+    const int64_t table_bytes = num_rows * width * element_bytes(dtable->type);
+    const bool flat = n && (dtable->stride == width || num_rows == 1) && aligned(dtable->data, 16);
+    Fill fill{dtable->data, flat && !accumulate ? (uint64_t)table_bytes : 0, streams(table_bytes)};
+    if (!flat && !accumulate) {
+        const unsigned grid = (unsigned)(num_rows < kFillBlocks ? num_rows : kFillBlocks);
+        const int st = with_type(dtable->type, [&](auto o) {
+            using O = decltype(o);
+            hipLaunchKernelGGL(clear_kernel<O>, dim3(grid), dim3(kOpThreads), 0, stream,
+                               static_cast<O *>(dtable->data), (uint32_t)num_rows, width,
+                               dtable->stride);
+            return status(hipGetLastError());
+        });
+        if (st != SEGTOPK_OK) return st;
+    }
+    if (!n) return SEGTOPK_OK;
+    if (queue_sort(ids, id_type, n, num_rows, order, nullptr, nullptr, sorted, workspace, stream,
+                   &fill) != hipSuccess)
         return SEGTOPK_HIP_ERROR;
     GradArgs a{};
     a.order = order;
@@ -282,16 +291,15 @@ extern "C" int segtopk_embedding_backward(const segtopk_rows *dout, const segtop
     a.chunks = p.chunks;
     a.num_rows = (uint32_t)num_rows;
     a.padding = padding_id >= 0 && padding_id < num_rows ? (uint32_t)padding_id : 0xFFFFFFFFu;
-    const int row_type = n ? dout->type : dtable->type;
     a.pieces = (uint32_t)(width / per);
     a.units = (uint32_t)units;
     a.cols = (uint32_t)cols;
     a.scale = scale;
     a.accumulate = accumulate != 0;
     a.width = width;
-    a.ds = n ? dout->stride : 0;
+    a.ds = dout->stride;
     a.ts = dtable->stride;
-    return with_type(row_type, [&](auto t) {
+    return with_type(dout->type, [&](auto t) {
         using T = decltype(t);
         return status(dtable->type == SEGTOPK_KEY_F32 ? queue_grad<T, float>(dout, dtable, a, stream)
                                                       : queue_grad<T, T>(dout, dtable, a, stream));

@@ -2,19 +2,20 @@
 // order = stable argsort of key_i, where key_i = id_i inside [0, S) and S
 // otherwise; position = its inverse; offsets[s] = #{i : key_i < s}.
 //
-// Least-significant-digit radix passes of at most 9 bits, by workgroups of 16
-// waves.  A block of up to 8192 items stays in registers, eight to a lane, each
-// wave holding consecutive items.  A wave takes its items 64 at a time and
+// Few ids among many segments, an embedding's tokens:
+//   rank_kernel        counts for each item those before it, n^2 comparisons spread
+//                      over the device
+// Otherwise least-significant-digit radix passes of at most 9 bits, by workgroups
+// of 16 waves.  A block of up to 8192 items stays in registers, eight to a lane,
+// each wave holding consecutive items.  A wave takes its items 64 at a time and
 // ranks equal digits by the lanes below (one ballot a bit) and the wave's own
 // counters in LDS; the counters of the 16 waves, summed digit by digit, then
-// say where each wave's items of a digit start.  No atomic decides an order, so
-// results are the same every time.
-//   block_sort_kernel  up to 8192 items: all passes in one launch, items
-//                      exchanged through LDS between them
-//   count_kernel       more: the digit histogram of each chunk of blocks,
+// say where each wave's items of a digit start.
+//   block_sort_kernel  a block in one pass, which is up to 511 segments
+//   count_kernel       more items or passes: the digit histogram of each chunk,
 //   scatter_kernel     and the pass itself, every workgroup adding up the
 //                      histograms of the chunks before its own
-// Up to 511 segments take one pass, up to 262143 two.
+// No atomic decides an order, so results are the same every time.
 //
 // Bound by launches and by the latency of the dependent steps, not by its
 // bytes (16 to 20 an item).
@@ -41,8 +42,9 @@ struct SortArgs {
     int32_t *position;     // last pass, or nullptr
     int64_t *offsets;      // of a sort in one pass, or nullptr
     uint32_t *hist;        // [chunks][bins]
-    uint32_t n, segments, chunk, chunks, shift, bins, bits, passes;
+    uint32_t n, segments, chunk, chunks, shift, bins, bits;
     uint32_t wide;         // ids of 64 bits
+    Fill fill;             // cleared by the workgroups past `chunks`
 };
 
 template <bool FIRST> __device__ inline uint32_t sort_key(const SortArgs &a, uint32_t i) {
@@ -114,66 +116,44 @@ __device__ inline uint32_t wave_starts(uint32_t *whist, uint32_t bins, uint32_t 
     return base;
 }
 
-// KEEP: room for the exchange between passes.
-template <bool KEEP>
 __global__ __launch_bounds__(kSortThreads) void block_sort_kernel(SortArgs a) {
     __shared__ uint32_t whist[kSortWaves * kMaxBins], wave_total[kSortWaves];
-    __shared__ uint32_t keys[KEEP ? kBlock : 1], slots[KEEP ? kBlock : 1];
+    if (blockIdx.x) return clear(a.fill, blockIdx.x - 1u, gridDim.x - 1u);
     const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
     Items x;
     x.items = (a.n + kSortThreads - 1) / kSortThreads;
     x.first = w * 64u * x.items + lane;
     x.count = a.n;
-    uint32_t slot[kItems];
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) x.key[r] = x.live(r) ? sort_key<true>(a, x.at(r)) : 0u;
+    for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
+    __syncthreads();
+    rank_items(x, 0, a.bits, whist + w * a.bins);
+    __syncthreads();
+    uint32_t own = 0;
+    if (t < a.bins)
+#pragma unroll
+        for (uint32_t i = 0; i < kSortWaves; ++i) own += whist[i * a.bins + t];
+    const uint32_t base = digit_prefix(own, wave_total);
+    if (t < a.bins) {
+        if (a.offsets) a.offsets[t] = base;  // bins = segments + 1
+        wave_starts(whist, a.bins, t, base);
+    }
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < kItems; ++r) {
-        slot[r] = x.at(r);
-        x.key[r] = x.live(r) ? sort_key<true>(a, slot[r]) : 0u;
-    }
-    for (uint32_t pass = 0, shift = 0; pass < a.passes; ++pass, shift += a.bits) {
-        for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
-        __syncthreads();
-        rank_items(x, shift, a.bits, whist + w * a.bins);
-        __syncthreads();
-        uint32_t own = 0;
-        if (t < a.bins)
-#pragma unroll
-            for (uint32_t i = 0; i < kSortWaves; ++i) own += whist[i * a.bins + t];
-        const uint32_t base = digit_prefix(own, wave_total);
-        if (t < a.bins) {
-            if (a.offsets) a.offsets[t] = base;  // one pass: bins = segments + 1
-            wave_starts(whist, a.bins, t, base);
-        }
-        __syncthreads();
-        const bool last = pass + 1 == a.passes;
-#pragma unroll
-        for (int r = 0; r < kItems; ++r) {
-            if (!x.live(r)) continue;
-            const uint32_t digit = (x.key[r] >> shift) & ((1u << a.bits) - 1u);
-            const uint32_t at = whist[w * a.bins + digit] + x.rank[r];
-            if (!last) {
-                keys[KEEP ? at : 0] = x.key[r];
-                slots[KEEP ? at : 0] = slot[r];
-            } else {
-                if (a.key_out) a.key_out[at] = x.key[r];
-                if (a.slot_out) a.slot_out[at] = slot[r];
-                if (a.position) a.position[slot[r]] = (int32_t)at;
-            }
-        }
-        if (!KEEP || last) break;
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kItems; ++r)
-            if (x.live(r)) {
-                x.key[r] = keys[x.at(r)];
-                slot[r] = slots[x.at(r)];
-            }
+        if (!x.live(r)) continue;
+        const uint32_t at = whist[w * a.bins + x.key[r]] + x.rank[r];
+        if (a.key_out) a.key_out[at] = x.key[r];
+        if (a.slot_out) a.slot_out[at] = x.at(r);
+        if (a.position) a.position[x.at(r)] = (int32_t)at;
     }
 }
 
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a) {
     __shared__ uint32_t cnt[kMaxBins];
+    if (blockIdx.x >= a.chunks) return clear(a.fill, blockIdx.x - a.chunks, gridDim.x - a.chunks);
     const uint32_t t = threadIdx.x;
     if (t < a.bins) cnt[t] = 0u;
     __syncthreads();
@@ -189,6 +169,7 @@ template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
     __shared__ uint32_t whist[kSortWaves * kMaxBins], wave_total[kSortWaves];
     __shared__ uint32_t total[kMaxBins], before[kMaxBins];
+    if (blockIdx.x >= a.chunks) return clear(a.fill, blockIdx.x - a.chunks, gridDim.x - a.chunks);
     const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
     const uint32_t b = blockIdx.x * a.chunk, e = min(a.n, b + a.chunk);
     const uint32_t block = min(a.chunk, kBlock);
@@ -251,6 +232,53 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
     }
 }
 
+// The place of an item is the number of items that go before it: those of a
+// smaller key, and of the same key before it.  A workgroup places 32 items, each
+// by 32 threads that go over n / 32 keys each.
+constexpr uint32_t kRankItems = 32;
+constexpr uint32_t kRankParts = kSortThreads / kRankItems;
+// Keys that a thread goes over: whole blocks of 32.
+__host__ __device__ inline uint32_t rank_part(uint32_t n) {
+    return (n + kSortThreads - 1u) / kSortThreads * kRankItems;
+}
+
+__global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
+    extern __shared__ uint4 staged[];  // twice each key; past the last one the largest number
+    __shared__ uint32_t place[kRankItems];
+    if (blockIdx.x >= a.chunks) return clear(a.fill, blockIdx.x - a.chunks, gridDim.x - a.chunks);
+    uint32_t *const twice = reinterpret_cast<uint32_t *>(staged);
+    const uint32_t t = threadIdx.x, first = blockIdx.x * kRankItems;
+    const uint32_t per = rank_part(a.n), all = per * kRankParts;
+    for (uint32_t i = t; i < all; i += kSortThreads)
+        twice[i] = i < a.n ? 2u * sort_key<true>(a, i) : 0xFFFFFFFFu;
+    if (t < kRankItems) place[t] = 0u;
+    __syncthreads();
+    const uint32_t item = first + t % kRankItems, part = t / kRankItems;
+    const uint32_t mine = item < a.n ? twice[item] : 0u;
+    uint32_t before = 0;
+    // A block of 32 keys lies before, at, or past the workgroup's items.  Before
+    // them equal keys count: 2 key_j < 2 key_i + 1.
+    for (uint32_t b = part * per; b < (part + 1u) * per; b += kRankItems) {
+        const uint32_t limit = mine + (b < first ? 1u : 0u);
+#pragma unroll
+        for (uint32_t j = 0; j < kRankItems / 4; ++j) {
+            const uint4 k = staged[b / 4 + j];
+            before += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+        }
+    }
+    // Of the workgroup's own items, one each.
+    const uint32_t other = first + part;
+    before += other < item && twice[other] == mine;
+    atomicAdd(&place[t % kRankItems], before);  // integers: any order gives the same sum
+    __syncthreads();
+    if (t < kRankItems && item < a.n) {
+        const uint32_t at = place[t];
+        if (a.key_out) a.key_out[at] = mine / 2u;
+        if (a.slot_out) a.slot_out[at] = item;
+        if (a.position) a.position[item] = (int32_t)at;
+    }
+}
+
 // offsets[s] of a sort in several passes: the first place of a key >= s.
 __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segments,
                                int64_t *offsets) {
@@ -265,7 +293,10 @@ __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segm
     offsets[s] = lo;
 }
 
+constexpr int64_t kMaxRanked = 15360;
+
 struct SortPlan {
+    bool ranked;  // by rank_kernel
     int passes, bits;
     uint32_t bins, chunk, chunks;
     size_t hist_bytes, pair_bytes, bytes;
@@ -285,6 +316,12 @@ SortPlan sort_plan(int64_t n, int64_t segments) {
         p.bits = (bits + p.passes - 1) / p.passes;
         p.bins = 1u << p.bits;
     }
+    p.ranked = p.passes > 1 && n <= kMaxRanked;
+    if (p.ranked) {
+        p.chunks = n ? (uint32_t)((n + kRankItems - 1) / kRankItems) : 1u;
+        p.pair_bytes = p.bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
+        return p;
+    }
     // One block, or chunks of whole blocks (of part of one, where there are few
     // items): few enough for a workgroup to add up all their histograms.
     int64_t chunk = kBlock;
@@ -301,7 +338,7 @@ SortPlan sort_plan(int64_t n, int64_t segments) {
     // and of one in several chunks, keys and slots between the passes, in two
     // buffers taken in turn.
     p.pair_bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
-    p.bytes = p.hist_bytes + (p.passes > 1 ? (p.chunks > 1 ? 5 : 1) : 0) * p.pair_bytes;
+    p.bytes = p.hist_bytes + (p.passes > 1 ? 5 : 0) * p.pair_bytes;
     return p;
 }
 
@@ -311,12 +348,12 @@ size_t sort_workspace(int64_t n, int64_t segments) { return sort_plan(n, segment
 
 hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments, int32_t *order,
                       int32_t *position, int64_t *offsets, uint32_t *sorted, void *workspace,
-                      hipStream_t stream) {
+                      hipStream_t stream, const Fill *fill) {
     const SortPlan p = sort_plan(n, segments);
     char *ws = static_cast<char *>(workspace);
     uint32_t *pair[2][2] = {};
     if (p.passes > 1 && !sorted) sorted = reinterpret_cast<uint32_t *>(ws + p.hist_bytes);
-    if (p.passes > 1 && p.chunks > 1)
+    if (p.passes > 1 && !p.ranked)
         for (int i = 0; i < 4; ++i)
             pair[i >> 1][i & 1] =
                 reinterpret_cast<uint32_t *>(ws + p.hist_bytes + (i + 1) * p.pair_bytes);
@@ -330,18 +367,32 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
     a.bins = p.bins;
     a.bits = (uint32_t)p.bits;
     a.wide = id_type == SEGTOPK_KEY_I64;
-    a.passes = (uint32_t)p.passes;
     a.offsets = p.passes == 1 ? offsets : nullptr;
-    hipError_t err;
-    if (p.chunks == 1) {
+    const Fill whole = fill ? *fill : Fill{};
+    const uint64_t launches = p.ranked || p.chunks == 1 ? 1 : 2 * p.passes;
+    const uint64_t share = ((whole.bytes + launches - 1) / launches + 15) & ~(uint64_t)15;
+    uint64_t filled = 0;
+    hipError_t err = hipSuccess;
+    const auto launch = [&](auto kernel, size_t lds) {
+        const uint64_t left = whole.bytes - filled;
+        a.fill = whole;
+        a.fill.data = static_cast<char *>(whole.data) + filled;
+        a.fill.bytes = left < share ? left : share;
+        filled += a.fill.bytes;
+        hipLaunchKernelGGL(kernel, dim3(p.chunks + fill_blocks(a.fill, kSortThreads)),
+                           dim3(kSortThreads), lds, stream, a);
+        err = hipGetLastError();
+        return err == hipSuccess;
+    };
+    if (p.ranked || p.chunks == 1) {
         a.key_out = sorted;
         a.slot_out = reinterpret_cast<uint32_t *>(order);
         a.position = position;
-        hipLaunchKernelGGL(p.passes > 1 ? block_sort_kernel<true> : block_sort_kernel<false>,
-                           dim3(1), dim3(kSortThreads), 0, stream, a);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        if (p.ranked ? !launch(rank_kernel, (size_t)rank_part(a.n) * kRankParts * 4)
+                     : !launch(block_sort_kernel, 0))
+            return err;
     }
-    for (int i = 0; p.chunks > 1 && i < p.passes; ++i) {
+    for (int i = 0; !p.ranked && p.chunks > 1 && i < p.passes; ++i) {
         const bool last = i == p.passes - 1;
         a.shift = (uint32_t)(i * p.bits);
         a.key_in = i ? pair[(i - 1) & 1][0] : nullptr;
@@ -349,12 +400,8 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
         a.key_out = last ? sorted : pair[i & 1][0];
         a.slot_out = last ? reinterpret_cast<uint32_t *>(order) : pair[i & 1][1];
         a.position = last ? position : nullptr;
-        hipLaunchKernelGGL(i ? count_kernel<false> : count_kernel<true>, dim3(p.chunks),
-                           dim3(kSortThreads), 0, stream, a);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-        hipLaunchKernelGGL(i ? scatter_kernel<false> : scatter_kernel<true>, dim3(p.chunks),
-                           dim3(kSortThreads), 0, stream, a);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
+        if (!launch(i ? count_kernel<false> : count_kernel<true>, 0)) return err;
+        if (!launch(i ? scatter_kernel<false> : scatter_kernel<true>, 0)) return err;
     }
     if (p.passes > 1 && offsets) {
         hipLaunchKernelGGL(offsets_kernel, dim3((unsigned)((segments + 256) / 256)), dim3(256), 0,

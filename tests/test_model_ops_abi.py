@@ -119,7 +119,6 @@ def test_embedding_matrix_refusals_and_empty_calls():
     assert need(-1, 5, 64) == need(10, -5, 64) == need(10, 5, 0) == 0
     # More work than one launch holds.
     assert embed_grad(n=2 ** 30, ws_bytes=2 ** 62) == NOT_SUPPORTED
-    assert embed_grad(num_rows=2 ** 29, ws_bytes=2 ** 62) == NOT_SUPPORTED
 
 
 def policy(ws=WS, ws_bytes=1 << 30, **kw):
