@@ -64,6 +64,7 @@ _SIGNATURES = {
 }
 
 
+_NO_ROWS = _Rows()
 _entries = {}
 
 
@@ -103,13 +104,21 @@ def _loss_workspace(tokens, vocab, num_segments):
 # where it is asked for.
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
+# A decode step calls these for microseconds of work each, so what the host does
+# counts: names that every call uses are the module's own, a tensor's metadata is
+# read once, and the checks of the usual case come before their messages.
+_Tensor, _I32T, _I64T, _F32T = torch.Tensor, torch.int32, torch.int64, torch.float32
+_empty = torch.empty_strided  # torch.empty takes a third longer to say the same
+
 
 def _on_its_stream(fn):
     """Runs fn on the device of its first tensor and on the stream asked for."""
     @functools.wraps(fn)
     def wrapped(first, *args, stream=None, **kw):
-        if isinstance(first, torch.Tensor) and first.is_cuda and (
-                stream is not None or first.device.index != _current_device()):
+        if not isinstance(first, _Tensor) or (stream is None and
+                                              first.get_device() == _current_device()):
+            return fn(first, *args, **kw)
+        if first.is_cuda:
             if stream is not None and stream.device != first.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors are on {first.device}")
             with torch.cuda.device(first.device), torch.cuda.stream(stream):
@@ -125,48 +134,40 @@ def _stream(dev):
 
 
 def _device_of(name, t):
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     return t.device
 
 
-def _matrix(name, t, dev, shape=None, dtype=None):
-    """t as rows with a unit inner stride that do not overlap."""
-    if isinstance(t, torch.Tensor) and t.device == dev and t.dtype in _FLOAT and t.dim() == 2 \
-            and t.is_contiguous() and t.shape[1] and shape is None and dtype is None:
-        return t
-    _device_tensor(name, t, dev)
-    if t.dtype not in _FLOAT:
+def _there(name, t, dev):
+    if not isinstance(t, _Tensor) or t.device != dev:
+        _device_tensor(name, t, dev)
+
+
+def _overlaps(t):
+    """Whether a matrix is other than rows with a unit inner stride, apart from each other."""
+    return (t.stride(1) != 1 and t.shape[1] > 1) or (t.stride(0) < t.shape[1] and t.shape[0] > 1)
+
+
+def _matrix(name, t, dev):
+    """t as rows with a unit inner stride that do not overlap: (t, number of
+    rows, width, the library's view of it)."""
+    _there(name, t, dev)
+    code, shape = _FLOAT.get(t.dtype), t.shape
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape) if shape else '(rows, width)'} "
-                         f"(got {tuple(t.shape)})")
-    if t.shape[1] < 1:
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have shape (rows, width) (got {tuple(shape)})")
+    rows, width = shape
+    if width < 1:
         raise ValueError(f"{name} must be at least one element wide")
-    if (t.stride(1) != 1 and t.shape[1] > 1) or (t.stride(0) < t.shape[1] and t.shape[0] > 1):
+    if t.is_contiguous():
+        return t, rows, width, _Rows(t.data_ptr(), width, code)
+    if _overlaps(t):
         t = t.contiguous()
-    return t
-
-
-def _result(name, t, dev, shape, dtype):
-    """An output that the caller gave, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _device_tensor(name, t, dev)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if t.dim() == 2 and ((t.stride(1) != 1 and t.shape[1] > 1) or
-                         (t.stride(0) < t.shape[1] and t.shape[0] > 1)):
-        raise ValueError(f"{name} must have a unit inner stride and rows that do not overlap")
-    if t.dim() != 2 and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    return t, rows, width, _rows(t)
 
 
 def _rows(t):
@@ -175,25 +176,47 @@ def _rows(t):
     return _Rows(t.data_ptr(), stride if stride > width else width, _FLOAT[t.dtype])
 
 
-def _ids(name, t, dev):
-    _device_tensor(name, t, dev)
-    if t.dtype not in _INDEX:
-        raise TypeError(f"{name} must be int32 or int64 (got {t.dtype})")
-    return t if t.is_contiguous() else t.contiguous()
-
-
-def _vector(name, t, dev, dtype, n):
-    _device_tensor(name, t, dev)
+def _result(name, t, dev, rows, width, dtype):
+    """An output matrix that the caller gave, checked, or a new one: (t, the
+    library's view of it)."""
+    if t is None:
+        t = _empty((rows, width), (width, 1), dtype=dtype, device=dev)
+        return t, _Rows(t.data_ptr(), width, _FLOAT[dtype])
+    _there(name, t, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != 1 or t.shape[0] != n:
+    if tuple(t.shape) != (rows, width):
+        raise ValueError(f"{name} must have shape {(rows, width)} (got {tuple(t.shape)})")
+    if _overlaps(t):
+        raise ValueError(f"{name} must have a unit inner stride and rows that do not overlap")
+    return t, _rows(t)
+
+
+def _ids(name, t, dev):
+    """(t contiguous, the library's code of its type)"""
+    _there(name, t, dev)
+    code = _INDEX.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be int32 or int64 (got {t.dtype})")
+    return (t if t.is_contiguous() else t.contiguous()), code
+
+
+def _vector(name, t, dev, n):
+    _there(name, t, dev)
+    if t.dtype != _F32T:
+        raise TypeError(f"{name} must be {_F32T} (got {t.dtype})")
+    if t.shape != (n,):
         raise ValueError(f"{name} must have shape ({n},) (got {tuple(t.shape)})")
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _new(n, dtype, dev):
+    return _empty((n,), (1,), dtype=dtype, device=dev)
+
+
 def _workspace(n, dev):
     # torch's blocks are aligned to 512 bytes.
-    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    return _new(n, torch.uint8, dev) if n else None
 
 
 def _ptr(t):
@@ -201,18 +224,20 @@ def _ptr(t):
 
 
 def _offsets(name, t, dev):
-    _device_tensor(name, t, dev)
-    if t.dtype != torch.int64:
+    """(t contiguous, number of segments)"""
+    _there(name, t, dev)
+    if t.dtype != _I64T:
         raise TypeError(f"{name} must be int64 (got {t.dtype})")
-    if len(t.shape) != 1 or t.shape[0] < 1:
+    shape = t.shape
+    if len(shape) != 1 or shape[0] < 1:
         raise ValueError(f"{name} must be 1-D with num_segments + 1 entries")
-    return t if t.is_contiguous() else t.contiguous()
+    return (t if t.is_contiguous() else t.contiguous()), shape[0] - 1
 
 
 def _slots(position, offsets, dev):
     """(position, offsets, tokens, k, pointer to the number of slots kept)."""
-    _device_tensor("position", position, dev)
-    if position.dtype != torch.int32:
+    _there("position", position, dev)
+    if position.dtype != _I32T:
         raise TypeError(f"position must be int32 (got {position.dtype})")
     shape = position.shape
     if len(shape) not in (1, 2):
@@ -222,23 +247,24 @@ def _slots(position, offsets, dev):
         raise ValueError("position needs at least one slot a token")
     if not position.is_contiguous():
         position = position.contiguous()
-    kept = None
-    if offsets is not None:
-        offsets = _offsets("offsets", offsets, dev)
-        kept = offsets.data_ptr() + 8 * (offsets.shape[0] - 1)
-    return position, offsets, tokens, k, kept
+    if offsets is None:
+        return position, None, tokens, k, None
+    offsets, segments = _offsets("offsets", offsets, dev)
+    return position, offsets, tokens, k, offsets.data_ptr() + 8 * segments
 
 
 def _weights(weights, dev, position, dtype):
+    """(weights contiguous, the library's code of their type)"""
     if weights is None:
-        return None, _FLOAT[torch.float32]
-    _device_tensor("weights", weights, dev)
-    if weights.dtype not in (torch.float32, dtype):
-        raise TypeError(f"weights must be float32 or {dtype} (got {weights.dtype})")
+        return None, _FLOAT[_F32T]
+    _there("weights", weights, dev)
+    wtype = weights.dtype
+    if wtype != _F32T and wtype != dtype:
+        raise TypeError(f"weights must be float32 or {dtype} (got {wtype})")
     if weights.shape != position.shape:
         raise ValueError(f"weights must have position's shape {tuple(position.shape)} "
                          f"(got {tuple(weights.shape)})")
-    return (weights if weights.is_contiguous() else weights.contiguous()), _FLOAT[weights.dtype]
+    return (weights if weights.is_contiguous() else weights.contiguous()), _FLOAT[wtype]
 
 
 @_on_its_stream
@@ -254,17 +280,17 @@ def sort_ids(ids: torch.Tensor, num_segments: int):
                 They are batched_topk's segment_offsets.
     """
     dev = _device_of("ids", ids)
-    ids = _ids("ids", ids, dev)
+    ids, code = _ids("ids", ids, dev)
     n, num_segments = ids.numel(), int(num_segments)
     if num_segments < 0:
         raise ValueError("num_segments must be >= 0")
-    order = torch.empty(n, dtype=torch.int32, device=dev)
-    position = torch.empty(ids.shape, dtype=torch.int32, device=dev)
-    offsets = torch.empty(num_segments + 1, dtype=torch.int64, device=dev)
+    order = _new(n, _I32T, dev)
+    position = torch.empty_like(ids, dtype=_I32T)
+    offsets = _new(num_segments + 1, _I64T, dev)
     need = _sort_workspace(n, num_segments)
     ws = _workspace(need, dev)
-    _call("segtopk_sort_ids", ids.data_ptr(), _INDEX[ids.dtype], n, num_segments,
-          order.data_ptr(), position.data_ptr(), offsets.data_ptr(), _ptr(ws), need, _stream(dev))
+    _call("segtopk_sort_ids", ids.data_ptr(), code, n, num_segments, order.data_ptr(),
+          position.data_ptr(), offsets.data_ptr(), _ptr(ws), need, _stream(dev))
     return order, position, offsets
 
 
@@ -280,14 +306,13 @@ def dispatch(x: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor | No
     Returns (tokens * k, width).
     """
     dev = _device_of("x", x)
-    x = _matrix("x", x, dev)
+    x, rows, width, xr = _matrix("x", x, dev)
     position, offsets, tokens, k, kept = _slots(position, offsets, dev)
-    width = x.shape[1]
-    if x.shape[0] != tokens:
-        raise ValueError(f"position is for {tokens} tokens, x has {x.shape[0]} rows")
-    out = _result("out", out, dev, (tokens * k, width), x.dtype)
-    _call("segtopk_dispatch_rows", _rows(x), _rows(out), tokens, k, width, position.data_ptr(),
-          kept, _stream(dev))
+    if rows != tokens:
+        raise ValueError(f"position is for {tokens} tokens, x has {rows} rows")
+    out, outr = _result("out", out, dev, tokens * k, width, x.dtype)
+    _call("segtopk_dispatch_rows", xr, outr, tokens, k, width, position.data_ptr(), kept,
+          _stream(dev))
     return out
 
 
@@ -303,13 +328,12 @@ def combine(rows: torch.Tensor, position: torch.Tensor, offsets: torch.Tensor | 
     """
     dev = _device_of("rows", rows)
     position, offsets, tokens, k, kept = _slots(position, offsets, dev)
-    rows = _matrix("rows", rows, dev)
-    width = rows.shape[1]
-    if rows.shape[0] != tokens * k:
-        raise ValueError(f"rows must have tokens * k = {tokens * k} rows (got {rows.shape[0]})")
-    weights, wtype = _weights(weights, dev, position, rows.dtype)
-    out = _result("out", out, dev, (tokens, width), rows.dtype)
-    _call("segtopk_combine_rows", _rows(rows), _rows(out), _ptr(weights), wtype, tokens, k, width,
+    rows, n, width, rr = _matrix("rows", rows, dev)
+    if n != tokens * k:
+        raise ValueError(f"rows must have tokens * k = {tokens * k} rows (got {n})")
+    weights, code = _weights(weights, dev, position, rows.dtype)
+    out, outr = _result("out", out, dev, tokens, width, rows.dtype)
+    _call("segtopk_combine_rows", rr, outr, _ptr(weights), code, tokens, k, width,
           position.data_ptr(), kept, _stream(dev))
     return out
 
@@ -335,20 +359,22 @@ def combine_backward(dout: torch.Tensor, rows: torch.Tensor | None, position: to
     """
     dev = _device_of("dout", dout)
     position, offsets, tokens, k, kept = _slots(position, offsets, dev)
-    dout = _matrix("dout", dout, dev)
-    width = dout.shape[1]
-    if dout.shape[0] != tokens:
-        raise ValueError(f"position is for {tokens} tokens, dout has {dout.shape[0]} rows")
-    weights, wtype = _weights(weights, dev, position, dout.dtype)
-    dweights = None
+    dout, n, width, dr = _matrix("dout", dout, dev)
+    if n != tokens:
+        raise ValueError(f"position is for {tokens} tokens, dout has {n} rows")
+    dtype = dout.dtype
+    weights, code = _weights(weights, dev, position, dtype)
+    dweights = rr = None
     if rows is not None:
-        rows = _matrix("rows", rows, dev, (tokens * k, width), dout.dtype)
-        dweights = torch.empty(position.shape, device=dev,
-                               dtype=torch.float32 if weights is None else weights.dtype)
-    out = _result("out", out, dev, (tokens * k, width), dout.dtype)
-    _call("segtopk_combine_rows_backward", _rows(dout), _rows(rows) if rows is not None else None,
-          _rows(out), _ptr(weights), _ptr(dweights), wtype, tokens, k, width,
-          position.data_ptr(), kept, _stream(dev))
+        rows, n, wide, rr = _matrix("rows", rows, dev)
+        if rows.dtype != dtype:
+            raise TypeError(f"rows must be {dtype} (got {rows.dtype})")
+        if n != tokens * k or wide != width:
+            raise ValueError(f"rows must have shape {(tokens * k, width)} (got {(n, wide)})")
+        dweights = torch.empty_like(position, dtype=_F32T if weights is None else weights.dtype)
+    out, outr = _result("out", out, dev, tokens * k, width, dtype)
+    _call("segtopk_combine_rows_backward", dr, rr, outr, _ptr(weights), _ptr(dweights), code, tokens,
+          k, width, position.data_ptr(), kept, _stream(dev))
     return out, dweights
 
 
@@ -359,12 +385,12 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
     the table.  ids: int32 or int64, any shape.  Returns ids' shape + (width,);
     ``out``, if given, is (number of ids, width) and is returned as it is."""
     dev = _device_of("table", table)
-    table = _matrix("table", table, dev)
-    ids = _ids("ids", ids, dev)
-    n, width = ids.numel(), table.shape[1]
-    res = _result("out", out, dev, (n, width), table.dtype)
-    _call("segtopk_embedding_rows", _rows(table), _rows(res), ids.data_ptr(), _INDEX[ids.dtype],
-          n, table.shape[0], width, float(scale), _stream(dev))
+    table, num_rows, width, tr = _matrix("table", table, dev)
+    ids, code = _ids("ids", ids, dev)
+    n = ids.numel()
+    res, rr = _result("out", out, dev, n, width, table.dtype)
+    _call("segtopk_embedding_rows", tr, rr, ids.data_ptr(), code, n, num_rows, width, float(scale),
+          _stream(dev))
     return res if out is not None or ids.dim() == 1 else res.view(*ids.shape, width)
 
 
@@ -384,29 +410,27 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, num_rows: int, *,
     Sums are held in 32 bits, in the order of the tokens within fixed chunks.
     """
     dev = _device_of("dout", dout)
-    ids = _ids("ids", ids, dev)
+    ids, code = _ids("ids", ids, dev)
     n, num_rows = ids.numel(), int(num_rows)
     if num_rows < 0:
         raise ValueError("num_rows must be >= 0")
     if dout.dim() != 2 and tuple(dout.shape[:-1]) == tuple(ids.shape):
         dout = dout.reshape(n, dout.shape[-1])
-    dout = _matrix("dout", dout, dev)
-    if dout.shape[0] != n:
-        raise ValueError(f"dout must have one row an id ({n}; got {dout.shape[0]})")
-    width = dout.shape[1]
+    dout, rows, width, dr = _matrix("dout", dout, dev)
+    if rows != n:
+        raise ValueError(f"dout must have one row an id ({n}; got {rows})")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if dtype is None:
         dtype = out.dtype if out is not None else dout.dtype
-    if dtype not in (dout.dtype, torch.float32):
+    if dtype != dout.dtype and dtype != _F32T:
         raise TypeError(f"the gradient must be float32 or {dout.dtype} (got {dtype})")
-    out = _result("out", out, dev, (num_rows, width), dtype)
+    out, outr = _result("out", out, dev, num_rows, width, dtype)
     need = _grad_workspace(n, num_rows, width)
     ws = _workspace(need, dev)
-    _call("segtopk_embedding_backward", _rows(dout), _rows(out), ids.data_ptr(),
-          _INDEX[ids.dtype], n, num_rows, width, float(scale),
-          -1 if padding_id is None else int(padding_id), int(bool(accumulate)), _ptr(ws), need,
-          _stream(dev))
+    _call("segtopk_embedding_backward", dr, outr, ids.data_ptr(), code, n, num_rows, width,
+          float(scale), -1 if padding_id is None else int(padding_id), int(bool(accumulate)),
+          _ptr(ws), need, _stream(dev))
     return out
 
 
@@ -414,41 +438,35 @@ def _policy(logits, token_ids, old_logp, advantages, segment_offsets, ref_logp, 
             clip_high, temperature, grad_scale, dlogits, want_grad):
     dev = _device_of("logits", logits)
     given = logits
-    logits = _matrix("logits", logits, dev)
-    tokens, vocab = logits.shape
-    token_ids = _ids("token_ids", token_ids, dev)
-    if tuple(token_ids.shape) != (tokens,):
+    logits, tokens, vocab, lr = _matrix("logits", logits, dev)
+    token_ids, code = _ids("token_ids", token_ids, dev)
+    if token_ids.shape != (tokens,):
         raise ValueError(f"token_ids must have shape ({tokens},) (got {tuple(token_ids.shape)})")
-    old_logp = _vector("old_logp", old_logp, dev, torch.float32, tokens)
-    advantages = _vector("advantages", advantages, dev, torch.float32, tokens)
+    old_logp = _vector("old_logp", old_logp, dev, tokens)
+    advantages = _vector("advantages", advantages, dev, tokens)
     if ref_logp is not None:
-        ref_logp = _vector("ref_logp", ref_logp, dev, torch.float32, tokens)
+        ref_logp = _vector("ref_logp", ref_logp, dev, tokens)
     elif kl_coef:
         raise ValueError("kl_coef needs ref_logp")
-    offsets = _offsets("segment_offsets", segment_offsets, dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    logp = torch.empty(tokens, dtype=torch.float32, device=dev)
-    a = _PolicyLossArgs()
-    a.logits = _rows(logits)
+    offsets, segments = _offsets("segment_offsets", segment_offsets, dev)
+    loss = _empty((), (), dtype=_F32T, device=dev)
+    logp = _new(tokens, _F32T, dev)
+    dr = _NO_ROWS
     if want_grad:
         if dlogits is given:
             if logits is not given:
                 raise ValueError("dlogits may be the logits only where these have a unit inner "
                                  "stride and rows that do not overlap")
+            dr = lr
         else:
-            dlogits = _result("dlogits", dlogits, dev, (tokens, vocab), logits.dtype)
-        a.dlogits = _rows(dlogits)
-    a.token_ids, a.id_type = token_ids.data_ptr(), _INDEX[token_ids.dtype]
-    a.clip_low, a.clip_high, a.kl_coef = float(clip_low), float(clip_high), float(kl_coef)
-    a.temperature, a.grad_scale = float(temperature), float(grad_scale)
-    a.tokens, a.vocab, a.num_segments = tokens, vocab, offsets.shape[0] - 1
-    a.segment_offsets = offsets.data_ptr()
-    a.old_logp, a.ref_logp = old_logp.data_ptr(), _ptr(ref_logp)
-    a.advantages = advantages.data_ptr()
-    a.loss, a.logp = loss.data_ptr(), logp.data_ptr()
-    need = _loss_workspace(tokens, vocab, offsets.shape[0] - 1)
+            dlogits, dr = _result("dlogits", dlogits, dev, tokens, vocab, logits.dtype)
+    a = _PolicyLossArgs(lr, dr, token_ids.data_ptr(), code, clip_low, clip_high, kl_coef,
+                        temperature, grad_scale, tokens, vocab, segments, offsets.data_ptr(),
+                        old_logp.data_ptr(), _ptr(ref_logp), advantages.data_ptr(),
+                        loss.data_ptr(), logp.data_ptr())
+    need = _loss_workspace(tokens, vocab, segments)
     ws = _workspace(need, dev)
-    _call("segtopk_policy_loss", ctypes.byref(a), _ptr(ws), need, _stream(dev))
+    _call("segtopk_policy_loss", a, _ptr(ws), need, _stream(dev))
     return loss, logp, dlogits
 
 
