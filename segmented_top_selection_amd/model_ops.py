@@ -115,10 +115,8 @@ def _on_its_stream(fn):
     """Runs fn on the device of its first tensor and on the stream asked for."""
     @functools.wraps(fn)
     def wrapped(first, *args, stream=None, **kw):
-        if not isinstance(first, _Tensor) or (stream is None and
-                                              first.get_device() == _current_device()):
-            return fn(first, *args, **kw)
-        if first.is_cuda:
+        if isinstance(first, _Tensor) and first.is_cuda and (
+                stream is not None or first.get_device() != _current_device()):
             if stream is not None and stream.device != first.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors are on {first.device}")
             with torch.cuda.device(first.device), torch.cuda.stream(stream):
