@@ -11,7 +11,9 @@
 // ranks equal digits by the lanes below (one ballot a bit) and the wave's own
 // counters in LDS; the counters of the 16 waves, summed digit by digit, then
 // say where each wave's items of a digit start.
-//   block_sort_kernel  a block in one pass, which is up to 511 segments
+//   block_sort_kernel  a block in one pass, which is up to 511 segments (8000 ids
+//                      9.5 us; 7.5 by the two launches below, of which each costs
+//                      the host 2.2 to 2.8)
 //   count_kernel       more items or passes: the digit histogram of each chunk,
 //   scatter_kernel     and the pass itself, every workgroup adding up the
 //                      histograms of the chunks before its own
@@ -30,8 +32,7 @@ constexpr int kItems = 8;  // of a lane
 constexpr uint32_t kBlock = kSortThreads * kItems;
 constexpr int kMaxBits = 9;
 constexpr uint32_t kMaxBins = 1u << kMaxBits;
-constexpr int64_t kMinChunk = 2048;
-constexpr int64_t kMaxChunks = 128;
+constexpr int64_t kMinChunk = 1024;
 
 struct SortArgs {
     const void *ids;       // first pass: the caller's ids
@@ -66,25 +67,35 @@ struct Items {
 // Counts the wave's items by digit in `mine` (zero before), and ranks each among
 // those before it in the wave.
 __device__ inline void rank_items(Items &x, uint32_t shift, uint32_t bits, uint32_t *mine) {
-    const uint32_t lane = threadIdx.x & 63u, mask = (1u << bits) - 1u;
+    const uint32_t mask = (1u << bits) - 1u;
+    uint32_t below[kItems], peers[kItems];  // lanes of the same digit: those below, all
+#pragma unroll
+    for (int r = 0; r < kItems; ++r) {
+        if ((uint32_t)r >= x.items) break;
+        const uint32_t digit = (x.key[r] >> shift) & mask;
+        const uint64_t live = __ballot(x.live(r));
+        uint32_t lo = (uint32_t)live, hi = (uint32_t)(live >> 32);
+#pragma unroll
+        for (int j = 0; j < kMaxBits; ++j) {  // bits past the digit's are all zero
+            const uint32_t bit = 0u - ((digit >> j) & 1u);
+            const uint64_t ones = __ballot(bit != 0u);
+            lo &= ~((uint32_t)ones ^ bit);
+            hi &= ~((uint32_t)(ones >> 32) ^ bit);
+        }
+        below[r] = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0u));
+        peers[r] = (uint32_t)(__popc(lo) + __popc(hi));
+    }
     volatile uint32_t *const next = mine;
 #pragma unroll
     for (int r = 0; r < kItems; ++r) {
         if ((uint32_t)r >= x.items) break;
-        const bool live = x.live(r);
         const uint32_t digit = (x.key[r] >> shift) & mask;
-        uint64_t peers = __ballot(live);
-        for (uint32_t j = 0; j < bits; ++j) {
-            const uint64_t ones = __ballot((digit >> j) & 1u);
-            peers &= ((digit >> j) & 1u) ? ones : ~ones;
-        }
-        const uint32_t below = (uint32_t)__popcll(peers & ((1ull << lane) - 1ull));
         uint32_t before = 0;
-        if (live) before = next[digit];
+        if (x.live(r)) before = next[digit];
         __builtin_amdgcn_wave_barrier();
-        if (live && below == 0) next[digit] = before + (uint32_t)__popcll(peers);
+        if (x.live(r) && below[r] == 0) next[digit] = before + peers[r];
         __builtin_amdgcn_wave_barrier();
-        x.rank[r] = before + below;
+        x.rank[r] = before + below[r];
     }
 }
 
@@ -145,9 +156,18 @@ __global__ __launch_bounds__(kSortThreads) void block_sort_kernel(SortArgs a) {
         if (!x.live(r)) continue;
         const uint32_t at = whist[w * a.bins + x.key[r]] + x.rank[r];
         if (a.key_out) a.key_out[at] = x.key[r];
-        if (a.slot_out) a.slot_out[at] = x.at(r);
         if (a.position) a.position[x.at(r)] = (int32_t)at;
+        x.rank[r] = at;
     }
+    if (!a.slot_out) return;
+    // The order, in the counters' place: stored from there it takes a line a wave.
+    static_assert(kSortWaves * kMaxBins >= kBlock, "room for a block");
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kItems; ++r)
+        if (x.live(r)) whist[x.rank[r]] = x.at(r);
+    __syncthreads();
+    for (uint32_t i = t; i < a.n; i += kSortThreads) a.slot_out[i] = whist[i];
 }
 
 template <bool FIRST>
@@ -189,11 +209,18 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
         const uint32_t d = t & (width - 1u), groups = kSortThreads / width;
         if (d < a.bins) {
             uint32_t all = 0, mine = 0;
-#pragma unroll 8
-            for (uint32_t c = t / width; c < a.chunks; c += groups) {
-                const uint32_t v = a.hist[(size_t)c * a.bins + d];
-                all += v;
-                mine += c < blockIdx.x ? v : 0u;
+            for (uint32_t c0 = t / width; c0 < a.chunks; c0 += 8u * groups) {
+                uint32_t v[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8u; ++j) {
+                    const uint32_t c = c0 + j * groups;
+                    v[j] = c < a.chunks ? a.hist[(size_t)c * a.bins + d] : 0u;
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < 8u; ++j) {
+                    all += v[j];
+                    mine += c0 + j * groups < blockIdx.x ? v[j] : 0u;
+                }
             }
             atomicAdd(&total[d], all);  // integers: any order gives the same sum
             atomicAdd(&before[d], mine);
@@ -323,10 +350,12 @@ SortPlan sort_plan(int64_t n, int64_t segments) {
         return p;
     }
     // One block, or chunks of whole blocks (of part of one, where there are few
-    // items): few enough for a workgroup to add up all their histograms.
+    // items): few enough for a workgroup to add up all their histograms, and more
+    // once that is little next to a chunk.
     int64_t chunk = kBlock;
     if (n > kBlock) {
-        chunk = (n + kMaxChunks - 1) / kMaxChunks;
+        chunk = (n + 127) / 128;
+        if (chunk > kBlock) chunk = (n + 255) / 256 > kBlock ? (n + 255) / 256 : kBlock;
         if (chunk < kMinChunk) chunk = kMinChunk;
         const int64_t unit = chunk > kBlock ? kBlock : kSortThreads;
         chunk = (chunk + unit - 1) / unit * unit;
