@@ -1,9 +1,10 @@
 """Builds the HIP library libsegtopk.so for gfx950 with hipcc (in-tree).
 
-Every source under csrc/ (the host code and one kernel unit per key type) is
-compiled to an object in parallel, then the objects are linked into one
-shared library.  Objects go to a build folder beside the sources.  The
-benchmark's stream-read probe (probe/stream_read.hip) is built alongside as
+Every HIP source under csrc/ (the host code, one kernel unit per key type, and
+the operators around the selection) is compiled to an object in parallel, then
+the objects are linked into one shared library.  Objects go to a build folder
+beside the sources.  The operators' binding for torch tensors (csrc/binding.cpp)
+is host code, built by g++ as the extension module _binding.so.  The benchmark's stream-read probe (probe/stream_read.hip) is built alongside as
 libsegtopk_probe.so; the top-k library does not use it.
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsegtopk.so")
 PROBE_SRC = os.path.join(HERE, "probe", "stream_read.hip")
 PROBE_LIB = os.path.join(HERE, "probe", "libsegtopk_probe.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_LIB = os.path.join(HERE, "_binding.so")
 ARCH = os.environ.get("SEGTOPK_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
@@ -35,6 +39,19 @@ def sources() -> list:
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
+def binding_command(out: str) -> list:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", os.path.join(ROOT, "include"),
+            "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
+            BINDING_SRC, "-o", out, "-L", os.path.join(base, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -43,6 +60,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     cmds = [[hipcc, *HIPCC_FLAGS, "-c", s, "-o", o] for s, o in zip(srcs, objs)]
     # The benchmark's stream-read probe: a library of its own.
     cmds.append([hipcc, *HIPCC_FLAGS, "-shared", PROBE_SRC, "-o", PROBE_LIB])
+    cmds.append(binding_command(BINDING_LIB + ".tmp"))
     if verbose:
         for c in cmds:
             print(" ".join(c), flush=True)
@@ -62,6 +80,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         print(" ".join(link), flush=True)
     subprocess.check_call(link)
     os.replace(tmp, LIB)
+    os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
     return LIB
 
 
