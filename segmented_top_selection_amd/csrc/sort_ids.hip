@@ -2,25 +2,24 @@
 // order = stable argsort of key_i, where key_i = id_i inside [0, S) and S
 // otherwise; position = its inverse; offsets[s] = #{i : key_i < s}.
 //
-// Few ids among many segments, an embedding's tokens:
-//   rank_kernel        counts for each item those before it, n^2 comparisons spread
-//                      over the device
-// Otherwise least-significant-digit radix passes of at most 9 bits, by workgroups
-// of 16 waves.  A block of up to 8192 items stays in registers, eight to a lane,
-// each wave holding consecutive items.  A wave takes its items 64 at a time and
-// ranks equal digits by the lanes below (one ballot a bit) and the wave's own
-// counters in LDS; the counters of the 16 waves, summed digit by digit, then
-// say where each wave's items of a digit start.
-//   block_sort_kernel  a block in one pass, which is up to 511 segments (8000 ids
-//                      9.5 us; 7.5 by the two launches below, of which each costs
-//                      the host 2.2 to 2.8)
-//   count_kernel       more items or passes: the digit histogram of each chunk,
-//   scatter_kernel     and the pass itself, every workgroup adding up the
-//                      histograms of the chunks before its own
-// No atomic decides an order, so results are the same every time.
+// Few ids:
+//   rank_kernel     counts for each item those before it, n^2 comparisons spread
+//                   over the device
+// More: least-significant-digit radix passes of at most 9 bits, by workgroups of
+// 16 waves.  A block of up to 8192 items stays in registers, eight to a lane, each
+// wave holding consecutive items.  A wave takes its items 64 at a time and ranks
+// equal digits by the lanes below (one ballot a bit) and the wave's own counters in
+// LDS; the counters of the 16 waves, summed digit by digit, then say where each
+// wave's items of a digit start.
+//   count_kernel    the digit histogram of each chunk,
+//   scatter_kernel  and the pass itself, every workgroup adding up the histograms
+//                   of the chunks before its own
+// Up to 511 segments take one pass, up to 262143 two.  No atomic decides an order,
+// so results are the same every time.
 //
 // Bound by launches and by the latency of the dependent steps, not by its
-// bytes (16 to 20 an item).
+// bytes (16 to 20 an item): 512 ids among 64 segments take 3.0 us, 8000 among 128
+// 8.5, 65536 among 128 8.8, 32768 among 131072 25.7, a million among 256 26.
 #include "ops_common.h"
 
 namespace segtopk_ops {
@@ -127,49 +126,6 @@ __device__ inline uint32_t wave_starts(uint32_t *whist, uint32_t bins, uint32_t 
     return base;
 }
 
-__global__ __launch_bounds__(kSortThreads) void block_sort_kernel(SortArgs a) {
-    __shared__ uint32_t whist[kSortWaves * kMaxBins], wave_total[kSortWaves];
-    if (blockIdx.x) return clear(a.fill, blockIdx.x - 1u, gridDim.x - 1u);
-    const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
-    Items x;
-    x.items = (a.n + kSortThreads - 1) / kSortThreads;
-    x.first = w * 64u * x.items + lane;
-    x.count = a.n;
-#pragma unroll
-    for (int r = 0; r < kItems; ++r) x.key[r] = x.live(r) ? sort_key<true>(a, x.at(r)) : 0u;
-    for (uint32_t i = t; i < kSortWaves * a.bins; i += kSortThreads) whist[i] = 0u;
-    __syncthreads();
-    rank_items(x, 0, a.bits, whist + w * a.bins);
-    __syncthreads();
-    uint32_t own = 0;
-    if (t < a.bins)
-#pragma unroll
-        for (uint32_t i = 0; i < kSortWaves; ++i) own += whist[i * a.bins + t];
-    const uint32_t base = digit_prefix(own, wave_total);
-    if (t < a.bins) {
-        if (a.offsets) a.offsets[t] = base;  // bins = segments + 1
-        wave_starts(whist, a.bins, t, base);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kItems; ++r) {
-        if (!x.live(r)) continue;
-        const uint32_t at = whist[w * a.bins + x.key[r]] + x.rank[r];
-        if (a.key_out) a.key_out[at] = x.key[r];
-        if (a.position) a.position[x.at(r)] = (int32_t)at;
-        x.rank[r] = at;
-    }
-    if (!a.slot_out) return;
-    // The order, in the counters' place: stored from there it takes a line a wave.
-    static_assert(kSortWaves * kMaxBins >= kBlock, "room for a block");
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kItems; ++r)
-        if (x.live(r)) whist[x.rank[r]] = x.at(r);
-    __syncthreads();
-    for (uint32_t i = t; i < a.n; i += kSortThreads) a.slot_out[i] = whist[i];
-}
-
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void count_kernel(SortArgs a) {
     __shared__ uint32_t cnt[kMaxBins];
@@ -261,12 +217,18 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
 
 // The place of an item is the number of items that go before it: those of a
 // smaller key, and of the same key before it.  A workgroup places 32 items, each
-// by 32 threads that go over n / 32 keys each.
+// by 32 threads that go over n / 32 keys each.  Further workgroups place the
+// segments' borders in the same way: before offsets[s] go the keys below s.
 constexpr uint32_t kRankItems = 32;
 constexpr uint32_t kRankParts = kSortThreads / kRankItems;
 // Keys that a thread goes over: whole blocks of 32.
 __host__ __device__ inline uint32_t rank_part(uint32_t n) {
     return (n + kSortThreads - 1u) / kSortThreads * kRankItems;
+}
+
+// Workgroups that place items: one at least.
+__host__ __device__ inline uint32_t rank_groups(uint32_t n) {
+    return n ? (n + kRankItems - 1u) / kRankItems : 1u;
 }
 
 __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
@@ -281,12 +243,14 @@ __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
     if (t < kRankItems) place[t] = 0u;
     __syncthreads();
     const uint32_t item = first + t % kRankItems, part = t / kRankItems;
-    const uint32_t mine = item < a.n ? twice[item] : 0u;
+    const uint32_t items = rank_groups(a.n) * kRankItems;
+    const bool borders = first >= items;
+    const uint32_t mine = borders ? 2u * (item - items) : item < a.n ? twice[item] : 0u;
     uint32_t before = 0;
     // A block of 32 keys lies before, at, or past the workgroup's items.  Before
     // them equal keys count: 2 key_j < 2 key_i + 1.
     for (uint32_t b = part * per; b < (part + 1u) * per; b += kRankItems) {
-        const uint32_t limit = mine + (b < first ? 1u : 0u);
+        const uint32_t limit = mine + (b < first && !borders ? 1u : 0u);
 #pragma unroll
         for (uint32_t j = 0; j < kRankItems / 4; ++j) {
             const uint4 k = staged[b / 4 + j];
@@ -295,11 +259,14 @@ __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
     }
     // Of the workgroup's own items, one each.
     const uint32_t other = first + part;
-    before += other < item && twice[other] == mine;
+    if (!borders) before += other < item && twice[other] == mine;
     atomicAdd(&place[t % kRankItems], before);  // integers: any order gives the same sum
     __syncthreads();
-    if (t < kRankItems && item < a.n) {
-        const uint32_t at = place[t];
+    if (t >= kRankItems) return;
+    const uint32_t at = place[t];
+    if (borders) {
+        if (item - items <= a.segments) a.offsets[item - items] = at;
+    } else if (item < a.n) {
         if (a.key_out) a.key_out[at] = mine / 2u;
         if (a.slot_out) a.slot_out[at] = item;
         if (a.position) a.position[item] = (int32_t)at;
@@ -320,7 +287,7 @@ __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segm
     offsets[s] = lo;
 }
 
-constexpr int64_t kMaxRanked = 15360;
+constexpr int64_t kMaxRanked = 12288, kMaxRankedOnePass = 8192, kManyBorders = 4096;
 
 struct SortPlan {
     bool ranked;  // by rank_kernel
@@ -343,29 +310,26 @@ SortPlan sort_plan(int64_t n, int64_t segments) {
         p.bits = (bits + p.passes - 1) / p.passes;
         p.bins = 1u << p.bits;
     }
-    p.ranked = p.passes > 1 && n <= kMaxRanked;
+    p.ranked = n <= (p.passes > 1 ? kMaxRanked : kMaxRankedOnePass);
     if (p.ranked) {
-        p.chunks = n ? (uint32_t)((n + kRankItems - 1) / kRankItems) : 1u;
-        p.pair_bytes = p.bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
+        p.chunks = rank_groups((uint32_t)n);
+        p.pair_bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
+        p.bytes = p.passes > 1 ? p.pair_bytes : 0;
         return p;
     }
-    // One block, or chunks of whole blocks (of part of one, where there are few
-    // items): few enough for a workgroup to add up all their histograms, and more
-    // once that is little next to a chunk.
-    int64_t chunk = kBlock;
-    if (n > kBlock) {
-        chunk = (n + 127) / 128;
-        if (chunk > kBlock) chunk = (n + 255) / 256 > kBlock ? (n + 255) / 256 : kBlock;
-        if (chunk < kMinChunk) chunk = kMinChunk;
-        const int64_t unit = chunk > kBlock ? kBlock : kSortThreads;
-        chunk = (chunk + unit - 1) / unit * unit;
-    }
+    // Chunks of whole blocks (of part of one, where there are few items): few enough
+    // for a workgroup to add up all their histograms, and more once that is little
+    // next to a chunk.
+    int64_t chunk = (n + 127) / 128;
+    if (chunk > kBlock) chunk = (n + 255) / 256 > kBlock ? (n + 255) / 256 : kBlock;
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    const int64_t unit = chunk > kBlock ? kBlock : kSortThreads;
+    chunk = (chunk + unit - 1) / unit * unit;
     p.chunk = (uint32_t)chunk;
-    p.chunks = n ? (uint32_t)((n + chunk - 1) / chunk) : 1u;
-    p.hist_bytes = p.chunks > 1 ? ((size_t)p.chunks * p.bins * 4 + 255) & ~(size_t)255 : 0;
+    p.chunks = (uint32_t)((n + chunk - 1) / chunk);
+    p.hist_bytes = ((size_t)p.chunks * p.bins * 4 + 255) & ~(size_t)255;
     // Of a sort in several passes, the keys in order, where offsets are searched;
-    // and of one in several chunks, keys and slots between the passes, in two
-    // buffers taken in turn.
+    // and keys and slots between the passes, in two buffers taken in turn.
     p.pair_bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
     p.bytes = p.hist_bytes + (p.passes > 1 ? 5 : 0) * p.pair_bytes;
     return p;
@@ -392,13 +356,14 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
     a.n = (uint32_t)n;
     a.segments = (uint32_t)segments;
     a.chunk = p.chunk;
-    a.chunks = p.chunks;
     a.bins = p.bins;
     a.bits = (uint32_t)p.bits;
     a.wide = id_type == SEGTOPK_KEY_I64;
-    a.offsets = p.passes == 1 ? offsets : nullptr;
+    const bool borders = p.ranked && offsets && segments < kManyBorders;
+    a.chunks = p.chunks + (borders ? (uint32_t)(segments / kRankItems + 1) : 0u);
+    a.offsets = borders || p.passes == 1 ? offsets : nullptr;
     const Fill whole = fill ? *fill : Fill{};
-    const uint64_t launches = p.ranked || p.chunks == 1 ? 1 : 2 * p.passes;
+    const uint64_t launches = p.ranked ? 1 : 2 * p.passes;
     const uint64_t share = ((whole.bytes + launches - 1) / launches + 15) & ~(uint64_t)15;
     uint64_t filled = 0;
     hipError_t err = hipSuccess;
@@ -408,20 +373,18 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
         a.fill.data = static_cast<char *>(whole.data) + filled;
         a.fill.bytes = left < share ? left : share;
         filled += a.fill.bytes;
-        hipLaunchKernelGGL(kernel, dim3(p.chunks + fill_blocks(a.fill, kSortThreads)),
+        hipLaunchKernelGGL(kernel, dim3(a.chunks + fill_blocks(a.fill, kSortThreads)),
                            dim3(kSortThreads), lds, stream, a);
         err = hipGetLastError();
         return err == hipSuccess;
     };
-    if (p.ranked || p.chunks == 1) {
+    if (p.ranked) {
         a.key_out = sorted;
         a.slot_out = reinterpret_cast<uint32_t *>(order);
         a.position = position;
-        if (p.ranked ? !launch(rank_kernel, (size_t)rank_part(a.n) * kRankParts * 4)
-                     : !launch(block_sort_kernel, 0))
-            return err;
+        if (!launch(rank_kernel, (size_t)rank_part(a.n) * kRankParts * 4)) return err;
     }
-    for (int i = 0; !p.ranked && p.chunks > 1 && i < p.passes; ++i) {
+    for (int i = 0; !p.ranked && i < p.passes; ++i) {
         const bool last = i == p.passes - 1;
         a.shift = (uint32_t)(i * p.bits);
         a.key_in = i ? pair[(i - 1) & 1][0] : nullptr;
@@ -432,7 +395,7 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
         if (!launch(i ? count_kernel<false> : count_kernel<true>, 0)) return err;
         if (!launch(i ? scatter_kernel<false> : scatter_kernel<true>, 0)) return err;
     }
-    if (p.passes > 1 && offsets) {
+    if (offsets && !a.offsets) {
         hipLaunchKernelGGL(offsets_kernel, dim3((unsigned)((segments + 256) / 256)), dim3(256), 0,
                            stream, sorted, (uint32_t)n, (uint32_t)segments, offsets);
         if ((err = hipGetLastError()) != hipSuccess) return err;

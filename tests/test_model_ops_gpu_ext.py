@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("segments", [128, 511, 512, 30000])
-@pytest.mark.parametrize("n", [31, 32, 33, 1024, 4095, 4096, 4097, 9001, 15359, 15360, 15361, 131073])
+@pytest.mark.parametrize("n", [31, 32, 33, 1024, 4096, 9001, 12287, 12288, 12289, 15361, 131073])
 def test_sort_ids_where_its_launches_change(n, segments):
     ids = torch.randint(-1, segments + 1, (n,), generator=gen(n + segments), device=DEV)
     check_sort(ids, segments)
