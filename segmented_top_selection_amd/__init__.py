@@ -8,8 +8,8 @@ selection runs in the library's HIP kernels; there is no other code path, and
 the binding raises if the library is missing.
 
 The operators around the selection (expert sort, dispatch and combine, embedding
-rows, policy loss, and their gradients) are bound the same way in
-``model_ops`` and reached from here.
+rows, policy loss, and their gradients) are bound in ``model_ops``, through a
+compiled module, and reached from here.
 """
 from __future__ import annotations
 

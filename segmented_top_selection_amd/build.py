@@ -1,10 +1,11 @@
 """Builds the HIP library libsegtopk.so for gfx950 with hipcc (in-tree).
 
-Every HIP source under csrc/ (the host code, one kernel unit per key type, and
-the operators around the selection) is compiled to an object in parallel, then
-the objects are linked into one shared library.  Objects go to a build folder
-beside the sources.  The operators' binding for torch tensors (csrc/binding.cpp)
-is host code, built by g++ as the extension module _binding.so.  The benchmark's stream-read probe (probe/stream_read.hip) is built alongside as
+Every HIP source under csrc/ (the host code and one kernel unit per key type) and
+csrc_ops/ (the operators around the selection) is compiled to an object in
+parallel, then the objects are linked into one shared library.  Objects go to a
+build folder beside the sources.  The operators' binding for torch tensors
+(csrc_ops/binding.cpp) is host code, built by g++ as the extension module
+_binding.so.  The benchmark's stream-read probe (probe/stream_read.hip) is built alongside as
 libsegtopk_probe.so; the top-k library does not use it.
 """
 from __future__ import annotations
@@ -18,11 +19,13 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+# Apart from the selection's sources, which the benchmark's traffic figures are tied to.
+CSRC_OPS = os.path.join(HERE, "csrc_ops")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsegtopk.so")
 PROBE_SRC = os.path.join(HERE, "probe", "stream_read.hip")
 PROBE_LIB = os.path.join(HERE, "probe", "libsegtopk_probe.so")
-BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_SRC = os.path.join(CSRC_OPS, "binding.cpp")
 BINDING_LIB = os.path.join(HERE, "_binding.so")
 ARCH = os.environ.get("SEGTOPK_OFFLOAD_ARCH", "gfx950")
 
@@ -36,7 +39,7 @@ HIPCC_FLAGS = [
 
 
 def sources() -> list:
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + sorted(glob.glob(os.path.join(CSRC_OPS, "*.hip")))
 
 
 def binding_command(out: str) -> list:

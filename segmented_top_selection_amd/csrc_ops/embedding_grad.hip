@@ -12,7 +12,11 @@
 //   finish_kernel  adds the partial rows of a run, chunk by chunk
 // Every sum has one fixed order: results are the same every time.
 //
-// Bound by writing the table, most of whose rows are zeros, and reading dout.
+// Bound by writing the table, most of whose rows are zeros, and reading dout:
+// 32768 tokens, 131072 x 4096 bf16 take 268 us (1.34 GB, 5.0 TB/s): sort and
+// clearing 188, sums 71, finish 8.  Looking up which rows to clear, in sum_kernel,
+// took as long.  Of 5003 tokens, 4099 x 1001 f32, the launches' latency is most:
+// 8.7 + 7.5 + 5.4 us.
 #include "ops_common.h"
 
 namespace segtopk_ops {

@@ -22,7 +22,13 @@
 // The terms of a loss cancel, so each has to be better than the plain 32 bits
 // that its size suggests: exponents are taken from the row's maximum, with the
 // factor log2(e) / temperature in two parts, and everything after the sum, once a
-// row, is in 64 bits.
+// row, is in 64 bits (relative error of the loss of drawn cases 2e-9 to 1e-7;
+// wholly in 32 bits up to 1e-5).
+//
+// Bound by memory where rows are many: 4096 x 131072 bf16 with its gradient, a
+// quarter of the rows left out, take 367 us, 5.1 TB/s of what has to be read and
+// written; by latency where they are few: 96 x 32003 f16 9.2 us, of which the
+// arrival takes 1 and the 64 bits 0.4.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>

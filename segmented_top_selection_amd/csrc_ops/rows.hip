@@ -16,7 +16,15 @@
 // a thread holds one 16-byte piece of it, so a token's row is read once for
 // its k copies (dispatch) or k gradients (combine backward), and a sum over k
 // rows stays in registers (32 bits).  Pieces past the last whole one are
-// single elements, one to a thread.
+// single elements, one to a thread.  What is read once, and outputs of 128 MiB or
+// more, go past the caches: left there they are written back while the next
+// kernel reads (sort, dispatch and combine of 8192 tokens x 8 x 4096 bf16 263 us,
+// so 216; a kernel that reads the rows right after loses 2%).
+//
+// 8192 tokens x 8 x 4096 bf16: dispatch 103 us (5.9 TB/s of what it reads and
+// writes), combine 104 (5.8), its gradient 217 (5.2); a 4 GiB copy reaches 4.7.
+// Lookup of 32768 rows of 4096 bf16: 60 us with the table's rows in the last
+// cache, 77 without.
 #include <type_traits>
 
 #include "ops_common.h"

@@ -287,6 +287,11 @@ __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segm
     offsets[s] = lo;
 }
 
+// Counting against radix passes: among 128 segments (one pass) 5000 ids take 6.1 us
+// against 7.4, 8000 8.5 against 7.5 but in one launch, of which each costs the host
+// 2.2 to 2.8, 9000 13.5 against 7.8; among 40000 (two passes) 9000 take 18.4 against
+// 22.3, 14000 25.2 against 22.5.  Borders past so many are searched in the sorted
+// keys, in a launch of their own.
 constexpr int64_t kMaxRanked = 12288, kMaxRankedOnePass = 8192, kManyBorders = 4096;
 
 struct SortPlan {

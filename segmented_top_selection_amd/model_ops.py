@@ -8,7 +8,7 @@ sampled tokens under the model's logits.  The gradients are calls of their own
 (``*_backward``, ``policy_loss_grad``); none of them records an autograd graph.
 
 Like ``batched_topk`` these only marshal arguments, in ``_binding`` (built from
-csrc/binding.cpp): tensor metadata is checked before anything is queued, outputs
+csrc_ops/binding.cpp): tensor metadata is checked before anything is queued, outputs
 not given and workspaces are allocated with torch, and the work runs in the
 library's HIP kernels, on ``stream`` or the current stream.  With ``stream``
 given, what is allocated or copied here belongs to that stream too; inputs made
