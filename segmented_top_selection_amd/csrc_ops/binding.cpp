@@ -242,9 +242,13 @@ Workspace workspace(int64_t bytes, at::Device dev) {
     return w;
 }
 
-hipStream_t stream_of(at::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
-
-void check(int status, const char *name) {
+// Runs f, which returns a status, without the interpreter's lock: a launch waits
+// where the device's queue is full.
+template <class F> void call(const char *name, at::Device dev, F f) {
+    const hipStream_t stream = c10::hip::getCurrentHIPStream(dev.index()).stream();
+    PyThreadState *const state = PyEval_SaveThread();
+    const int status = f(stream);  // throws nothing
+    PyEval_RestoreThread(state);
     if (status == SEGTOPK_OK) return;
     PyObject *e = PyObject_CallFunction(call_error, "is", status, name);
     if (e) {
@@ -291,12 +295,13 @@ PyObject *sort_ids(PyObject *const *a) {
     const Tensor position = fresh(ids.t.sizes(), ScalarType::Int, dev);
     const Tensor offsets = fresh({segments + 1}, ScalarType::Long, dev);
     const Workspace ws = workspace(lib.sort_ids_workspace(n, segments), dev);
-    check(lib.sort_ids(ids.t.data_ptr(), ids.code, n, segments,
-                       static_cast<int32_t *>(order.data_ptr()),
-                       static_cast<int32_t *>(position.data_ptr()),
-                       static_cast<int64_t *>(offsets.data_ptr()), ws.data, ws.bytes,
-                       stream_of(dev)),
-          "segtopk_sort_ids");
+    const void *const in = ids.t.data_ptr();
+    int32_t *const o = static_cast<int32_t *>(order.data_ptr());
+    int32_t *const p = static_cast<int32_t *>(position.data_ptr());
+    int64_t *const f = static_cast<int64_t *>(offsets.data_ptr());
+    call("segtopk_sort_ids", dev, [&](hipStream_t stream) {
+        return lib.sort_ids(in, ids.code, n, segments, o, p, f, ws.data, ws.bytes, stream);
+    });
     return tuple(THPVariable_Wrap(order), THPVariable_Wrap(position), THPVariable_Wrap(offsets));
 }
 
@@ -309,8 +314,9 @@ PyObject *dispatch(PyObject *const *a) {
     TORCH_CHECK_VALUE(x.rows == s.tokens, "position is for ", s.tokens, " tokens, x has ", x.rows,
                       " rows");
     const Matrix out = result("out", a[3], dev, s.tokens * s.k, x.width, x.t.scalar_type());
-    check(lib.dispatch_rows(&x.v, &out.v, s.tokens, s.k, x.width, s.at, s.kept, stream_of(dev)),
-          "segtopk_dispatch_rows");
+    call("segtopk_dispatch_rows", dev, [&](hipStream_t stream) {
+        return lib.dispatch_rows(&x.v, &out.v, s.tokens, s.k, x.width, s.at, s.kept, stream);
+    });
     return output(a[3], out.t);
 }
 
@@ -325,9 +331,10 @@ PyObject *combine(PyObject *const *a) {
     const ScalarType type = rows.t.scalar_type();
     const Weights w = weights_of(a[3], dev, s.position, type);
     const Matrix out = result("out", a[4], dev, s.tokens, rows.width, type);
-    check(lib.combine_rows(&rows.v, &out.v, w.data, w.code, s.tokens, s.k, rows.width, s.at, s.kept,
-                           stream_of(dev)),
-          "segtopk_combine_rows");
+    call("segtopk_combine_rows", dev, [&](hipStream_t stream) {
+        return lib.combine_rows(&rows.v, &out.v, w.data, w.code, s.tokens, s.k, rows.width, s.at,
+                                s.kept, stream);
+    });
     return output(a[4], out.t);
 }
 
@@ -354,10 +361,11 @@ PyObject *combine_backward(PyObject *const *a) {
         dweights = fresh(s.position.sizes(), w.data ? w.t.scalar_type() : ScalarType::Float, dev);
     }
     const Matrix out = result("out", a[5], dev, s.tokens * s.k, dout.width, type);
-    check(lib.combine_rows_backward(&dout.v, both ? &rows.v : nullptr, &out.v, w.data,
-                                    both ? dweights.data_ptr() : nullptr, w.code, s.tokens, s.k,
-                                    dout.width, s.at, s.kept, stream_of(dev)),
-          "segtopk_combine_rows_backward");
+    void *const dw = both ? dweights.data_ptr() : nullptr;
+    call("segtopk_combine_rows_backward", dev, [&](hipStream_t stream) {
+        return lib.combine_rows_backward(&dout.v, both ? &rows.v : nullptr, &out.v, w.data, dw,
+                                         w.code, s.tokens, s.k, dout.width, s.at, s.kept, stream);
+    });
     return tuple(output(a[5], out.t), both ? THPVariable_Wrap(dweights) : same(Py_None));
 }
 
@@ -367,12 +375,14 @@ PyObject *embedding(PyObject *const *a) {
     const c10::DeviceGuard guard(dev);
     const Matrix table = matrix("table", given_table);
     const Ids ids = ids_of("ids", there("ids", a[1], dev));
-    const double scale = real(a[2]);
+    const float scale = static_cast<float>(real(a[2]));
     const int64_t n = ids.t.numel();
     const Matrix out = result("out", a[3], dev, n, table.width, table.t.scalar_type());
-    check(lib.embedding_rows(&table.v, &out.v, ids.t.data_ptr(), ids.code, n, table.rows,
-                             table.width, static_cast<float>(scale), stream_of(dev)),
-          "segtopk_embedding_rows");
+    const void *const in = ids.t.data_ptr();
+    call("segtopk_embedding_rows", dev, [&](hipStream_t stream) {
+        return lib.embedding_rows(&table.v, &out.v, in, ids.code, n, table.rows, table.width, scale,
+                                  stream);
+    });
     if (given(a[3]) || ids.t.dim() == 1) return output(a[3], out.t);
     auto shape = ids.t.sizes().vec();
     shape.push_back(table.width);
@@ -390,6 +400,8 @@ PyObject *embedding_backward(PyObject *const *a) {
                       given_dout.sizes().slice(0, given_dout.dim() - 1) == ids.t.sizes();
     const Matrix dout = matrix("dout", deep ? given_dout.reshape({n, given_dout.size(-1)}) : given_dout);
     TORCH_CHECK_VALUE(dout.rows == n, "dout must have one row an id (", n, "; got ", dout.rows, ")");
+    const float scale = static_cast<float>(real(a[3]));
+    const int64_t padding = given(a[4]) ? integer(a[4]) : -1;
     const int accumulate = PyObject_IsTrue(a[7]);
     if (accumulate < 0) throw python_error();
     TORCH_CHECK_VALUE(!accumulate || given(a[6]), "accumulate needs out");
@@ -405,10 +417,11 @@ PyObject *embedding_backward(PyObject *const *a) {
                      type_name(type), ")");
     const Matrix out = result("out", a[6], dev, num_rows, dout.width, type);
     const Workspace ws = workspace(lib.embedding_backward_workspace(n, num_rows, dout.width), dev);
-    check(lib.embedding_backward(&dout.v, &out.v, ids.t.data_ptr(), ids.code, n, num_rows, dout.width,
-                                 static_cast<float>(real(a[3])), given(a[4]) ? integer(a[4]) : -1,
-                                 accumulate, ws.data, ws.bytes, stream_of(dev)),
-          "segtopk_embedding_backward");
+    const void *const in = ids.t.data_ptr();
+    call("segtopk_embedding_backward", dev, [&](hipStream_t stream) {
+        return lib.embedding_backward(&dout.v, &out.v, in, ids.code, n, num_rows, dout.width, scale,
+                                      padding, accumulate, ws.data, ws.bytes, stream);
+    });
     return output(a[6], out.t);
 }
 
@@ -461,7 +474,8 @@ PyObject *policy_loss(PyObject *const *a) {
     q.loss = static_cast<float *>(loss.data_ptr());
     q.logp = static_cast<float *>(logp.data_ptr());
     const Workspace ws = workspace(lib.policy_loss_workspace(q.tokens, q.vocab, q.num_segments), dev);
-    check(lib.policy_loss(&q, ws.data, ws.bytes, stream_of(dev)), "segtopk_policy_loss");
+    call("segtopk_policy_loss", dev,
+         [&](hipStream_t stream) { return lib.policy_loss(&q, ws.data, ws.bytes, stream); });
     if (!gradient) return tuple(THPVariable_Wrap(loss), THPVariable_Wrap(logp));
     return tuple(THPVariable_Wrap(loss), THPVariable_Wrap(logp), output(a[11], dlogits.t));
 }

@@ -57,6 +57,7 @@ __device__ inline int64_t token_of(const void *ids, uint32_t wide, uint32_t t) {
 }
 
 constexpr uint32_t kCountThreads = 1024;
+constexpr int64_t kCountBlocks = 1 << 16;  // of a launch; further answers in turn
 
 // Rows arrive at one of 64 counters, and the last row of each at the counter
 // before them: additions to one word follow each other 14 ns apart, which took
@@ -76,33 +77,35 @@ __global__ __launch_bounds__(kCountThreads) void count_kernel(const void *ids, u
         const int64_t v = offsets[s];
         return (uint32_t)(v < 0 ? 0 : v > (int64_t)tokens ? (int64_t)tokens : v);
     };
-    const uint32_t s = blockIdx.x;
-    const uint32_t b = segments ? at(s) : tokens, e = segments ? at(s + 1) : tokens;
-    if (threadIdx.x == 0) total = 0u;
-    if (s == 0 && threadIdx.x <= kCounters) arrived[threadIdx.x * kCounterWords] = 0u;
-    __syncthreads();
-    uint32_t n = 0;
-    for (uint32_t t0 = b + threadIdx.x; t0 < e; t0 += 4u * kCountThreads) {
-        int64_t y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t t = t0 + j * kCountThreads;
-            y[j] = t < e ? token_of(ids, wide, t) : -1;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) n += y[j] >= 0 && y[j] < (int64_t)vocab;
-    }
-    if (n) atomicAdd(&total, n);
-    __syncthreads();
-    n = total;
-    for (uint32_t t = b + threadIdx.x; t < e; t += kCountThreads) {
-        const int64_t y = token_of(ids, wide, t);
-        live[t] = y >= 0 && y < (int64_t)vocab ? n : 0u;
-    }
-    if (s == 0)
+    const auto named = [&](int64_t y) { return y >= 0 && y < (int64_t)vocab; };
+    if (blockIdx.x == 0) {  // the counters, and the rows outside every answer
+        if (threadIdx.x <= kCounters) arrived[threadIdx.x * kCounterWords] = 0u;
+        const uint32_t b = segments ? at(0) : tokens, e = segments ? at(segments) : tokens;
         for (uint32_t t = threadIdx.x; t < b; t += kCountThreads) live[t] = 0u;
-    if (segments && s == segments - 1)
         for (uint32_t t = e + threadIdx.x; t < tokens; t += kCountThreads) live[t] = 0u;
+    }
+    for (uint32_t s = blockIdx.x; s < segments; s += gridDim.x) {
+        const uint32_t b = at(s), e = at(s + 1);
+        if (threadIdx.x == 0) total = 0u;
+        __syncthreads();
+        uint32_t n = 0;
+        for (uint32_t t0 = b + threadIdx.x; t0 < e; t0 += 4u * kCountThreads) {
+            int64_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t t = t0 + j * kCountThreads;
+                y[j] = t < e ? token_of(ids, wide, t) : -1;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n += named(y[j]);
+        }
+        if (n) atomicAdd(&total, n);
+        __syncthreads();
+        n = total;
+        for (uint32_t t = b + threadIdx.x; t < e; t += kCountThreads)
+            live[t] = named(token_of(ids, wide, t)) ? n : 0u;
+        __syncthreads();
+    }
 }
 
 constexpr double kLog2e = 1.44269504088896340736;
@@ -379,7 +382,8 @@ extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *w
     a.factor = (float)factor;
     if ((double)a.factor >= factor) a.factor = std::nextafter(a.factor, 0.0f);
     a.rest = std::fmax((float)(factor - (double)a.factor), FLT_MIN);
-    hipLaunchKernelGGL(count_kernel, dim3(q.num_segments ? (unsigned)q.num_segments : 1u),
+    const int64_t groups = q.num_segments < kCountBlocks ? q.num_segments : kCountBlocks;
+    hipLaunchKernelGGL(count_kernel, dim3(groups ? (unsigned)groups : 1u),
                        dim3(kCountThreads), 0, stream, q.token_ids, a.wide, a.tokens, a.vocab,
                        q.segment_offsets, (uint32_t)q.num_segments, live, a.arrived);
     if (hipGetLastError() != hipSuccess) return SEGTOPK_HIP_ERROR;

@@ -245,15 +245,15 @@ __global__ __launch_bounds__(kOpThreads) void combine_backward_kernel(
 
 // A group of threads takes ROWS rows, so that a thread has that many loads in
 // flight.
-template <class T, class I, int ROWS, bool STREAM>
-__global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restrict__ table,
+template <class T, class I, int ROWS, bool STREAM, int THREADS>
+__global__ __launch_bounds__(THREADS) void embedding_kernel(const T *__restrict__ table,
                                                                int64_t ts, T *__restrict__ out,
                                                                int64_t os,
                                                                const I *__restrict__ ids,
                                                                uint32_t n, int64_t num_rows,
                                                                float scale, Cut c) {
     using P = Piece<T>;
-    const uint32_t per = kOpThreads / c.lanes;
+    const uint32_t per = (uint32_t)THREADS / c.lanes;
     for (uint32_t i0 = blockIdx.x * per * ROWS + threadIdx.x / c.lanes; i0 < n;
          i0 += gridDim.x * per * ROWS) {
         int64_t id[ROWS];  // -1: a row of zeros
@@ -293,27 +293,27 @@ __global__ __launch_bounds__(kOpThreads) void embedding_kernel(const T *__restri
 
 constexpr int64_t kManyPieces = 4 * 256 * 2048;  // four for each thread that 256 CUs hold
 
-Cut cut_of(int64_t width, int elem_bytes) {
+Cut cut_of(int64_t width, int elem_bytes, uint32_t threads = kOpThreads) {
     const int64_t n = 16 / elem_bytes;
     Cut c;
     c.pieces = (uint32_t)(width / n);
     c.units = (uint32_t)(width / n + width % n);
     c.lanes = 8;
-    while (c.lanes < (uint32_t)kOpThreads && c.lanes < c.units) c.lanes <<= 1;
+    while (c.lanes < threads && c.lanes < c.units) c.lanes <<= 1;
     return c;
 }
 
 // A launch holds fewer than 2^32 threads in a direction; the kernels loop over
 // the tokens that are left.
-unsigned blocks_of(int64_t tokens, const Cut &c) {
-    const int64_t per = kOpThreads / c.lanes, most = 1 << 22;
+unsigned blocks_of(int64_t tokens, const Cut &c, uint32_t threads = kOpThreads) {
+    const int64_t per = threads / c.lanes, most = ((int64_t)1 << 30) / threads;
     const int64_t n = (tokens + per - 1) / per;
     return (unsigned)(n < most ? n : most);
 }
 
-dim3 grid_of(int64_t tokens, const Cut &c) {
+dim3 grid_of(int64_t tokens, const Cut &c, uint32_t threads = kOpThreads) {
     const uint32_t y = (c.units + c.lanes - 1) / c.lanes;
-    return dim3(blocks_of(tokens, c), y < 65535u ? y : 65535u);
+    return dim3(blocks_of(tokens, c, threads), y < 65535u ? y : 65535u);
 }
 
 bool good_slots(int64_t tokens, int64_t k, int64_t width, const int32_t *position,
@@ -455,27 +455,33 @@ extern "C" int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_r
         return SEGTOPK_INVALID_ARGUMENT;
     return with_type(out->type, [&](auto t) {
         using T = decltype(t);
-        const Cut c = cut_of(width, sizeof(T));
-        // Four rows a thread once there is work for every wave the device holds.
-        const bool many = n * c.units >= kManyPieces;
-        const dim3 grid = grid_of(many ? (n + 3) / 4 : n, c);
-        const auto go = [&](auto i, auto rows) {
-            using I = decltype(i);
-            constexpr int kRows = decltype(rows)::value;
-            const bool past = kRows > 1 && streams(n * width * (int64_t)sizeof(T));
-            hipLaunchKernelGGL((past ? embedding_kernel<T, I, kRows, (kRows > 1)>
-                                     : embedding_kernel<T, I, kRows, false>),
-                               grid, dim3(kOpThreads), 0, stream,
-                               static_cast<const T *>(num_rows ? table->data : nullptr),
-                               num_rows ? table->stride : 0, static_cast<T *>(out->data),
-                               out->stride, static_cast<const I *>(ids), (uint32_t)n, num_rows,
-                               scale, c);
+        const int64_t units = cut_of(width, sizeof(T)).units;
+        const auto go = [&](auto i, auto rows, auto past, auto threads) {
+            constexpr int kRows = decltype(rows)::value, kThreads = decltype(threads)::value;
+            const Cut c = cut_of(width, sizeof(T), kThreads);
+            hipLaunchKernelGGL(
+                (embedding_kernel<T, decltype(i), kRows, decltype(past)::value, kThreads>),
+                grid_of((n + kRows - 1) / kRows, c, kThreads), dim3(kThreads), 0, stream,
+                static_cast<const T *>(num_rows ? table->data : nullptr),
+                num_rows ? table->stride : 0, static_cast<T *>(out->data), out->stride,
+                static_cast<const decltype(i) *>(ids), (uint32_t)n, num_rows, scale, c);
             return status(hipGetLastError());
         };
-        const auto by_rows = [&](auto i) {
-            return many ? go(i, std::integral_constant<int, 4>{})
-                        : go(i, std::integral_constant<int, 1>{});
+        const auto by_size = [&](auto i) {
+            using One = std::integral_constant<int, 1>;
+            using Four = std::integral_constant<int, 4>;
+            using Small = std::integral_constant<int, kOpThreads>;
+            using Large = std::integral_constant<int, 1024>;
+            // Four rows a thread once there is work for every wave the device holds.
+            if (n * units < kManyPieces) return go(i, One{}, std::false_type{}, Small{});
+            // Whole wide rows by one workgroup: 32768 x 4096 bf16 72 us, by two 77.
+            const bool wide = units > kOpThreads;
+            if (!streams(n * width * (int64_t)sizeof(T)))
+                return wide ? go(i, Four{}, std::false_type{}, Large{})
+                            : go(i, Four{}, std::false_type{}, Small{});
+            return wide ? go(i, Four{}, std::true_type{}, Large{})
+                        : go(i, Four{}, std::true_type{}, Small{});
         };
-        return id_type == SEGTOPK_KEY_I64 ? by_rows(int64_t{}) : by_rows(int32_t{});
+        return id_type == SEGTOPK_KEY_I64 ? by_size(int64_t{}) : by_size(int32_t{});
     });
 }

@@ -89,7 +89,7 @@ def test_policy_rows_where_the_workgroup_changes(kib, dtype):
             assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T,S", [(63, 5), (64, 1), (65, 64), (128, 2), (129, 7), (5003, 1), (5003, 4000)])
+@pytest.mark.parametrize("T,S", [(63, 5), (64, 1), (65, 64), (128, 2), (129, 7), (5003, 1), (5003, 4000), (129, 70000)])
 def test_policy_loss_of_many_rows(T, S):
     # Terms of both signs that nearly cancel.  A row's log-probability is off by its
     # sum's error alone, relative: 20 additions deep, a product, its exponent's error
