@@ -23,8 +23,7 @@
 //
 // 8192 tokens x 8 x 4096 bf16: dispatch 103 us (5.9 TB/s of what it reads and
 // writes), combine 104 (5.8), its gradient 217 (5.2); a 4 GiB copy reaches 4.7.
-// Lookup of 32768 rows of 4096 bf16: 60 us with the table's rows in the last
-// cache, 77 without.
+// Lookup of 32768 rows of 4096 bf16, new rows each time: 70 us (5.1 TB/s).
 #include <type_traits>
 
 #include "ops_common.h"

@@ -13,7 +13,7 @@ not given and workspaces are allocated with torch, and the work runs in the
 library's HIP kernels, on ``stream`` or the current stream.  With ``stream``
 given, what is allocated or copied here belongs to that stream too; inputs made
 on another one must be ready for it, as for any torch call under
-``torch.cuda.stream``.  Matrices need a unit stride along their rows' elements and
+``torch.cuda.stream``, and are kept until that stream has used them.  Matrices need a unit stride along their rows' elements and
 non-overlapping rows; others are copied first.  All calls may be captured into a
 graph.
 """
@@ -26,6 +26,7 @@ import torch
 from . import LIB_PATH, SegTopKError, library
 
 
+# The C interface for callers with raw pointers: `entry` gives its functions.
 class _Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("type", ctypes.c_int32)]
 
@@ -99,7 +100,12 @@ def _on(stream, name, *args):
         if stream.device != first.device:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {first.device}")
         with torch.cuda.stream(stream):
-            return getattr(_native, name)(*args)
+            out = getattr(_native, name)(*args)
+        # What the caller may free before that stream has come to it.
+        for t in args:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        return out
     return getattr(_native, name)(*args)
 
 

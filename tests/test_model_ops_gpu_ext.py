@@ -156,3 +156,23 @@ def test_a_graph_of_the_calls_in_several_launches():
         kept = [v.clone() for v in outs]
         assert same_bits(calls(new), kept)
         torch.cuda.synchronize()
+
+
+def test_inputs_freed_before_their_stream_has_used_them():
+    g = gen(60)
+    side = torch.cuda.Stream()
+    table = randn(g, 700, 129)
+    want = table.clone()
+    ids = torch.arange(700, device=DEV).flip(0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20000000)
+    got = st.embedding(table, ids, stream=side)
+    del table, ids
+    for _ in range(4):  # would be given the same memory
+        torch.full((700, 129), -1.0, device=DEV)
+        torch.zeros(700, dtype=torch.int64, device=DEV)
+    side.synchronize()
+    assert torch.equal(got, want.flip(0))
+    with pytest.raises(ValueError):
+        st.embedding(want.cpu(), torch.zeros(3, dtype=torch.int64), stream=side)
