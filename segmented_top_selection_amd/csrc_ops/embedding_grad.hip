@@ -217,14 +217,12 @@ template <class T, class O>
 hipError_t queue_grad(const segtopk_rows *dout, const segtopk_rows *dtable, const GradArgs &a,
                       hipStream_t stream) {
     O *table = static_cast<O *>(dtable->data);
-    hipLaunchKernelGGL((sum_kernel<T, O>), dim3(a.chunks * a.cols), dim3(kOpThreads), 0, stream,
-                       static_cast<const T *>(dout->data), table, a);
-    const hipError_t err = hipGetLastError();
+    const hipError_t err = launch(sum_kernel<T, O>, dim3(a.chunks * a.cols), kOpThreads, stream, 0,
+                                  static_cast<const T *>(dout->data), table, a);
     if (err != hipSuccess || a.chunks < 2) return err;
     const int64_t y = (a.width + 255) / 256;
-    hipLaunchKernelGGL(finish_kernel<O>, dim3(a.chunks - 1, (unsigned)(y < 64 ? y : 64)),
-                       dim3(kOpThreads), 0, stream, table, a);
-    return hipGetLastError();
+    return launch(finish_kernel<O>, dim3(a.chunks - 1, (unsigned)(y < 64 ? y : 64)), kOpThreads,
+                  stream, 0, table, a);
 }
 
 bool good_sizes(int64_t n, int64_t num_rows, int64_t width) {
@@ -275,10 +273,9 @@ extern "C" int segtopk_embedding_backward(const segtopk_rows *dout, const segtop
         const unsigned grid = (unsigned)(num_rows < kFillBlocks ? num_rows : kFillBlocks);
         const int st = with_type(dtable->type, [&](auto o) {
             using O = decltype(o);
-            hipLaunchKernelGGL(clear_kernel<O>, dim3(grid), dim3(kOpThreads), 0, stream,
-                               static_cast<O *>(dtable->data), (uint32_t)num_rows, width,
-                               dtable->stride);
-            return status(hipGetLastError());
+            return status(launch(clear_kernel<O>, dim3(grid), kOpThreads, stream, 0,
+                                 static_cast<O *>(dtable->data), (uint32_t)num_rows, width,
+                                 dtable->stride));
         });
         if (st != SEGTOPK_OK) return st;
     }

@@ -350,8 +350,7 @@ extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *w
     if (workspace_bytes < 0 || (size_t)workspace_bytes < need) return SEGTOPK_SCRATCH_TOO_SMALL;
 
     if (!q.tokens) {
-        hipLaunchKernelGGL(no_rows_kernel, dim3(1), dim3(1), 0, stream, q.loss);
-        return status(hipGetLastError());
+        return status(launch(no_rows_kernel, dim3(1), 1, stream, 0, q.loss));
     }
     LossArgs a{};
     a.stride = q.logits.stride;
@@ -383,20 +382,20 @@ extern "C" int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *w
     if ((double)a.factor >= factor) a.factor = std::nextafter(a.factor, 0.0f);
     a.rest = std::fmax((float)(factor - (double)a.factor), FLT_MIN);
     const int64_t groups = q.num_segments < kCountBlocks ? q.num_segments : kCountBlocks;
-    hipLaunchKernelGGL(count_kernel, dim3(groups ? (unsigned)groups : 1u),
-                       dim3(kCountThreads), 0, stream, q.token_ids, a.wide, a.tokens, a.vocab,
-                       q.segment_offsets, (uint32_t)q.num_segments, live, a.arrived);
-    if (hipGetLastError() != hipSuccess) return SEGTOPK_HIP_ERROR;
+    if (launch(count_kernel, dim3(groups ? (unsigned)groups : 1u), kCountThreads, stream, 0,
+               q.token_ids, a.wide, a.tokens, a.vocab, q.segment_offsets, (uint32_t)q.num_segments,
+               live, a.arrived) != hipSuccess)
+        return SEGTOPK_HIP_ERROR;
     return with_type(q.logits.type, [&](auto v) {
         using T = decltype(v);
         const T *in = static_cast<const T *>(q.logits.data);
         T *out = static_cast<T *>(q.dlogits.data);
         const auto go = [&](auto with_grad, auto stream_stores, auto threads) {
             constexpr int kThreads = decltype(threads)::value;
-            hipLaunchKernelGGL(
-                (row_kernel<T, decltype(with_grad)::value, decltype(stream_stores)::value, kThreads>),
-                dim3(a.tokens), dim3(kThreads), 0, stream, in, out, a);
-            return status(hipGetLastError());
+            constexpr bool kGrad = decltype(with_grad)::value;
+            constexpr bool kStream = decltype(stream_stores)::value;
+            return status(launch(row_kernel<T, kGrad, kStream, kThreads>, dim3(a.tokens), kThreads,
+                                 stream, 0, in, out, a));
         };
         const auto by_length = [&](auto with_grad, auto stream_stores) {
             // The smallest workgroup that holds a row in registers.  4096 rows of

@@ -350,11 +350,10 @@ extern "C" int segtopk_dispatch_rows(const segtopk_rows *x, const segtopk_rows *
         using T = decltype(t);
         const Cut c = cut_of(width, sizeof(T));
         const auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid_of(tokens, c), dim3(kOpThreads), 0, stream,
-                               static_cast<const T *>(x->data), x->stride,
-                               static_cast<T *>(rows->data), rows->stride,
-                               slots_of(tokens, k, position, kept), c);
-            return status(hipGetLastError());
+            return status(launch(kernel, grid_of(tokens, c), kOpThreads, stream, 0,
+                                 static_cast<const T *>(x->data), x->stride,
+                                 static_cast<T *>(rows->data), rows->stride,
+                                 slots_of(tokens, k, position, kept), c));
         };
         if (c.lanes < 64u) return go(dispatch_kernel<T, false, false>);
         return streams(tokens * k * width * (int64_t)sizeof(T)) ? go(dispatch_kernel<T, true, true>)
@@ -374,22 +373,21 @@ extern "C" int segtopk_combine_rows(const segtopk_rows *rows, const segtopk_rows
     return with_type(rows->type, [&](auto t) {
         using T = decltype(t);
         const Cut c = cut_of(width, sizeof(T));
-        const auto launch = [&](auto kernel, auto w) {
-            hipLaunchKernelGGL(kernel, grid_of(tokens, c), dim3(kOpThreads), 0, stream,
-                               static_cast<const T *>(rows->data), rows->stride,
-                               static_cast<T *>(out->data), out->stride,
-                               static_cast<const decltype(w) *>(weights),
-                               slots_of(tokens, k, position, kept), c);
-            return status(hipGetLastError());
+        const auto with = [&](auto kernel, auto w) {
+            return status(launch(kernel, grid_of(tokens, c), kOpThreads, stream, 0,
+                                 static_cast<const T *>(rows->data), rows->stride,
+                                 static_cast<T *>(out->data), out->stride,
+                                 static_cast<const decltype(w) *>(weights),
+                                 slots_of(tokens, k, position, kept), c));
         };
         const auto go = [&](auto w) {
             using W = decltype(w);
             const bool one = c.lanes >= 64u;
             if (k <= kFewSlots)
-                return one ? launch(combine_kernel<T, W, true, kFewSlots>, w)
-                           : launch(combine_kernel<T, W, false, kFewSlots>, w);
-            return one ? launch(combine_kernel<T, W, true, kSlotsAtOnce>, w)
-                       : launch(combine_kernel<T, W, false, kSlotsAtOnce>, w);
+                return one ? with(combine_kernel<T, W, true, kFewSlots>, w)
+                           : with(combine_kernel<T, W, false, kFewSlots>, w);
+            return one ? with(combine_kernel<T, W, true, kSlotsAtOnce>, w)
+                       : with(combine_kernel<T, W, false, kSlotsAtOnce>, w);
         };
         return weights && weight_type != SEGTOPK_KEY_F32 ? go(t) : go(float{});
     });
@@ -418,23 +416,22 @@ extern "C" int segtopk_combine_rows_backward(const segtopk_rows *dout, const seg
         const bool wide = c.units > 256u || (c.units > 128u && tokens < 2048);
         c.lanes = wide ? (uint32_t)kOpThreads : 64u;
         const bool past = streams(tokens * k * width * (int64_t)sizeof(T));
-        const auto launch = [&](auto kernel, auto w) {
+        const auto with = [&](auto kernel, auto w) {
             using W = decltype(w);
-            hipLaunchKernelGGL(kernel, dim3(blocks_of(tokens, c)), dim3(kOpThreads), 0, stream,
-                               static_cast<const T *>(dout->data), dout->stride,
-                               static_cast<const T *>(rows ? rows->data : nullptr),
-                               rows ? rows->stride : 0, static_cast<T *>(drows->data),
-                               drows->stride, static_cast<const W *>(weights),
-                               static_cast<W *>(dweights), slots_of(tokens, k, position, kept), c);
-            return status(hipGetLastError());
+            return status(launch(kernel, dim3(blocks_of(tokens, c)), kOpThreads, stream, 0,
+                                 static_cast<const T *>(dout->data), dout->stride,
+                                 static_cast<const T *>(rows ? rows->data : nullptr),
+                                 rows ? rows->stride : 0, static_cast<T *>(drows->data),
+                                 drows->stride, static_cast<const W *>(weights),
+                                 static_cast<W *>(dweights), slots_of(tokens, k, position, kept), c));
         };
         const auto go = [&](auto w) {
             using W = decltype(w);
             if (k <= kFewSlots)
-                return past ? launch(combine_backward_kernel<T, W, true, kFewSlots>, w)
-                            : launch(combine_backward_kernel<T, W, false, kFewSlots>, w);
-            return past ? launch(combine_backward_kernel<T, W, true, kSlotsAtOnce>, w)
-                        : launch(combine_backward_kernel<T, W, false, kSlotsAtOnce>, w);
+                return past ? with(combine_backward_kernel<T, W, true, kFewSlots>, w)
+                            : with(combine_backward_kernel<T, W, false, kFewSlots>, w);
+            return past ? with(combine_backward_kernel<T, W, true, kSlotsAtOnce>, w)
+                        : with(combine_backward_kernel<T, W, false, kSlotsAtOnce>, w);
         };
         return (weights || dweights) && weight_type != SEGTOPK_KEY_F32 ? go(t) : go(float{});
     });
@@ -458,13 +455,12 @@ extern "C" int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_r
         const auto go = [&](auto i, auto rows, auto past, auto threads) {
             constexpr int kRows = decltype(rows)::value, kThreads = decltype(threads)::value;
             const Cut c = cut_of(width, sizeof(T), kThreads);
-            hipLaunchKernelGGL(
-                (embedding_kernel<T, decltype(i), kRows, decltype(past)::value, kThreads>),
-                grid_of((n + kRows - 1) / kRows, c, kThreads), dim3(kThreads), 0, stream,
+            return status(launch(
+                embedding_kernel<T, decltype(i), kRows, decltype(past)::value, kThreads>,
+                grid_of((n + kRows - 1) / kRows, c, kThreads), kThreads, stream, 0,
                 static_cast<const T *>(num_rows ? table->data : nullptr),
                 num_rows ? table->stride : 0, static_cast<T *>(out->data), out->stride,
-                static_cast<const decltype(i) *>(ids), (uint32_t)n, num_rows, scale, c);
-            return status(hipGetLastError());
+                static_cast<const decltype(i) *>(ids), (uint32_t)n, num_rows, scale, c));
         };
         const auto by_size = [&](auto i) {
             using One = std::integral_constant<int, 1>;

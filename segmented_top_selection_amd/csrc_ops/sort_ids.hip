@@ -40,7 +40,7 @@ struct SortArgs {
     uint32_t *key_out;     // nullptr: not wanted
     uint32_t *slot_out;
     int32_t *position;     // last pass, or nullptr
-    int64_t *offsets;      // of a sort in one pass, or nullptr
+    int64_t *offsets;      // or nullptr: searched in the sorted keys afterwards
     uint32_t *hist;        // [chunks][bins]
     uint32_t n, segments, chunk, chunks, shift, bins, bits;
     uint32_t wide;         // ids of 64 bits
@@ -372,22 +372,21 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
     const uint64_t share = ((whole.bytes + launches - 1) / launches + 15) & ~(uint64_t)15;
     uint64_t filled = 0;
     hipError_t err = hipSuccess;
-    const auto launch = [&](auto kernel, size_t lds) {
+    const auto queue = [&](auto kernel, size_t lds) {
         const uint64_t left = whole.bytes - filled;
         a.fill = whole;
         a.fill.data = static_cast<char *>(whole.data) + filled;
         a.fill.bytes = left < share ? left : share;
         filled += a.fill.bytes;
-        hipLaunchKernelGGL(kernel, dim3(a.chunks + fill_blocks(a.fill, kSortThreads)),
-                           dim3(kSortThreads), lds, stream, a);
-        err = hipGetLastError();
+        err = launch(kernel, dim3(a.chunks + fill_blocks(a.fill, kSortThreads)), kSortThreads,
+                     stream, lds, a);
         return err == hipSuccess;
     };
     if (p.ranked) {
         a.key_out = sorted;
         a.slot_out = reinterpret_cast<uint32_t *>(order);
         a.position = position;
-        if (!launch(rank_kernel, (size_t)rank_part(a.n) * kRankParts * 4)) return err;
+        if (!queue(rank_kernel, (size_t)rank_part(a.n) * kRankParts * 4)) return err;
     }
     for (int i = 0; !p.ranked && i < p.passes; ++i) {
         const bool last = i == p.passes - 1;
@@ -397,14 +396,12 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
         a.key_out = last ? sorted : pair[i & 1][0];
         a.slot_out = last ? reinterpret_cast<uint32_t *>(order) : pair[i & 1][1];
         a.position = last ? position : nullptr;
-        if (!launch(i ? count_kernel<false> : count_kernel<true>, 0)) return err;
-        if (!launch(i ? scatter_kernel<false> : scatter_kernel<true>, 0)) return err;
+        if (!queue(i ? count_kernel<false> : count_kernel<true>, 0)) return err;
+        if (!queue(i ? scatter_kernel<false> : scatter_kernel<true>, 0)) return err;
     }
-    if (offsets && !a.offsets) {
-        hipLaunchKernelGGL(offsets_kernel, dim3((unsigned)((segments + 256) / 256)), dim3(256), 0,
-                           stream, sorted, (uint32_t)n, (uint32_t)segments, offsets);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-    }
+    if (offsets && !a.offsets)
+        return launch(offsets_kernel, dim3((unsigned)((segments + 256) / 256)), 256, stream, 0,
+                      sorted, (uint32_t)n, (uint32_t)segments, offsets);
     return hipSuccess;
 }
 
