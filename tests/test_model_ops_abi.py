@@ -114,8 +114,10 @@ def test_embedding_matrix_refusals_and_empty_calls():
         assert embed(out=bad) == embed_grad(dout=bad) == INVALID
     assert embed(n=0) == OK and embed_grad(num_rows=0) == OK
     need = mo.entry("segtopk_embedding_backward_workspace")
-    assert embed_grad(ws=None) == embed_grad(ws=WS + 4) == INVALID
-    assert embed_grad(ws_bytes=need(10, 5, 64) - 1) == TOO_SMALL
+    assert need(10, 5, 64) == 0  # one launch
+    assert embed_grad(n=3000, ws=None) == embed_grad(n=3000, ws=WS + 4) == INVALID
+    assert embed_grad(n=3000, ws_bytes=need(3000, 5, 64) - 1) == TOO_SMALL
+    assert embed_grad(ws_bytes=-1) == TOO_SMALL
     assert need(-1, 5, 64) == need(10, -5, 64) == need(10, 5, 0) == 0
     # More work than one launch holds.
     assert embed_grad(n=2 ** 30, ws_bytes=2 ** 62) == NOT_SUPPORTED

@@ -176,3 +176,32 @@ def test_inputs_freed_before_their_stream_has_used_them():
     assert torch.equal(got, want.flip(0))
     with pytest.raises(ValueError):
         st.embedding(want.cpu(), torch.zeros(3, dtype=torch.int64), stream=side)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("n,num_rows,width", [
+    (2, 1, 1), (7, 100, 513), (255, 3, 64), (256, 2, 65), (257, 900, 7), (1024, 30, 512),
+    (1024, 5, 1024), (1024, 3, 1025), (1025, 40, 100), (128, 9, 8191), (1, 70000, 5), (600, 1, 40)])
+def test_embedding_backward_of_few_tokens(n, num_rows, width, dtype):
+    g = gen(n + width)
+    for what in ("random", "same", "ends"):
+        ids = torch.randint(-1, num_rows + 1, (n,), generator=g, device=DEV)
+        if what == "same":
+            ids[:] = num_rows - 1
+        elif what == "ends":  # an id's first and last token far apart
+            ids[[0, -1]] = num_rows // 2
+        dout = randn(g, n, width, dtype=dtype)
+        for padding in (None, 0):
+            exact, inner, touched = exact_table(dout, ids, num_rows, padding)
+            out = torch.full((num_rows, width + 3), 5.0, dtype=dtype, device=DEV)
+            got = st.embedding_backward(dout, ids, num_rows, padding_id=padding, out=out[:, 1:-2])
+            close(got, exact, inner)
+            assert not bool(got[~touched].any())
+            assert bool((out[:, :1] == 5).all()) and bool((out[:, -2:] == 5).all())
+            assert torch.equal(got, st.embedding_backward(dout, ids.int(), num_rows, padding_id=padding))
+            base = randn(g, num_rows, width)
+            res = st.embedding_backward(dout, ids, num_rows, padding_id=padding, out=base.clone(),
+                                        accumulate=True)
+            assert torch.equal(res[~touched], base[~touched])
+            total = exact + base.double()
+            close(res, total, inner + U * (total.abs() + exact.abs()))
