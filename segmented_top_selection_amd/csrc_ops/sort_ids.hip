@@ -18,8 +18,8 @@
 // so results are the same every time.
 //
 // Bound by launches and by the latency of the dependent steps, not by its
-// bytes (16 to 20 an item): 512 ids among 64 segments take 3.0 us, 8000 among 128
-// 8.5, 65536 among 128 8.8, 32768 among 131072 25.7, a million among 256 26.
+// bytes (16 to 20 an item): 512 ids among 64 segments take 2.7 us, 8000 among 128
+// 8.8, 65536 among 128 8.8, 32768 among 131072 25.7, a million among 256 26.
 #include "ops_common.h"
 
 namespace segtopk_ops {
@@ -216,12 +216,13 @@ __global__ __launch_bounds__(kSortThreads) void scatter_kernel(SortArgs a) {
 }
 
 // The place of an item is the number of items that go before it: those of a
-// smaller key, and of the same key before it.  A workgroup places 32 items, each
-// by 32 threads that go over n / 32 keys each.  Further workgroups place the
+// smaller key, and of the same key before it.  A workgroup places 16 items, each
+// by 64 threads that go over n / 64 keys each (3000 ids 3.8 us; 32 items to a
+// workgroup leave CUs idle, 4.6).  Further workgroups place the
 // segments' borders in the same way: before offsets[s] go the keys below s.
-constexpr uint32_t kRankItems = 32;
+constexpr uint32_t kRankItems = 16;
 constexpr uint32_t kRankParts = kSortThreads / kRankItems;
-// Keys that a thread goes over: whole blocks of 32.
+// Keys that a thread goes over: whole blocks of 16.
 __host__ __device__ inline uint32_t rank_part(uint32_t n) {
     return (n + kSortThreads - 1u) / kSortThreads * kRankItems;
 }
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
     const bool borders = first >= items;
     const uint32_t mine = borders ? 2u * (item - items) : item < a.n ? twice[item] : 0u;
     uint32_t before = 0;
-    // A block of 32 keys lies before, at, or past the workgroup's items.  Before
+    // A block of 16 keys lies before, at, or past the workgroup's items.  Before
     // them equal keys count: 2 key_j < 2 key_i + 1.
     for (uint32_t b = part * per; b < (part + 1u) * per; b += kRankItems) {
         const uint32_t limit = mine + (b < first && !borders ? 1u : 0u);
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
     }
     // Of the workgroup's own items, one each.
     const uint32_t other = first + part;
-    if (!borders) before += other < item && twice[other] == mine;
+    if (!borders && part < kRankItems) before += other < item && twice[other] == mine;
     atomicAdd(&place[t % kRankItems], before);  // integers: any order gives the same sum
     __syncthreads();
     if (t >= kRankItems) return;
@@ -288,8 +289,8 @@ __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segm
 }
 
 // Counting against radix passes: among 128 segments (one pass) 5000 ids take 6.1 us
-// against 7.4, 8000 8.5 against 7.5 but in one launch, of which each costs the host
-// 2.2 to 2.8, 9000 13.5 against 7.8; among 40000 (two passes) 9000 take 18.4 against
+// against 7.4, 8000 8.8 against 7.5 but in one launch, of which each costs the host
+// 2.2 to 2.8, 9000 13.5 against 7.8; among 40000 (two passes) 9000 take 18.0 against
 // 22.3, 14000 25.2 against 22.5.  Borders past so many are searched in the sorted
 // keys, in a launch of their own.
 constexpr int64_t kMaxRanked = 12288, kMaxRankedOnePass = 8192, kManyBorders = 4096;
