@@ -39,7 +39,7 @@ HIPCC_FLAGS = [
 
 
 def sources() -> list:
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + sorted(glob.glob(os.path.join(CSRC_OPS, "*.hip")))
+    return [s for folder in (CSRC, CSRC_OPS) for s in sorted(glob.glob(os.path.join(folder, "*.hip")))]
 
 
 def binding_command(out: str) -> list:

@@ -22,7 +22,7 @@
 // The terms of a loss cancel, so each has to be better than the plain 32 bits
 // that its size suggests: exponents are taken from the row's maximum, with the
 // factor log2(e) / temperature in two parts, and everything after the sum, once a
-// row, is in 64 bits (relative error of the loss of drawn cases 2e-9 to 1e-7;
+// row, is in 64 bits (relative error of the loss on random cases 2e-9 to 1e-7;
 // wholly in 32 bits up to 1e-5).
 //
 // Bound by memory where rows are many: 4096 x 131072 bf16 with its gradient, a

@@ -8,14 +8,14 @@ sampled tokens under the model's logits.  The gradients are calls of their own
 (``*_backward``, ``policy_loss_grad``); none of them records an autograd graph.
 
 Like ``batched_topk`` these only marshal arguments, in ``_binding`` (built from
-csrc_ops/binding.cpp): tensor metadata is checked before anything is queued, outputs
-not given and workspaces are allocated with torch, and the work runs in the
-library's HIP kernels, on ``stream`` or the current stream.  With ``stream``
+csrc_ops/binding.cpp): tensor metadata is checked before anything is queued,
+outputs not given and workspaces are allocated with torch, and the work runs in
+the library's HIP kernels, on ``stream`` or the current stream.  With ``stream``
 given, what is allocated or copied here belongs to that stream too; inputs made
 on another one must be ready for it, as for any torch call under
-``torch.cuda.stream``, and are kept until that stream has used them.  Matrices need a unit stride along their rows' elements and
-non-overlapping rows; others are copied first.  All calls may be captured into a
-graph.
+``torch.cuda.stream``, and are kept until that stream has used them.  Matrices
+need a unit stride along their rows' elements and non-overlapping rows; others
+are copied first.  All calls may be captured into a graph.
 """
 from __future__ import annotations
 
