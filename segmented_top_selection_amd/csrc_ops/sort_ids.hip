@@ -5,6 +5,9 @@
 // Few ids:
 //   rank_kernel     counts for each item those before it, n^2 comparisons spread
 //                   over the device
+// Somewhat more, among many segments:
+//   rank_kernel     sorts chunks of 1024 that way,
+//   merge_kernel    and this counts for each item those before it in the others
 // More: least-significant-digit radix passes of at most 9 bits, by workgroups of
 // 16 waves.  A block of up to 8192 items stays in registers, eight to a lane, each
 // wave holding consecutive items.  A wave takes its items 64 at a time and ranks
@@ -237,16 +240,18 @@ __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
     __shared__ uint32_t place[kRankItems];
     if (blockIdx.x >= a.chunks) return clear(a.fill, blockIdx.x - a.chunks, gridDim.x - a.chunks);
     uint32_t *const twice = reinterpret_cast<uint32_t *>(staged);
-    const uint32_t t = threadIdx.x, first = blockIdx.x * kRankItems;
-    const uint32_t per = rank_part(a.n), all = per * kRankParts;
+    const uint32_t t = threadIdx.x, items = rank_groups(a.n) * kRankItems;
+    const bool borders = blockIdx.x * kRankItems >= items;
+    // The chunk of the workgroup's items; `first` and `item` count from its start.
+    const uint32_t base = borders ? 0u : blockIdx.x * kRankItems / a.chunk * a.chunk;
+    const uint32_t count = min(a.chunk, a.n - base), first = blockIdx.x * kRankItems - base;
+    const uint32_t per = rank_part(min(a.chunk, a.n)), all = per * kRankParts;
     for (uint32_t i = t; i < all; i += kSortThreads)
-        twice[i] = i < a.n ? 2u * sort_key<true>(a, i) : 0xFFFFFFFFu;
+        twice[i] = i < count ? 2u * sort_key<true>(a, base + i) : 0xFFFFFFFFu;
     if (t < kRankItems) place[t] = 0u;
     __syncthreads();
     const uint32_t item = first + t % kRankItems, part = t / kRankItems;
-    const uint32_t items = rank_groups(a.n) * kRankItems;
-    const bool borders = first >= items;
-    const uint32_t mine = borders ? 2u * (item - items) : item < a.n ? twice[item] : 0u;
+    const uint32_t mine = borders ? 2u * (item - items) : item < count ? twice[item] : 0u;
     uint32_t before = 0;
     // A block of 16 keys lies before, at, or past the workgroup's items.  Before
     // them equal keys count: 2 key_j < 2 key_i + 1.
@@ -264,13 +269,77 @@ __global__ __launch_bounds__(kSortThreads) void rank_kernel(SortArgs a) {
     atomicAdd(&place[t % kRankItems], before);  // integers: any order gives the same sum
     __syncthreads();
     if (t >= kRankItems) return;
-    const uint32_t at = place[t];
+    const uint32_t at = base + place[t];
     if (borders) {
         if (item - items <= a.segments) a.offsets[item - items] = at;
-    } else if (item < a.n) {
+    } else if (item < count) {
         if (a.key_out) a.key_out[at] = mine / 2u;
-        if (a.slot_out) a.slot_out[at] = item;
-        if (a.position) a.position[item] = (int32_t)at;
+        if (a.slot_out) a.slot_out[at] = base + item;
+        if (a.position) a.position[base + item] = (int32_t)at;
+    }
+}
+
+// Chunks of 1024 items, each in order, joined: an item goes past its place in its
+// own chunk by the keys of the other chunks that go before it, each found by
+// halving.  A workgroup places 64 items (one to a lane), or 64 borders; its waves
+// take the chunks in turn, 15 at a time from LDS.
+constexpr uint32_t kMergeChunk = 1024, kMergeItems = 64, kMergeChunks = 15;
+
+__global__ __launch_bounds__(kSortThreads) void merge_kernel(SortArgs a) {
+    extern __shared__ uint4 staged[];  // keys; past the last one the largest number
+    __shared__ uint32_t place[kMergeItems];
+    if (blockIdx.x >= a.chunks) return clear(a.fill, blockIdx.x - a.chunks, gridDim.x - a.chunks);
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(staged);
+    const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
+    const uint32_t items = (a.n + kMergeItems - 1u) / kMergeItems * kMergeItems;
+    const uint32_t i = blockIdx.x * kMergeItems + lane;
+    const bool borders = i >= items;
+    const uint32_t key = borders ? i - items : i < a.n ? a.key_in[i] : 0u;
+    const uint32_t own = borders ? 0xFFFFFFFFu : i / kMergeChunk;  // of the workgroup: 64 divides 1024
+    const uint32_t chunks = (a.n + kMergeChunk - 1u) / kMergeChunk;
+    if (t < kMergeItems) place[t] = 0u;
+    uint32_t before = 0;
+    for (uint32_t c0 = 0; c0 < chunks; c0 += kMergeChunks) {
+        const uint32_t here = min(kMergeChunks, chunks - c0);
+        __syncthreads();
+        static_assert(kMergeChunk == kSortThreads, "a key of each chunk to a thread");
+        uint32_t k[kMergeChunks];  // loaded together
+#pragma unroll
+        for (uint32_t j = 0; j < kMergeChunks; ++j) {
+            const uint32_t at = (c0 + j) * kMergeChunk + t;
+            k[j] = at < a.n ? a.key_in[at] : 0xFFFFFFFFu;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kMergeChunks; ++j)
+            if (j < here) keys[j * kMergeChunk + t] = k[j];
+        __syncthreads();
+        if (w >= here) continue;
+        const uint32_t c = c0 + w;
+        if (c == own) {
+            before += i % kMergeChunk;
+            continue;
+        }
+        // Equal keys of an earlier chunk go before it.
+        const uint32_t limit = key + (!borders && c < own ? 1u : 0u);
+        const uint32_t *const list = keys + w * kMergeChunk;
+        uint32_t below = 0;
+#pragma unroll
+        for (uint32_t step = kMergeChunk / 2; step; step >>= 1)
+            if (list[below + step - 1u] < limit) below += step;
+        before += below + (list[below] < limit ? 1u : 0u);
+    }
+    __syncthreads();
+    if (before) atomicAdd(&place[lane], before);  // integers: any order gives the same sum
+    __syncthreads();
+    if (w) return;
+    const uint32_t at = place[lane];
+    if (borders) {
+        if (key <= a.segments) a.offsets[key] = at;
+    } else if (i < a.n) {
+        const uint32_t slot = a.slot_in[i];
+        if (a.key_out) a.key_out[at] = key;
+        if (a.slot_out) a.slot_out[at] = slot;
+        if (a.position) a.position[slot] = (int32_t)at;
     }
 }
 
@@ -290,13 +359,17 @@ __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segm
 
 // Counting against radix passes: among 128 segments (one pass) 5000 ids take 6.1 us
 // against 7.4, 8000 8.8 against 7.5 but in one launch, of which each costs the host
-// 2.2 to 2.8, 9000 13.5 against 7.8; among 40000 (two passes) 9000 take 18.0 against
-// 22.3, 14000 25.2 against 22.5.  Borders past so many are searched in the sorted
-// keys, in a launch of their own.
-constexpr int64_t kMaxRanked = 12288, kMaxRankedOnePass = 8192, kManyBorders = 4096;
+// 2.2 to 2.8, 9000 13.5 against 7.8.  Where radix takes two passes, four launches:
+// 5000 among 3000 6.2 by counting, 7000 10.8 and 7.8 by chunks joined; with the
+// search of 40001 borders 9000 take 17.9 by counting, 13.6 by chunks and 22.3 by
+// radix, 20000 18.6 and 23.1, 32768 among 131072 24.5 and 25.6, but then the tables
+// of a gradient, cleared beside it, want the longer sort; 50000 40.8 and 28.1.
+// Borders past so many are searched in the sorted keys, in a launch of their own.
+constexpr int64_t kMaxRanked = 5120, kMaxMerged = 20480, kMaxRankedOnePass = 8192;
+constexpr int64_t kManyBorders = 4096;
 
 struct SortPlan {
-    bool ranked;  // by rank_kernel
+    bool ranked, merged;  // by rank_kernel alone, or with merge_kernel
     int passes, bits;
     uint32_t bins, chunk, chunks;
     size_t hist_bytes, pair_bytes, bytes;
@@ -321,6 +394,12 @@ SortPlan sort_plan(int64_t n, int64_t segments) {
         p.chunks = rank_groups((uint32_t)n);
         p.pair_bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
         p.bytes = p.passes > 1 ? p.pair_bytes : 0;
+        return p;
+    }
+    if ((p.merged = p.passes > 1 && n <= kMaxMerged)) {
+        p.chunks = rank_groups((uint32_t)n);
+        p.pair_bytes = ((size_t)n * 4 + 255) & ~(size_t)255;
+        p.bytes = 3 * p.pair_bytes;
         return p;
     }
     // Chunks of whole blocks (of part of one, where there are few items): few enough
@@ -353,7 +432,7 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
     uint32_t *pair[2][2] = {};
     if (p.passes > 1 && !sorted) sorted = reinterpret_cast<uint32_t *>(ws + p.hist_bytes);
     if (p.passes > 1 && !p.ranked)
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < (p.merged ? 2 : 4); ++i)
             pair[i >> 1][i & 1] =
                 reinterpret_cast<uint32_t *>(ws + p.hist_bytes + (i + 1) * p.pair_bytes);
     SortArgs a{};
@@ -361,15 +440,15 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
     a.hist = reinterpret_cast<uint32_t *>(ws);
     a.n = (uint32_t)n;
     a.segments = (uint32_t)segments;
-    a.chunk = p.chunk;
+    a.chunk = p.ranked ? (n ? (uint32_t)n : 1u) : p.merged ? kMergeChunk : p.chunk;
     a.bins = p.bins;
     a.bits = (uint32_t)p.bits;
     a.wide = id_type == SEGTOPK_KEY_I64;
-    const bool borders = p.ranked && offsets && segments < kManyBorders;
-    a.chunks = p.chunks + (borders ? (uint32_t)(segments / kRankItems + 1) : 0u);
+    const bool borders = (p.ranked || p.merged) && offsets && segments < kManyBorders;
+    a.chunks = p.chunks + (borders && p.ranked ? (uint32_t)(segments / kRankItems + 1) : 0u);
     a.offsets = borders || p.passes == 1 ? offsets : nullptr;
     const Fill whole = fill ? *fill : Fill{};
-    const uint64_t launches = p.ranked ? 1 : 2 * p.passes;
+    const uint64_t launches = p.ranked ? 1 : p.merged ? 2 : 2 * p.passes;
     const uint64_t share = ((whole.bytes + launches - 1) / launches + 15) & ~(uint64_t)15;
     uint64_t filled = 0;
     hipError_t err = hipSuccess;
@@ -387,9 +466,24 @@ hipError_t queue_sort(const void *ids, int id_type, int64_t n, int64_t segments,
         a.key_out = sorted;
         a.slot_out = reinterpret_cast<uint32_t *>(order);
         a.position = position;
-        if (!queue(rank_kernel, (size_t)rank_part(a.n) * kRankParts * 4)) return err;
+        if (!queue(rank_kernel, (size_t)rank_part(a.n ? a.n : 1u) * kRankParts * 4)) return err;
     }
-    for (int i = 0; !p.ranked && i < p.passes; ++i) {
+    if (p.merged) {
+        a.key_out = pair[0][0];
+        a.slot_out = pair[0][1];
+        if (!queue(rank_kernel, (size_t)rank_part(kMergeChunk) * kRankParts * 4)) return err;
+        a.key_in = a.key_out;
+        a.slot_in = a.slot_out;
+        a.key_out = sorted;
+        a.slot_out = reinterpret_cast<uint32_t *>(order);
+        a.position = position;
+        a.chunks = (uint32_t)((n + kMergeItems - 1) / kMergeItems) +
+                   (borders ? (uint32_t)(segments / kMergeItems + 1) : 0u);
+        const int64_t held = (n + kMergeChunk - 1) / kMergeChunk;
+        const size_t most = (size_t)(held < kMergeChunks ? held : kMergeChunks);
+        if (!queue(merge_kernel, most * kMergeChunk * 4)) return err;
+    }
+    for (int i = 0; !p.ranked && !p.merged && i < p.passes; ++i) {
         const bool last = i == p.passes - 1;
         a.shift = (uint32_t)(i * p.bits);
         a.key_in = i ? pair[(i - 1) & 1][0] : nullptr;

@@ -16,7 +16,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("segments", [128, 511, 512, 30000])
-@pytest.mark.parametrize("n", [31, 32, 33, 1024, 4096, 9001, 12287, 12288, 12289, 15361, 131073])
+@pytest.mark.parametrize("n", [15, 16, 17, 1024, 4096, 5119, 5120, 5121, 6145, 9001, 15360, 15361,
+                               20480, 20481, 131073])
 def test_sort_ids_where_its_launches_change(n, segments):
     ids = torch.randint(-1, segments + 1, (n,), generator=gen(n + segments), device=DEV)
     check_sort(ids, segments)
