@@ -376,7 +376,9 @@ int segtopk_embedding_backward(const segtopk_rows *dout, const segtopk_rows *dta
  * answer's live rows; an answer without one adds zero.  A row is live if its
  * token is in [0, vocab) and it lies in an answer; the others, and rows whose
  * logits are all -inf, have logp 0, no term and a gradient of zero, and what
- * else they hold does not matter.  A logit of -inf is a token ruled out.
+ * else they hold does not matter.  A logit of -inf is a token ruled out.  NaN
+ * in a live row (logits, old_logp, advantage; ref_logp if kl_coef is not 0) and
+ * a logit of +inf make the loss and the row's gradient NaN.
  *
  *   dlogits.data  NULL: no gradient.  Else grad_scale * d loss / d logits, of
  *                 the logits' type; it may be the logits themselves (same

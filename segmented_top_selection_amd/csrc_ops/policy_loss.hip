@@ -11,7 +11,8 @@
 //                   + kl (1 - exp(ref - lp))
 //   dlogits[c] = weight_t (d term / d lp) (1[c = y] - exp(z[c] - lse)) / temperature
 // A row without a token in [0, vocab), or in no answer, counts for nothing: its
-// gradient is zero.
+// gradient is zero.  NaN in what any other row is made of, and a logit of +inf,
+// give a loss and a gradient of that row that are NaN.
 //
 //   count_kernel  one workgroup an answer: the number of its live rows
 //   row_kernel    one workgroup a row: maximum and sum in one pass, then, where
@@ -205,11 +206,18 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const T *logits, T *dlogit
                 // Nothing but -inf: no distribution, and no loss.
                 if (st.m != -INFINITY || st.s != 0.0f) {
                     lp = ((double)xy - (double)st.m) / a.temperature - log((double)st.s);
+                    // Comparisons with NaN are false: it takes the side that is not
+                    // clipped, and so reaches the term and the gradient.
                     const double adv = adv32, ratio = exp(lp - (double)old);
-                    const double clipped = fmin(fmax(ratio, 1.0 - a.clip_low), 1.0 + a.clip_high);
-                    const bool free = ratio * adv <= clipped * adv;
-                    term = -(free ? ratio : clipped) * adv;
-                    d = free ? -ratio * adv : 0.0;
+                    const double low = 1.0 - a.clip_low, high = 1.0 + a.clip_high;
+                    const double clipped = ratio < low ? low : ratio > high ? high : ratio;
+                    // No advantage is nothing, at a ratio past the range too.
+                    const bool nothing = adv == 0.0 && ratio == INFINITY;
+                    const double gain = nothing ? 0.0 : ratio * adv;
+                    const double bound = nothing ? 0.0 : clipped * adv;
+                    const bool held = gain > bound;
+                    term = held ? -bound : -gain;
+                    d = held ? 0.0 : -gain;
                     if (a.kl_coef != 0.0) {
                         const double apart = (double)ref - lp, e = exp(apart);
                         term += a.kl_coef * (e - apart - 1.0);

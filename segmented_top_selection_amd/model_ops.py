@@ -226,6 +226,8 @@ def policy_loss(logits: torch.Tensor, token_ids: torch.Tensor, old_logp: torch.T
       + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1)
     and the loss is the mean over answers of each answer's mean over its rows.
     Returns the loss (float32, 0-D) and logp (float32, 0 for rows left out).
+    Rows left out may hold anything; NaN or a logit of +inf in any other row
+    makes the loss, and that row's gradient, NaN.
     """
     args = (logits, token_ids, old_logp, advantages, segment_offsets, ref_logp, kl_coef, clip_low,
             clip_high, temperature, 1.0, None, False)
