@@ -344,6 +344,7 @@ GradPlan grad_plan(int64_t n, int64_t num_rows, int64_t width) {
 template <class T, class O>
 hipError_t queue_grad(const segtopk_rows *dout, const segtopk_rows *dtable, const GradArgs &a,
                       hipStream_t stream) {
+    if (!a.chunks) return hipSuccess;  // no tokens: nothing to add, and dout may be absent
     O *table = static_cast<O *>(dtable->data);
     const hipError_t err = launch(sum_kernel<T, O>, dim3(a.chunks * a.cols), kOpThreads, stream, 0,
                                   static_cast<const T *>(dout->data), table, a);
