@@ -379,6 +379,9 @@ int segtopk_embedding_backward(const segtopk_rows *dout, const segtopk_rows *dta
  * else they hold does not matter.  A logit of -inf is a token ruled out.  NaN
  * in a live row (logits, old_logp, advantage; ref_logp if kl_coef is not 0) and
  * a logit of +inf make the loss and the row's gradient NaN.
+ * A sampled token that is ruled out has logp -inf and r 0.  With kl_coef its
+ * term, and the loss, are +inf, and so is the size of the row's gradient; that
+ * of the other tokens ruled out is zero.
  *
  *   dlogits.data  NULL: no gradient.  Else grad_scale * d loss / d logits, of
  *                 the logits' type; it may be the logits themselves (same

@@ -220,7 +220,8 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const T *logits, T *dlogit
                     d = held ? 0.0 : -gain;
                     if (a.kl_coef != 0.0) {
                         const double apart = (double)ref - lp, e = exp(apart);
-                        term += a.kl_coef * (e - apart - 1.0);
+                        // Infinite where a token ruled out was sampled: apart is, too.
+                        term += a.kl_coef * (e == INFINITY ? e : e - apart - 1.0);
                         d += a.kl_coef * (1.0 - e);
                     }
                     const double weight = 1.0 / (a.answers * (double)live);
@@ -248,6 +249,13 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const T *logits, T *dlogit
             for (uint32_t u = i; u < pieces; u += THREADS)
                 store_piece<STREAM>(grad + (size_t)u * P::N, (typename P::vec)(T)0.0f);
             if (single < a.vocab) grad[single] = (T)0.0f;
+        } else if (fabsf(slope) == INFINITY) {
+            // Of a token ruled out: infinite, but zero where no probability moves.
+            for (uint32_t c = i; c < a.vocab; c += THREADS) {
+                const float p = __builtin_amdgcn_exp2f(fmaf((float)row[c] - m, a.factor, -l));
+                const float moves = (c == token ? 1.0f : 0.0f) - p;
+                grad[c] = (T)(moves == 0.0f ? 0.0f : slope * moves);
+            }
         } else {
             const uint32_t hot = token / P::N, place = token % P::N;
             for (uint32_t g = groups; g-- > 0;) {
