@@ -87,7 +87,8 @@ const Tensor &there(const char *name, PyObject *o, at::Device dev) {
 bool given(PyObject *o) { return o != Py_None; }
 
 int64_t integer(PyObject *o) {
-    PyObject *i = PyLong_Check(o) ? (Py_INCREF(o), o) : PyNumber_Long(o);
+    // Integers of any kind; no text, and nothing that would lose its fraction.
+    PyObject *i = PyNumber_Index(o);
     if (!i) throw python_error();
     const int64_t v = PyLong_AsLongLong(i);
     Py_DECREF(i);
