@@ -280,8 +280,13 @@ PyObject *same(PyObject *o) {
     return o;
 }
 
-// The tensor that the caller gave, or the new one.
-PyObject *output(PyObject *o, const Tensor &t) { return given(o) ? same(o) : THPVariable_Wrap(t); }
+// The tensor that the caller gave, or the new one.  Autograd is told that the
+// caller's was written, so that a graph that keeps it refuses to go on.
+PyObject *output(PyObject *o, const Tensor &t) {
+    if (!given(o)) return THPVariable_Wrap(t);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    return same(o);
+}
 
 // ---- the calls ----------------------------------------------------------
 // Arguments come by position from model_ops, None for those not given.

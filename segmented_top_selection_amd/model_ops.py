@@ -15,7 +15,8 @@ given, what is allocated or copied here belongs to that stream too; inputs made
 on another one must be ready for it, as for any torch call under
 ``torch.cuda.stream``, and are kept until that stream has used them.  Matrices
 need a unit stride along their rows' elements and non-overlapping rows; others
-are copied first.  All calls may be captured into a graph.
+are copied first.  All calls may be captured into a graph.  Tensors that a call
+writes into (``out``, ``dlogits``) count as modified in place for autograd.
 """
 from __future__ import annotations
 
