@@ -63,26 +63,34 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     cmds = [[hipcc, *HIPCC_FLAGS, "-c", s, "-o", o] for s, o in zip(srcs, objs)]
     # The benchmark's stream-read probe: a library of its own.
     cmds.append([hipcc, *HIPCC_FLAGS, "-shared", PROBE_SRC, "-o", PROBE_LIB])
-    cmds.append(binding_command(BINDING_LIB + ".tmp"))
-    if verbose:
-        for c in cmds:
+
+    def run(c):
+        if verbose:
             print(" ".join(c), flush=True)
-    jobs = jobs or min(len(cmds), max(1, min(16, os.cpu_count() or 1)))
+        return subprocess.run(c, capture_output=True, text=True)
+
+    def check(r):
+        if r.stderr and verbose:
+            # hipcc's host pass warns about the device-only feature flag.
+            lines = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln]
+            if lines:
+                print("\n".join(lines), flush=True)
+        if r.returncode != 0:
+            raise subprocess.CalledProcessError(r.returncode, r.args, r.stdout, r.stderr)
+
+    jobs = jobs or min(len(cmds) + 1, max(1, min(16, os.cpu_count() or 1)))
     with ThreadPoolExecutor(jobs) as ex:
-        for r in ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), cmds):
-            if r.stderr and verbose:
-                # hipcc's host pass warns about the device-only feature flag.
-                lines = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln]
-                if lines:
-                    print("\n".join(lines), flush=True)
-            if r.returncode != 0:
-                raise subprocess.CalledProcessError(r.returncode, r.args, r.stdout, r.stderr)
-    tmp = LIB + ".tmp"
-    link = [hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
-    if verbose:
-        print(" ".join(link), flush=True)
-    subprocess.check_call(link)
-    os.replace(tmp, LIB)
+        # The C library needs hipcc alone, and is linked whatever comes of the binding.
+        binding = ex.submit(lambda: run(binding_command(BINDING_LIB + ".tmp")))
+        for r in ex.map(run, cmds):
+            check(r)
+        tmp = LIB + ".tmp"
+        link = [hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
+        if verbose:
+            print(" ".join(link), flush=True)
+        subprocess.check_call(link)
+        os.replace(tmp, LIB)
+        check(binding.result())
     os.replace(BINDING_LIB + ".tmp", BINDING_LIB)
     return LIB
 
