@@ -352,8 +352,9 @@ int segtopk_embedding_rows(const segtopk_rows *table, const segtopk_rows *out, c
  * add nothing, nor does padding_id (outside [0, num_rows): no padding).
  * accumulate != 0: the sums are added to what dtable holds, and rows of ids that
  * do not occur are neither read nor written.  dtable is of dout's type or
- * SEGTOPK_KEY_F32.  SEGTOPK_NOT_SUPPORTED: more work than one launch holds
- * (about n * width / 64 Ki >= 2^24).
+ * SEGTOPK_KEY_F32.  SEGTOPK_NOT_SUPPORTED: more work than one launch holds,
+ * ceil(n / 64) * ceil(u / 256) >= 2^24 - 1, where u is the number of whole 16-byte
+ * pieces in a row of dout and of elements past them.
  */
 int64_t segtopk_embedding_backward_workspace(int64_t n, int64_t num_rows, int64_t width);
 int segtopk_embedding_backward(const segtopk_rows *dout, const segtopk_rows *dtable,
