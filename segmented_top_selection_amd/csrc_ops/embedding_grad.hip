@@ -14,10 +14,10 @@
 //
 // Bound by writing the table, most of whose rows are zeros, and reading dout, or by
 // latency where there is little of both (20 tokens, 5000 x 500: 3.9 us):
-// 32768 tokens, 131072 x 4096 bf16 take 268 us (1.34 GB, 5.0 TB/s): sort and
-// clearing 188, sums 71, finish 8.  Looking up which rows to clear, in sum_kernel,
+// 32768 tokens, 131072 x 4096 bf16 take 269 us (1.34 GB, 5.0 TB/s): sort and
+// clearing 188, sums 70, finish 8.  Looking up which rows to clear, in sum_kernel,
 // took as long.  Of 5003 tokens, 4099 x 1001 f32, the launches' latency is most:
-// 8.2 + 7.5 + 5.3 us.
+// 8.2 + 7.6 + 5.2 us.
 #include "ops_common.h"
 
 namespace segtopk_ops {

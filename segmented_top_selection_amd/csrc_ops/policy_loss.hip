@@ -27,9 +27,9 @@
 // wholly in 32 bits up to 1e-5).
 //
 // Bound by memory where rows are many: 4096 x 131072 bf16 with its gradient, a
-// quarter of the rows left out, take 367 us, 5.1 TB/s of what has to be read and
-// written; by latency where they are few: 96 x 32003 f16 9.2 us, of which the
-// arrival takes 1 and the 64 bits 0.4.
+// quarter of the rows left out, take 366 us, 5.1 TB/s of what has to be read and
+// written; by latency where they are few, a workgroup to a row: 96 x 32003 f16
+// 10 us, of which the arrival takes 1 and the 64 bits 0.4.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const T *logits, T *dlogit
         // The term is stored past this XCD's cache, and has arrived where every
         // XCD sees it before the row counts as arrived.  A release at device
         // scope would do so by writing the whole cache back, the gradient with
-        // it, once a row: 638 us for 4096 x 131072 bf16 where this takes 368.
+        // it, once a row: 638 us for 4096 x 131072 bf16 where this takes 366.
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         mine = arrive(a.arrived + (1u + t % kCounters) * kCounterWords);
     }

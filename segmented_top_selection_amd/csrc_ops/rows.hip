@@ -18,11 +18,12 @@
 // rows stays in registers (32 bits).  Pieces past the last whole one are
 // single elements, one to a thread.  What is read once, and outputs of 128 MiB or
 // more, go past the caches: left there they are written back while the next
-// kernel reads (sort, dispatch and combine of 8192 tokens x 8 x 4096 bf16 263 us,
-// so 216; a kernel that reads the rows right after loses 2%).
+// kernel reads (sort, dispatch and combine of 8192 tokens x 8 x 4096 bf16, the same
+// inputs again and again, 263 us, so 216; a kernel that reads the rows right after
+// loses 2%).  On new inputs each time the three take 236.
 //
-// 8192 tokens x 8 x 4096 bf16: dispatch 103 us (5.9 TB/s of what it reads and
-// writes), combine 104 (5.8), its gradient 217 (5.2); a 4 GiB copy reaches 4.7.
+// 8192 tokens x 8 x 4096 bf16: dispatch 102 us (5.9 TB/s of what it reads and
+// writes), combine 104 (5.8), its gradient 219 (5.2); a 4 GiB copy reaches 4.7.
 // Lookup of 32768 rows of 4096 bf16, new rows each time: 70 us (5.1 TB/s).
 #include <type_traits>
 
@@ -410,9 +411,14 @@ extern "C" int segtopk_combine_rows_backward(const segtopk_rows *dout, const seg
     return with_type(dout->type, [&](auto t) {
         using T = decltype(t);
         Cut c = cut_of(width, sizeof(T));
-        // A wave to a token where that fills the device: 2048 tokens x 4 x 2048 bf16,
-        // with its other gradient, 26.2 us against 29.0; 777 x 6 x 1410 f16 19.0
-        // against 17.0.  A wide row takes four either way (4096 bf16: 346, 322).
+        // A row of more than 128 units by a wave or by a workgroup, us of this kernel, bf16
+        // (k = 2, 4, 8 in turn).  Few tokens leave waves idle: 256 x 1410 6.0, 7.5, 13.0
+        // and 4.5, 5.7, 8.8; 1024 x 2048 8.5, 12.7, 19.6 and 6.7, 10.2, 17.1.  From 2048
+        // on the waves fill the device: 2048 x 1410 10.1, 15.9, 27.0 and 12.4, 18.6, 31.7;
+        // 4096 x 1410 14.4, 23.6, 47.4 and 19.5, 30.2, 61.3.  At the widest, 256 units, it
+        // depends on k: 4096 x 2048 16.7, 28.7, 69.1 and 18.1, 28.8, 57.4.  Wider rows
+        // are a workgroup's: 4096 x 4096 31.4 and 31.2 (k = 2), 123 and 112 (k = 8).  Up to
+        // 128 units a wave holds the row in two rounds: 2048 x 1000 7.1 and 9.3 (k = 2).
         const bool wide = c.units > 256u || (c.units > 128u && tokens < 2048);
         c.lanes = wide ? (uint32_t)kOpThreads : 64u;
         const bool past = streams(tokens * k * width * (int64_t)sizeof(T));

@@ -359,12 +359,14 @@ __global__ void offsets_kernel(const uint32_t *sorted, uint32_t n, uint32_t segm
 
 // Counting against radix passes: among 128 segments (one pass) 5000 ids take 6.1 us
 // against 7.4, 8000 8.8 against 7.5 but in one launch, of which each costs the host
-// 2.2 to 2.8, 9000 13.5 against 7.8.  Where radix takes two passes, four launches:
-// 5000 among 3000 6.2 by counting, 7000 10.8 and 7.8 by chunks joined; with the
-// search of 40001 borders 9000 take 17.9 by counting, 13.6 by chunks and 22.3 by
-// radix, 20000 18.6 and 23.1, 32768 among 131072 24.5 and 25.6, but then the tables
-// of a gradient, cleared beside it, want the longer sort; 50000 40.8 and 28.1.
-// Borders past so many are searched in the sorted keys, in a launch of their own.
+// 2.2 to 2.8, 9000 13.5 against 7.8 (from about 6500 to 8192 ids, a captured graph,
+// which does not pay the host, would be served better by radix).  Where radix takes
+// two passes, four launches: 5000 among 3000 6.2 by counting, 7000 10.8 and 7.8 by
+// chunks joined; with the search of 40001 borders 9000 take 17.9 by counting, 13.6
+// by chunks and 22.3 by radix, 20000 18.6 and 23.1, 32768 among 131072 24.5 and 25.6,
+// but then the tables of a gradient, cleared beside it, want the longer sort; 50000
+// 40.8 and 28.1.  Borders past so many are searched in the sorted keys, in a launch
+// of their own.
 constexpr int64_t kMaxRanked = 5120, kMaxMerged = 20480, kMaxRankedOnePass = 8192;
 constexpr int64_t kManyBorders = 4096;
 
