@@ -96,6 +96,11 @@ int64_t integer(PyObject *o) {
     return v;
 }
 
+// Before outputs of that many entries are allocated.
+void check_count(const char *name, int64_t v) {
+    TORCH_CHECK_VALUE(v >= 0 && v < INT32_MAX, name, " must be >= 0 and below 2^31 - 1 (got ", v, ")");
+}
+
 double real(PyObject *o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -296,7 +301,7 @@ PyObject *sort_ids(PyObject *const *a) {
     const c10::DeviceGuard guard(dev);
     const Ids ids = ids_of("ids", given_ids);
     const int64_t n = ids.t.numel(), segments = integer(a[1]);
-    TORCH_CHECK_VALUE(segments >= 0, "num_segments must be >= 0");
+    check_count("num_segments", segments);
     const Tensor order = fresh({n}, ScalarType::Int, dev);
     const Tensor position = fresh(ids.t.sizes(), ScalarType::Int, dev);
     const Tensor offsets = fresh({segments + 1}, ScalarType::Long, dev);
@@ -401,7 +406,7 @@ PyObject *embedding_backward(PyObject *const *a) {
     const c10::DeviceGuard guard(dev);
     const Ids ids = ids_of("ids", there("ids", a[1], dev));
     const int64_t n = ids.t.numel(), num_rows = integer(a[2]);
-    TORCH_CHECK_VALUE(num_rows >= 0, "num_rows must be >= 0");
+    check_count("num_rows", num_rows);
     const bool deep = given_dout.dim() != 2 && given_dout.dim() >= 1 &&
                       given_dout.sizes().slice(0, given_dout.dim() - 1) == ids.t.sizes();
     const Matrix dout = matrix("dout", deep ? given_dout.reshape({n, given_dout.size(-1)}) : given_dout);

@@ -74,3 +74,14 @@ def test_inputs_and_tensors_outside_autograd_are_left_as_they_were():
         st.embedding(x, ids, out=out)
     st.embedding(x, ids, out=out)  # has no version to count
     assert torch.equal(out, x)
+
+
+@pytest.mark.parametrize("count", [-1, 2 ** 31 - 1, 2 ** 40, 2 ** 63 - 1])
+def test_counts_past_the_limits_are_refused_before_anything_is_allocated(count):
+    x, ids = torch.zeros(4, 8, device=DEV), torch.zeros(4, dtype=torch.int64, device=DEV)
+    held = torch.cuda.max_memory_allocated()
+    with pytest.raises(ValueError):
+        st.sort_ids(ids, count)
+    with pytest.raises(ValueError):
+        st.embedding_backward(x, ids, count)
+    assert torch.cuda.max_memory_allocated() == held
