@@ -159,8 +159,8 @@ def _weights(g, E, N, K):
         w = torch.zeros(nb * 128, kb * 128, device=DEV)
         w[:N, :K] = torch.randn(N, K, generator=g, device=DEV) * K ** -0.5
         most = w.view(nb, 128, kb, 128).abs().amax((1, 3)).clamp(min=FLOOR)
-        scales[e] = most / F8_MAX
-        w = w.view(nb, 128, kb, 128) * (F8_MAX / most)[:, None, :, None]
+        scales[e] = _ratio(most, F8_MAX)
+        w = w.view(nb, 128, kb, 128) * _ratio(F8_MAX, most)[:, None, :, None]
         q[e] = w.view(nb * 128, kb * 128)[:N, :K].to(F8)
     return q, scales
 
@@ -278,11 +278,17 @@ def _plain_route_backward(s):
     return d.to(s["logits"].dtype)
 
 
+def _ratio(a, b):
+    """a / b rounded once to 32 bits (torch multiplies by a number's reciprocal)."""
+    a, b = (torch.as_tensor(v, dtype=torch.float64, device=DEV) for v in (a, b))
+    return (a / b).float()
+
+
 def _blocks(x, dim):
     """x in 8 bits with a scale for each 128 along `dim` (a multiple of 128): the values that stand for it."""
     b = x.unflatten(dim, (-1, 128))
     most = b.abs().amax(dim + 1, keepdim=True).clamp(min=FLOOR)
-    return ((b * (F8_MAX / most)).to(F8).float() * (most / F8_MAX)).flatten(dim, dim + 1)
+    return ((b * _ratio(F8_MAX, most)).to(F8).float() * _ratio(most, F8_MAX)).flatten(dim, dim + 1)
 
 
 def _pad(x, n):
@@ -443,7 +449,8 @@ def _exact_route(case, s):
 def _eight_bits(x):
     """x (n, up to 128 numbers): the values that stand for them."""
     most = torch.linalg.vector_norm(x, math.inf, dim=1, keepdim=True).clamp(min=FLOOR)
-    return (x * (F8_MAX / most)).to(F8).double() * (most / F8_MAX).double()
+    down, up = F8_MAX / most.double(), most.double() / F8_MAX
+    return (x * down.float()).to(F8).double() * up.float().double()
 
 
 def _exact_experts(case, s):
