@@ -407,6 +407,182 @@ int64_t segtopk_policy_loss_workspace(int64_t tokens, int64_t vocab, int64_t num
 int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *workspace,
                         int64_t workspace_bytes, hipStream_t stream);
 
+/* ---- routing ----------------------------------------------------------- */
+#define SEGTOPK_SOFTMAX 0
+#define SEGTOPK_SIGMOID 1
+
+/*
+ * segtopk_route -- a router's selection, from logits to gate weights.
+ *
+ * For each token with logits x [num_experts]:
+ *   p = softmax(x) or sigmoid(x)
+ *   s = p + bias (bias may be NULL: zero); an expert whose logit or bias is -inf
+ *       is ruled out
+ *   Experts form `groups` groups of num_experts / groups neighbours.  A group's
+ *   score is the sum of its group_best (1 or 2) best s; the kept_groups best
+ *   groups that have an expert left stay, the others' experts are ruled out.
+ *   experts [tokens * k]  the k best by s, best first, ties to the lower index
+ *                         (groups too); -1 where none is left
+ *   weights [tokens * k]  scale p, divided by the sum of the chosen p if
+ *                         renormalize is not 0; 0 where the expert is -1
+ * Scores are compared in 64 bits, and as the logits themselves where that is the
+ * same order (no bias, and no sum of two).  A NaN counts as the lowest score that
+ * is not ruled out; with SEGTOPK_SOFTMAX a NaN or +inf makes all of the token's
+ * weights NaN, with SEGTOPK_SIGMOID a NaN those that it takes part in.
+ * logits: rows of num_experts.  1 <= num_experts <= 1024, 1 <= groups <= 64 and a
+ * divisor of num_experts, 1 <= kept_groups <= groups,
+ * 1 <= k <= min(64, kept_groups * num_experts / groups), 0 <= tokens < 2^31 - 1.
+ */
+typedef struct segtopk_route_args {
+    segtopk_rows logits;
+    int64_t tokens, num_experts, k;
+    int32_t scoring, renormalize;
+    double scale;
+    const float *bias;
+    int64_t groups, kept_groups;
+    int32_t group_best;
+    float *weights;
+    int32_t *experts;
+} segtopk_route_args;
+int segtopk_route(const segtopk_route_args *args, hipStream_t stream);
+
+/*
+ * segtopk_route_backward -- the gradient of the logits, given that of the weights
+ * and the experts chosen (the choice itself has none):
+ *   g_j = scale dweights[j], S = sum of the chosen p, u_j = p_j / S
+ *   dp_j = renormalize ? (g_j - sum_i g_i u_i) / S : g_j     for the chosen, else 0
+ *   dlogits = p (dp - <dp, p>) (softmax), dp p (1 - p) (sigmoid)
+ * dlogits is of the logits' type.  Slots whose expert is outside
+ * [0, num_experts) add nothing, whatever their dweights.  Limits are segtopk_route's.
+ */
+int segtopk_route_backward(const segtopk_rows *logits, const segtopk_rows *dlogits,
+                           const int32_t *experts, const float *dweights, int64_t tokens,
+                           int64_t num_experts, int64_t k, int32_t scoring, int32_t renormalize,
+                           double scale, hipStream_t stream);
+
+/* ---- the experts' products in 8 bits ------------------------------------- */
+/* Element type of rows in 8 bits: OCP e4m3 (largest value 448, no infinities).
+ * It is no key type.  Such rows are aligned to 16 bytes, their stride is a
+ * multiple of 16, and they are read, and by the quantizers written (with zeros),
+ * up to the next multiple of 16 bytes. */
+#define SEGTOPK_E4M3 32
+
+/* Matrices one behind the other: matrix e begins at data + e * matrix_stride
+ * elements. */
+typedef struct segtopk_matrices {
+    void *data;
+    int64_t matrix_stride, stride;
+    int32_t type;
+} segtopk_matrices;
+
+/*
+ * segtopk_quantize_rows -- rows in 8 bits, with a scale for each 128 columns:
+ *   a = max(|x|) over the block, at least 2^-96
+ *   scale = a / 448,  q = e4m3(x * (448 / a))     each rounded once, to nearest even
+ * x has `tokens` rows of `width`.  position NULL (k is 1 then): q[t] and
+ * scales[t * blocks + b] belong to x[t], blocks = ceil(width / 128).  Else row t is
+ * written to each row position[t * k + j] as by segtopk_dispatch_rows; rows of
+ * dropped slots are zero and have scales 0.  inf or NaN in a block makes its values NaN.
+ */
+int segtopk_quantize_rows(const segtopk_rows *x, const segtopk_rows *q, float *scales,
+                          int64_t tokens, int64_t k, int64_t width, const int32_t *position,
+                          const int64_t *kept, hipStream_t stream);
+
+/*
+ * segtopk_quantize_blocks -- matrices in 8 bits, with a scale for each block of
+ * 128 x 128, as segtopk_quantize_rows makes them:
+ * scales [matrices][ceil(rows / 128)][ceil(width / 128)].
+ */
+int segtopk_quantize_blocks(const segtopk_matrices *x, const segtopk_matrices *q, float *scales,
+                            int64_t matrices, int64_t rows, int64_t width, hipStream_t stream);
+
+/*
+ * segtopk_expert_matmul -- each row times the transposed weights of its expert:
+ *   out[r][n] = sum_b row_scales[r][b] weight_scales[e][n / 128][b]
+ *                     sum over block b's c of rows[r][c] weights[e][n][c]
+ * for the rows offsets[e] .. offsets[e + 1] of expert e; rows from
+ * offsets[num_experts] on are zero.  rows is num_rows x depth, weights num_experts
+ * matrices of width x depth, both SEGTOPK_E4M3; out is num_rows x width.  Offsets do
+ * not decrease and are within [0, num_rows].  Sums are held in 32 bits; for a result
+ * of 16, each eight products are added up with the smaller cut off at 2^-13 of the
+ * largest, as the 8-bit matrix instruction does.
+ * With the weights (and their scales) transposed this is the gradient of the rows.
+ * num_rows < 2^31 - 1, 1 <= num_experts <= 65535.  SEGTOPK_NOT_SUPPORTED: more
+ * workgroups than one launch holds.
+ */
+typedef struct segtopk_expert_matmul_args {
+    segtopk_rows rows, out;
+    segtopk_matrices weights;
+    const float *row_scales, *weight_scales;
+    const int64_t *offsets;
+    int64_t num_rows, num_experts, width, depth;
+} segtopk_expert_matmul_args;
+int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hipStream_t stream);
+
+/*
+ * segtopk_expert_dweights -- the gradient of the experts' weights:
+ *   dweights[e] = sum over the rows r of expert e of dout[r]^T rows[r]
+ * with dout (num_rows x width) and rows (num_rows x depth) of one type, taken to 8
+ * bits with a scale for each column and each 128 rows of an expert, counted from
+ * its first.  dweights: num_experts matrices of width x depth, of dout's type or
+ * SEGTOPK_KEY_F32; zero for an expert without rows; sums as segtopk_expert_matmul's.  accumulate not 0: added to
+ * what they hold.  Rows behind offsets[num_experts] are not read.
+ */
+typedef struct segtopk_expert_dweights_args {
+    segtopk_rows dout, rows;
+    segtopk_matrices dweights;
+    const int64_t *offsets;
+    int64_t num_rows, num_experts, width, depth;
+    int32_t accumulate;
+} segtopk_expert_dweights_args;
+int64_t segtopk_expert_dweights_workspace(int64_t num_rows, int64_t num_experts, int64_t width,
+                                          int64_t depth);
+int segtopk_expert_dweights(const segtopk_expert_dweights_args *args, void *workspace,
+                            int64_t workspace_bytes, hipStream_t stream);
+
+/* ---- verification of drafted tokens --------------------------------------- */
+/*
+ * segtopk_verify_drafts -- which drafted tokens stand, and the token behind them.
+ *
+ * Request r drafted tokens draft_offsets[r] .. draft_offsets[r + 1], and has one row
+ * of target logits more than that: its drafted token i was to be drawn from target
+ * row i + r, and the token behind its last from row draft_offsets[r + 1] + r.
+ * p = softmax(target row / temperature), and q the same of draft row i.
+ *   Token t of draft i stands if accept[i] q(t) < p(t).
+ *   Behind the last that stands comes one token more: from the row of the first that
+ *   does not, the lowest c with sum of w up to c > sample[r] (sum of w),
+ *   w = max(p - q, 0) (p if those are all zero); from the row behind all drafts if
+ *   all stand, with w = p.
+ * draft.data NULL: the drafts were certain, q is one at the token and zero elsewhere.
+ * temperature 0: p is one at the largest logit (the lowest index of equal ones) and
+ * zero elsewhere, and the drafts count as certain.
+ *   temperatures [num_requests], or NULL: `temperature` for all; finite, >= 0
+ *   accept [num_drafts], sample [num_requests]  in [0, 1)
+ *   tokens [num_drafts + num_requests], of the drafts' id type: request r's from
+ *          draft_offsets[r] + r on, -1 behind its last
+ *   counts [num_requests]  how many tokens request r gets
+ * A logit of -inf is a token ruled out.  A drafted token outside [0, vocab) does not
+ * stand.  A row with NaN or +inf, or nothing but -inf, has no distribution: the draft
+ * does not stand if its target row or its draft row is such a one, and the token
+ * drawn from such a row (or from one whose draft row is) is -1.
+ * Probabilities and sums are in 64 bits.  Offsets do not decrease, from 0 to
+ * num_drafts.  num_drafts + num_requests < 2^22, 1 <= vocab < 2^31.
+ */
+typedef struct segtopk_verify_args {
+    segtopk_rows target, draft;
+    const void *draft_tokens;
+    int32_t id_type;
+    const int64_t *draft_offsets;
+    int64_t num_drafts, num_requests, vocab;
+    double temperature;
+    const float *temperatures, *accept, *sample;
+    void *tokens;
+    int32_t *counts;
+} segtopk_verify_args;
+int64_t segtopk_verify_workspace(int64_t num_drafts, int64_t num_requests, int64_t vocab);
+int segtopk_verify_drafts(const segtopk_verify_args *args, void *workspace,
+                          int64_t workspace_bytes, hipStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *segtopk_status_string(int status);
 

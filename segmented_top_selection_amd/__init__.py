@@ -263,4 +263,6 @@ def batched_topk(keys: torch.Tensor, segment_offsets: torch.Tensor, k: int, *,
 
 
 from .model_ops import (combine, combine_backward, dispatch, dispatch_backward,  # noqa: E402,F401
-                        embedding, embedding_backward, policy_loss, policy_loss_grad, sort_ids)
+                        dispatch_quantized, embedding, embedding_backward, expert_matmul,
+                        expert_matmul_dweights, policy_loss, policy_loss_grad, quantize_blocks,
+                        quantize_rows, route, route_backward, sort_ids, verify_drafts)

@@ -37,6 +37,15 @@ struct Library {
     decltype(&segtopk_embedding_backward) embedding_backward;
     decltype(&segtopk_policy_loss_workspace) policy_loss_workspace;
     decltype(&segtopk_policy_loss) policy_loss;
+    decltype(&segtopk_route) route;
+    decltype(&segtopk_route_backward) route_backward;
+    decltype(&segtopk_quantize_rows) quantize_rows;
+    decltype(&segtopk_quantize_blocks) quantize_blocks;
+    decltype(&segtopk_expert_matmul) expert_matmul;
+    decltype(&segtopk_expert_dweights_workspace) expert_dweights_workspace;
+    decltype(&segtopk_expert_dweights) expert_dweights;
+    decltype(&segtopk_verify_workspace) verify_workspace;
+    decltype(&segtopk_verify_drafts) verify_drafts;
 } lib;
 PyObject *call_error;  // (status, name of the call) -> the exception
 
@@ -491,6 +500,341 @@ PyObject *policy_loss(PyObject *const *a) {
     return tuple(THPVariable_Wrap(loss), THPVariable_Wrap(logp), output(a[11], dlogits.t));
 }
 
+// logits, k, scoring, bias, groups, kept_groups, group_best, whether to
+// renormalize, scale
+PyObject *route(PyObject *const *a) {
+    const Tensor &given_logits = device_tensor("logits", a[0]);
+    const at::Device dev = given_logits.device();
+    const c10::DeviceGuard guard(dev);
+    const Matrix logits = matrix("logits", given_logits);
+    segtopk_route_args q{};
+    q.logits = logits.v;
+    q.tokens = logits.rows;
+    q.num_experts = logits.width;
+    q.k = integer(a[1]);
+    q.scoring = (int32_t)integer(a[2]);
+    Tensor bias;
+    if (given(a[3])) {
+        bias = vector("bias", a[3], dev, logits.width);
+        q.bias = static_cast<const float *>(bias.data_ptr());
+    }
+    q.groups = integer(a[4]);
+    q.kept_groups = given(a[5]) ? integer(a[5]) : q.groups;
+    const int64_t best = integer(a[6]);
+    const int renormalize = PyObject_IsTrue(a[7]);
+    if (renormalize < 0) throw python_error();
+    q.renormalize = renormalize;
+    q.scale = real(a[8]);
+    TORCH_CHECK_VALUE(q.num_experts <= 1024, "at most 1024 experts (got ", q.num_experts, ")");
+    TORCH_CHECK_VALUE(q.groups >= 1 && q.groups <= 64 && q.num_experts % q.groups == 0,
+                      "groups must be 1 to 64 and divide the number of experts (got ", q.groups, ")");
+    TORCH_CHECK_VALUE(q.kept_groups >= 1 && q.kept_groups <= q.groups,
+                      "kept_groups must be 1 to groups (got ", q.kept_groups, ")");
+    TORCH_CHECK_VALUE(best == 1 || best == 2, "group_best must be 1 or 2 (got ", best, ")");
+    TORCH_CHECK_VALUE(q.k >= 1 && q.k <= 64 && q.k <= q.kept_groups * (q.num_experts / q.groups),
+                      "k must be 1 to 64 and at most the number of experts in the groups kept (got ",
+                      q.k, ")");
+    q.group_best = (int32_t)best;
+    const Tensor weights = fresh({q.tokens, q.k}, ScalarType::Float, dev);
+    const Tensor experts = fresh({q.tokens, q.k}, ScalarType::Int, dev);
+    q.weights = static_cast<float *>(weights.data_ptr());
+    q.experts = static_cast<int32_t *>(experts.data_ptr());
+    call("segtopk_route", dev, [&](hipStream_t stream) { return lib.route(&q, stream); });
+    return tuple(THPVariable_Wrap(weights), THPVariable_Wrap(experts));
+}
+
+// dweights, logits, experts, scoring, whether to renormalize, scale, out
+PyObject *route_backward(PyObject *const *a) {
+    const Tensor &given_dweights = device_tensor("dweights", a[0]);
+    const at::Device dev = given_dweights.device();
+    const c10::DeviceGuard guard(dev);
+    const Matrix logits = matrix("logits", there("logits", a[1], dev));
+    TORCH_CHECK_VALUE(logits.width <= 1024, "at most 1024 experts (got ", logits.width, ")");
+    const Tensor &e = there("experts", a[2], dev);
+    TORCH_CHECK_TYPE(e.scalar_type() == ScalarType::Int, "experts must be int32 (got ",
+                     type_name(e.scalar_type()), ")");
+    TORCH_CHECK_VALUE(e.dim() == 2 && e.size(0) == logits.rows && e.size(1) >= 1 &&
+                          e.size(1) <= 64 && e.size(1) <= logits.width,
+                      "experts must have shape (tokens, k), k 1 to 64 and at most the number of "
+                      "experts (got ", shape_name(e.sizes()), ")");
+    TORCH_CHECK_TYPE(given_dweights.scalar_type() == ScalarType::Float,
+                     "dweights must be torch.float32 (got ", type_name(given_dweights.scalar_type()),
+                     ")");
+    TORCH_CHECK_VALUE(given_dweights.sizes() == e.sizes(), "dweights must have experts' shape ",
+                      shape_name(e.sizes()), " (got ", shape_name(given_dweights.sizes()), ")");
+    const Tensor experts = e.contiguous(), dweights = given_dweights.contiguous();
+    const int32_t scoring = (int32_t)integer(a[3]);
+    const int renormalize = PyObject_IsTrue(a[4]);
+    if (renormalize < 0) throw python_error();
+    const double scale = real(a[5]);
+    const Matrix out = result("out", a[6], dev, logits.rows, logits.width, logits.t.scalar_type());
+    const int64_t k = e.size(1);
+    const int32_t *const chosen = static_cast<const int32_t *>(experts.data_ptr());
+    const float *const grads = static_cast<const float *>(dweights.data_ptr());
+    call("segtopk_route_backward", dev, [&](hipStream_t stream) {
+        return lib.route_backward(&logits.v, &out.v, chosen, grads, logits.rows, logits.width, k,
+                                  scoring, renormalize, scale, stream);
+    });
+    return output(a[6], out.t);
+}
+
+// ---- 8 bits ---------------------------------------------------------------
+constexpr ScalarType kBits8 = ScalarType::Float8_e4m3fn;
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Rows in 8 bits begin at multiples of 128 bytes.
+Tensor fresh8(std::vector<int64_t> shape, at::Device dev) {
+    const int64_t width = shape.back();
+    shape.back() = round_up(width, 128);
+    const Tensor t = fresh(shape, kBits8, dev);
+    return shape.back() == width ? t : t.narrow(-1, 0, width);
+}
+
+// x, position, offsets
+PyObject *quantize_rows(PyObject *const *a) {
+    const Tensor &given_x = device_tensor("x", a[0]);
+    const at::Device dev = given_x.device();
+    const c10::DeviceGuard guard(dev);
+    const Matrix x = matrix("x", given_x);
+    Slots s{{}, {}, x.rows, 1, nullptr, nullptr};
+    if (given(a[1])) s = slots(a[1], a[2], dev);
+    TORCH_CHECK_VALUE(x.rows == s.tokens, "position is for ", s.tokens, " tokens, x has ", x.rows,
+                      " rows");
+    const int64_t rows = s.tokens * s.k;
+    check_count("rows", rows);
+    const Tensor q = fresh8({rows, x.width}, dev);
+    const Tensor scales = fresh({rows, round_up(x.width, 128) / 128}, ScalarType::Float, dev);
+    const segtopk_rows v{q.data_ptr(), round_up(x.width, 128), SEGTOPK_E4M3};
+    float *const f = static_cast<float *>(scales.data_ptr());
+    call("segtopk_quantize_rows", dev, [&](hipStream_t stream) {
+        return lib.quantize_rows(&x.v, &v, f, s.tokens, s.k, x.width, s.at, s.kept, stream);
+    });
+    return tuple(THPVariable_Wrap(q), THPVariable_Wrap(scales));
+}
+
+// Matrices with a unit inner stride whose rows do not overlap, nor the matrices.
+bool plain_matrices(const Tensor &t) {
+    const auto s = t.sizes(), d = t.strides();
+    return (d[2] == 1 || s[2] <= 1) && (d[1] >= s[2] || s[1] <= 1) &&
+           (d[0] >= (s[1] - 1) * (s[1] > 1 ? d[1] : 0) + s[2] || s[0] <= 1);
+}
+segtopk_matrices view3(const Tensor &t, int code, int64_t least) {
+    // The stride of a single row or matrix is never used.
+    const int64_t stride = t.size(1) > 1 ? t.stride(1) : least;
+    return {t.data_ptr(), t.size(0) > 1 ? t.stride(0) : 0, stride, code};
+}
+
+PyObject *quantize_blocks(PyObject *const *a) {
+    const Tensor &given_x = device_tensor("x", a[0]);
+    const at::Device dev = given_x.device();
+    const c10::DeviceGuard guard(dev);
+    const ScalarType type = given_x.scalar_type();
+    TORCH_CHECK_TYPE(float_code(type) >= 0, "x must be float32, bfloat16 or float16 (got ",
+                     type_name(type), ")");
+    TORCH_CHECK_VALUE((given_x.dim() == 2 || given_x.dim() == 3) && given_x.size(-1) >= 1,
+                      "x must have shape (rows, width) or (matrices, rows, width) (got ",
+                      shape_name(given_x.sizes()), ")");
+    const bool one = given_x.dim() == 2;
+    Tensor x = one ? given_x.unsqueeze(0) : given_x;
+    if (!plain_matrices(x)) x = x.contiguous();
+    const int64_t m = x.size(0), rows = x.size(1), width = x.size(2);
+    check_count("matrices", m);
+    check_count("rows", rows);
+    const Tensor q = fresh8({m, rows, width}, dev);
+    const Tensor scales = fresh({m, round_up(rows, 128) / 128, round_up(width, 128) / 128},
+                                ScalarType::Float, dev);
+    const segtopk_matrices in = view3(x, float_code(type), width);
+    const int64_t stride = round_up(width, 128);
+    const segtopk_matrices to{q.data_ptr(), rows * stride, stride, SEGTOPK_E4M3};
+    float *const f = static_cast<float *>(scales.data_ptr());
+    call("segtopk_quantize_blocks", dev, [&](hipStream_t stream) {
+        return lib.quantize_blocks(&in, &to, f, m, rows, width, stream);
+    });
+    return tuple(THPVariable_Wrap(one ? q.squeeze(0) : q), THPVariable_Wrap(one ? scales.squeeze(0) : scales));
+}
+
+// The operand in 8 bits, copied where its rows do not begin at multiples of 16 bytes.
+Tensor bits8(const char *name, const Tensor &t, int64_t dim) {
+    TORCH_CHECK_TYPE(t.scalar_type() == kBits8, name, " must be torch.float8_e4m3fn (got ",
+                     type_name(t.scalar_type()), ")");
+    TORCH_CHECK_VALUE(t.dim() == dim && t.size(-1) >= 1, name, " must be ", dim,
+                      "-D and at least one element wide (got ", shape_name(t.sizes()), ")");
+    bool good = (t.stride(-1) == 1 || t.size(-1) == 1) &&
+                reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0;
+    for (int64_t d = 0; good && d + 1 < dim; ++d)
+        good = t.size(d) <= 1 || (t.stride(d) % 16 == 0 && t.stride(d) >= (d + 2 == dim ? t.size(-1) : 0));
+    if (good) return t;
+    Tensor c = fresh8(t.sizes().vec(), t.device());
+    c.copy_(t);
+    return c;
+}
+
+Tensor scales_of(const char *name, PyObject *o, at::Device dev, at::IntArrayRef shape) {
+    const Tensor &t = there(name, o, dev);
+    TORCH_CHECK_TYPE(t.scalar_type() == ScalarType::Float, name, " must be torch.float32 (got ",
+                     type_name(t.scalar_type()), ")");
+    TORCH_CHECK_VALUE(t.sizes() == shape, name, " must have shape ", shape_name(shape), " (got ",
+                      shape_name(t.sizes()), ")");
+    return t.contiguous();
+}
+
+ScalarType type_of(PyObject *dtype, PyObject *out, ScalarType otherwise) {
+    if (given(dtype)) {
+        TORCH_CHECK_TYPE(THPDtype_Check(dtype), "dtype must be a torch.dtype");
+        return reinterpret_cast<THPDtype *>(dtype)->scalar_type;
+    }
+    return given(out) ? tensor("out", out).scalar_type() : otherwise;
+}
+
+// rows, row_scales, weights, weight_scales, offsets, dtype, out
+PyObject *expert_matmul(PyObject *const *a) {
+    const Tensor &given_rows = device_tensor("rows", a[0]);
+    const at::Device dev = given_rows.device();
+    const c10::DeviceGuard guard(dev);
+    const Tensor rows = bits8("rows", given_rows, 2);
+    const Tensor weights = bits8("weights", there("weights", a[2], dev), 3);
+    const int64_t n = rows.size(0), depth = rows.size(1), experts = weights.size(0),
+                  width = weights.size(1);
+    TORCH_CHECK_VALUE(weights.size(2) == depth, "weights must be as deep as rows are wide (", depth,
+                      "; got ", shape_name(weights.sizes()), ")");
+    TORCH_CHECK_VALUE(experts >= 1 && experts <= 65535 && width >= 1,
+                      "weights must have shape (experts, width, depth), 1 to 65535 experts (got ",
+                      shape_name(weights.sizes()), ")");
+    const int64_t blocks = round_up(depth, 128) / 128;
+    const Tensor row_scales = scales_of("row_scales", a[1], dev, {n, blocks});
+    const Tensor weight_scales =
+        scales_of("weight_scales", a[3], dev, {experts, round_up(width, 128) / 128, blocks});
+    const Tensor offsets = offsets_of("offsets", a[4], dev);
+    TORCH_CHECK_VALUE(offsets.size(0) == experts + 1, "offsets must have ", experts + 1,
+                      " entries (got ", offsets.size(0), ")");
+    const ScalarType type = type_of(a[5], a[6], ScalarType::BFloat16);
+    TORCH_CHECK_TYPE(float_code(type) >= 0, "the result must be float32, bfloat16 or float16 (got ",
+                     type_name(type), ")");
+    const Matrix out = result("out", a[6], dev, n, width, type);
+    segtopk_expert_matmul_args q{};
+    q.rows = {rows.data_ptr(), n > 1 ? rows.stride(0) : round_up(depth, 16), SEGTOPK_E4M3};
+    q.out = out.v;
+    q.weights = view3(weights, SEGTOPK_E4M3, round_up(depth, 16));
+    q.row_scales = static_cast<const float *>(row_scales.data_ptr());
+    q.weight_scales = static_cast<const float *>(weight_scales.data_ptr());
+    q.offsets = static_cast<const int64_t *>(offsets.data_ptr());
+    q.num_rows = n;
+    q.num_experts = experts;
+    q.width = width;
+    q.depth = depth;
+    call("segtopk_expert_matmul", dev,
+         [&](hipStream_t stream) { return lib.expert_matmul(&q, stream); });
+    return output(a[6], out.t);
+}
+
+// dout, rows, offsets, dtype, out, accumulate
+PyObject *expert_dweights(PyObject *const *a) {
+    const Tensor &given_dout = device_tensor("dout", a[0]);
+    const at::Device dev = given_dout.device();
+    const c10::DeviceGuard guard(dev);
+    const Matrix dout = matrix("dout", given_dout);
+    const Matrix rows = matrix("rows", there("rows", a[1], dev));
+    const ScalarType in = dout.t.scalar_type();
+    TORCH_CHECK_TYPE(rows.t.scalar_type() == in, "rows must be ", type_name(in), " (got ",
+                     type_name(rows.t.scalar_type()), ")");
+    TORCH_CHECK_VALUE(rows.rows == dout.rows, "rows must have dout's ", dout.rows, " rows (got ",
+                      rows.rows, ")");
+    const Tensor offsets = offsets_of("offsets", a[2], dev);
+    const int64_t experts = offsets.size(0) - 1;
+    TORCH_CHECK_VALUE(experts >= 1 && experts <= 65535, "offsets must be for 1 to 65535 experts (got ",
+                      experts, ")");
+    const int accumulate = PyObject_IsTrue(a[5]);
+    if (accumulate < 0) throw python_error();
+    TORCH_CHECK_VALUE(!accumulate || given(a[4]), "accumulate needs out");
+    const ScalarType type = type_of(a[3], a[4], in);
+    TORCH_CHECK_TYPE(type == in || type == ScalarType::Float, "the gradient must be float32 or ",
+                     type_name(in), " (got ", type_name(type), ")");
+    Tensor out;
+    if (given(a[4])) {
+        out = there("out", a[4], dev);
+        TORCH_CHECK_TYPE(out.scalar_type() == type, "out must be ", type_name(type), " (got ",
+                         type_name(out.scalar_type()), ")");
+        TORCH_CHECK_VALUE(out.sizes() == at::IntArrayRef({experts, dout.width, rows.width}),
+                          "out must have shape ", shape_name({experts, dout.width, rows.width}),
+                          " (got ", shape_name(out.sizes()), ")");
+        TORCH_CHECK_VALUE(plain_matrices(out),
+                          "out must have a unit inner stride and rows that do not overlap");
+    } else {
+        out = fresh({experts, dout.width, rows.width}, type, dev);
+    }
+    segtopk_expert_dweights_args q{};
+    q.dout = dout.v;
+    q.rows = rows.v;
+    q.dweights = view3(out, float_code(type), rows.width);
+    q.offsets = static_cast<const int64_t *>(offsets.data_ptr());
+    q.num_rows = dout.rows;
+    q.num_experts = experts;
+    q.width = dout.width;
+    q.depth = rows.width;
+    q.accumulate = accumulate;
+    const Workspace ws =
+        workspace(lib.expert_dweights_workspace(q.num_rows, experts, q.width, q.depth), dev);
+    call("segtopk_expert_dweights", dev,
+         [&](hipStream_t stream) { return lib.expert_dweights(&q, ws.data, ws.bytes, stream); });
+    return output(a[4], out);
+}
+
+// target_logits, draft_tokens, draft_offsets, accept, sample, draft_logits, temperature
+PyObject *verify_drafts(PyObject *const *a) {
+    const Tensor &given_target = device_tensor("target_logits", a[0]);
+    const at::Device dev = given_target.device();
+    const c10::DeviceGuard guard(dev);
+    const Matrix target = matrix("target_logits", given_target);
+    const Ids ids = ids_of("draft_tokens", there("draft_tokens", a[1], dev));
+    TORCH_CHECK_VALUE(ids.t.dim() == 1, "draft_tokens must be 1-D (got ", shape_name(ids.t.sizes()),
+                      ")");
+    const Tensor offsets = offsets_of("draft_offsets", a[2], dev);
+    const int64_t drafts = ids.t.size(0), requests = offsets.size(0) - 1;
+    TORCH_CHECK_VALUE(target.rows == drafts + requests, "target_logits must have one row a draft and "
+                      "one a request (", drafts + requests, "; got ", target.rows, ")");
+    TORCH_CHECK_VALUE(drafts == 0 || requests > 0, "drafted tokens need a request");
+    const Tensor accept = vector("accept", a[3], dev, drafts);
+    const Tensor sample = vector("sample", a[4], dev, requests);
+    segtopk_verify_args q{};
+    Matrix draft{};
+    if (given(a[5])) {
+        draft = matrix("draft_logits", there("draft_logits", a[5], dev));
+        TORCH_CHECK_TYPE(draft.t.scalar_type() == target.t.scalar_type(), "draft_logits must be ",
+                         type_name(target.t.scalar_type()), " (got ",
+                         type_name(draft.t.scalar_type()), ")");
+        TORCH_CHECK_VALUE(draft.rows == drafts && draft.width == target.width,
+                          "draft_logits must have shape ", shape_name({drafts, target.width}),
+                          " (got ", shape_name({draft.rows, draft.width}), ")");
+        q.draft = draft.v;
+    }
+    Tensor temperatures;
+    if (THPVariable_Check(a[6])) {
+        temperatures = vector("temperature", a[6], dev, requests);
+        q.temperatures = static_cast<const float *>(temperatures.data_ptr());
+    } else {
+        q.temperature = real(a[6]);
+        TORCH_CHECK_VALUE(q.temperature >= 0.0 && q.temperature <= 1e300,
+                          "temperature must be finite and >= 0 (got ", q.temperature, ")");
+    }
+    const Tensor tokens = fresh({drafts + requests}, ids.t.scalar_type(), dev);
+    const Tensor counts = fresh({requests}, ScalarType::Int, dev);
+    q.target = target.v;
+    q.draft_tokens = ids.t.data_ptr();
+    q.id_type = ids.code;
+    q.draft_offsets = static_cast<const int64_t *>(offsets.data_ptr());
+    q.num_drafts = drafts;
+    q.num_requests = requests;
+    q.vocab = target.width;
+    q.accept = static_cast<const float *>(accept.data_ptr());
+    q.sample = static_cast<const float *>(sample.data_ptr());
+    q.tokens = tokens.data_ptr();
+    q.counts = static_cast<int32_t *>(counts.data_ptr());
+    const Workspace ws = workspace(lib.verify_workspace(drafts, requests, q.vocab), dev);
+    call("segtopk_verify_drafts", dev,
+         [&](hipStream_t stream) { return lib.verify_drafts(&q, ws.data, ws.bytes, stream); });
+    return tuple(THPVariable_Wrap(tokens), THPVariable_Wrap(counts));
+}
+
 // ---- the module ---------------------------------------------------------
 template <PyObject *(*CALL)(PyObject *const *), Py_ssize_t COUNT>
 PyObject *method(PyObject *, PyObject *const *args, Py_ssize_t count) {
@@ -521,6 +865,15 @@ PyObject *load(PyObject *const *a) {
     find(file, "segtopk_embedding_backward", lib.embedding_backward);
     find(file, "segtopk_policy_loss_workspace", lib.policy_loss_workspace);
     find(file, "segtopk_policy_loss", lib.policy_loss);
+    find(file, "segtopk_route", lib.route);
+    find(file, "segtopk_route_backward", lib.route_backward);
+    find(file, "segtopk_quantize_rows", lib.quantize_rows);
+    find(file, "segtopk_quantize_blocks", lib.quantize_blocks);
+    find(file, "segtopk_expert_matmul", lib.expert_matmul);
+    find(file, "segtopk_expert_dweights_workspace", lib.expert_dweights_workspace);
+    find(file, "segtopk_expert_dweights", lib.expert_dweights);
+    find(file, "segtopk_verify_workspace", lib.verify_workspace);
+    find(file, "segtopk_verify_drafts", lib.verify_drafts);
     Py_INCREF(a[1]);
     Py_XDECREF(call_error);
     call_error = a[1];
@@ -542,6 +895,13 @@ PyMethodDef methods[] = {
     entry<embedding, 4>("embedding"),
     entry<embedding_backward, 8>("embedding_backward"),
     entry<policy_loss, 13>("policy_loss"),
+    entry<route, 9>("route"),
+    entry<route_backward, 7>("route_backward"),
+    entry<quantize_rows, 3>("quantize_rows"),
+    entry<quantize_blocks, 1>("quantize_blocks"),
+    entry<expert_matmul, 7>("expert_matmul"),
+    entry<expert_dweights, 6>("expert_dweights"),
+    entry<verify_drafts, 7>("verify_drafts"),
     {nullptr, nullptr, 0, nullptr},
 };
 

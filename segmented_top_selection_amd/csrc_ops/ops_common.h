@@ -53,6 +53,8 @@ __device__ inline float wave_sum(float v) {
 }
 
 // ---- host ---------------------------------------------------------------
+// Workgroups of kOpThreads that one launch holds: fewer than 2^32 threads.
+constexpr int64_t kMostBlocks = (1 << 24) - 1;
 inline int element_bytes(int type) {
     return type == SEGTOPK_KEY_F32 ? 4
            : (type == SEGTOPK_KEY_BF16 || type == SEGTOPK_KEY_F16) ? 2 : 0;

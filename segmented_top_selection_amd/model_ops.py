@@ -4,8 +4,11 @@ A router's top-k picks each token's experts: ``sort_ids`` lists the slots
 expert by expert, ``dispatch`` copies the tokens into that order, ``combine``
 brings the experts' results back with the gate weights applied.  A sampler's
 top-k picks the next token: ``embedding`` looks it up, ``policy_loss`` scores
-sampled tokens under the model's logits.  The gradients are calls of their own
-(``*_backward``, ``policy_loss_grad``); none of them records an autograd graph.
+sampled tokens under the model's logits.  ``route`` is a router's whole selection, from
+scores to gate weights; ``dispatch_quantized`` and ``expert_matmul`` are the experts'
+products in 8 bits; ``verify_drafts`` says which tokens of a draft model stand.  The
+gradients are calls of their own
+(``*_backward``, ``policy_loss_grad``, ``expert_matmul_dweights``); none of them records an autograd graph.
 
 Like ``batched_topk`` these only marshal arguments, in ``_binding`` (built from
 csrc_ops/binding.cpp): tensor metadata is checked before anything is queued,
@@ -44,8 +47,48 @@ class _PolicyLossArgs(ctypes.Structure):
                 ("logp", ctypes.c_void_p)]
 
 
+class _Matrices(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("matrix_stride", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
+class _RouteArgs(ctypes.Structure):
+    _fields_ = [("logits", _Rows), ("tokens", ctypes.c_int64), ("num_experts", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("scoring", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_double), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int64),
+                ("kept_groups", ctypes.c_int64), ("group_best", ctypes.c_int32),
+                ("weights", ctypes.c_void_p), ("experts", ctypes.c_void_p)]
+
+
+class _ExpertMatmulArgs(ctypes.Structure):
+    _fields_ = [("rows", _Rows), ("out", _Rows), ("weights", _Matrices),
+                ("row_scales", ctypes.c_void_p), ("weight_scales", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+                ("num_experts", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("depth", ctypes.c_int64)]
+
+
+class _ExpertDweightsArgs(ctypes.Structure):
+    _fields_ = [("dout", _Rows), ("rows", _Rows), ("dweights", _Matrices),
+                ("offsets", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+                ("num_experts", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("depth", ctypes.c_int64), ("accumulate", ctypes.c_int32)]
+
+
+class _VerifyArgs(ctypes.Structure):
+    _fields_ = [("target", _Rows), ("draft", _Rows), ("draft_tokens", ctypes.c_void_p),
+                ("id_type", ctypes.c_int32), ("draft_offsets", ctypes.c_void_p),
+                ("num_drafts", ctypes.c_int64), ("num_requests", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("temperature", ctypes.c_double),
+                ("temperatures", ctypes.c_void_p), ("accept", ctypes.c_void_p),
+                ("sample", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p)]
+
+
 _P, _I64, _I32, _F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+_F64 = ctypes.c_double
 _R = ctypes.POINTER(_Rows)
+_M = ctypes.POINTER(_Matrices)
 _SIGNATURES = {
     "segtopk_sort_ids_workspace": (_I64, [_I64, _I64]),
     "segtopk_sort_ids": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P, _P, _I64, _P]),
@@ -59,6 +102,15 @@ _SIGNATURES = {
                                           _P, _I64, _P]),
     "segtopk_policy_loss_workspace": (_I64, [_I64, _I64, _I64]),
     "segtopk_policy_loss": (_I32, [ctypes.POINTER(_PolicyLossArgs), _P, _I64, _P]),
+    "segtopk_route": (_I32, [ctypes.POINTER(_RouteArgs), _P]),
+    "segtopk_route_backward": (_I32, [_R, _R, _P, _P, _I64, _I64, _I64, _I32, _I32, _F64, _P]),
+    "segtopk_quantize_rows": (_I32, [_R, _R, _P, _I64, _I64, _I64, _P, _P, _P]),
+    "segtopk_quantize_blocks": (_I32, [_M, _M, _P, _I64, _I64, _I64, _P]),
+    "segtopk_expert_matmul": (_I32, [ctypes.POINTER(_ExpertMatmulArgs), _P]),
+    "segtopk_expert_dweights_workspace": (_I64, [_I64, _I64, _I64, _I64]),
+    "segtopk_expert_dweights": (_I32, [ctypes.POINTER(_ExpertDweightsArgs), _P, _I64, _P]),
+    "segtopk_verify_workspace": (_I64, [_I64, _I64, _I64]),
+    "segtopk_verify_drafts": (_I32, [ctypes.POINTER(_VerifyArgs), _P, _I64, _P]),
 }
 
 
@@ -253,3 +305,173 @@ def policy_loss_grad(logits: torch.Tensor, token_ids: torch.Tensor, old_logp: to
     if stream is not None:
         return _on(stream, "policy_loss", *args)
     return _native.policy_loss(*args)
+
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(name: str) -> int:
+    if name not in _SCORING:
+        raise ValueError(f"scoring must be one of {', '.join(_SCORING)} (got {name!r})")
+    return _SCORING[name]
+
+
+def route(logits: torch.Tensor, k: int, *, scoring: str = "softmax",
+          bias: torch.Tensor | None = None, groups: int = 1, kept_groups: int | None = None,
+          group_best: int = 2, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """A router's selection, from logits to gate weights: (weights, experts).
+
+    logits       (tokens, experts)
+    scoring      p = "softmax" of a token's logits, or their "sigmoid"
+    bias         float32 (experts,), added to p for the choice alone
+    groups       experts form this many groups of neighbours; the kept_groups
+                 (default: all) best of them, by the sum of their group_best (1
+                 or 2) best p + bias, stay in the choice
+    renormalize  the chosen p are divided by their sum
+    Returns
+      weights  float32 (tokens, k): scale p of the chosen
+      experts  int32 (tokens, k): the k best by p + bias, best first, ties to the
+               lower index; -1, with weight 0, where none is left
+    A logit (or bias) of -inf rules an expert out.  Scores are compared in 64 bits.
+    ``experts`` is what sort_ids takes, which drops the -1; ``weights`` is combine's.
+    At most 1024 experts, 64 groups and k = 64.
+    """
+    args = (logits, k, _scoring(scoring), bias, groups, kept_groups, group_best, renormalize, scale)
+    if stream is not None:
+        return _on(stream, "route", *args)
+    return _native.route(*args)
+
+
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, *,
+                   scoring: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                   out: torch.Tensor | None = None, stream=None):
+    """The gradient of route in its logits, of their shape and dtype.
+
+    dweights  float32 (tokens, k), the gradient of route's weights
+    experts   int32 (tokens, k), the experts that it chose
+    The other arguments are route's; the choice, and with it the bias, has no gradient.
+    """
+    args = dweights, logits, experts, _scoring(scoring), renormalize, scale, out
+    if stream is not None:
+        return _on(stream, "route_backward", *args)
+    return _native.route_backward(*args)
+
+
+def quantize_rows(x: torch.Tensor, *, stream=None):
+    """Rows in 8 bits with a scale for each 128 columns: (rows, scales).
+
+    x is (rows, width).  Returns float8_e4m3fn of x's shape, its rows 128-byte
+    aligned, and float32 (rows, ceil(width / 128)):
+    scale = max |x| / 448 over the block (at least 2^-96 / 448), and
+    rows = x * (448 / max |x|) rounded to nearest even, so that x is about
+    rows * scale.
+    """
+    if stream is not None:
+        return _on(stream, "quantize_rows", x, None, None)
+    return _native.quantize_rows(x, None, None)
+
+
+def quantize_blocks(x: torch.Tensor, *, stream=None):
+    """Matrices in 8 bits with a scale for each block of 128 x 128: (matrices, scales).
+
+    x is (rows, width) or (matrices, rows, width), weights for instance; the scales
+    are float32 (..., ceil(rows / 128), ceil(width / 128)), made as by quantize_rows.
+    """
+    if stream is not None:
+        return _on(stream, "quantize_blocks", x)
+    return _native.quantize_blocks(x)
+
+
+def dispatch_quantized(x: torch.Tensor, position: torch.Tensor,
+                       offsets: torch.Tensor | None = None, *, stream=None):
+    """dispatch and quantize_rows in one: tokens in expert order, in 8 bits.
+
+    Takes dispatch's arguments; returns quantize_rows' (rows, scales) with
+    tokens * k rows.  Rows of dropped slots, and their scales, are zero.
+    """
+    if position is None:
+        raise TypeError("position must be a torch tensor")
+    if stream is not None:
+        return _on(stream, "quantize_rows", x, position, offsets)
+    return _native.quantize_rows(x, position, offsets)
+
+
+def expert_matmul(rows: torch.Tensor, row_scales: torch.Tensor, weights: torch.Tensor,
+                  weight_scales: torch.Tensor, offsets: torch.Tensor, *,
+                  dtype: torch.dtype | None = None, out: torch.Tensor | None = None, stream=None):
+    """Each row times its expert's transposed weights, both in 8 bits with scales.
+
+    rows           float8_e4m3fn (rows, depth) in expert order, and
+    row_scales     float32 (rows, ceil(depth / 128)): dispatch_quantized's, or
+                   quantize_rows' of rows that are in expert order
+    weights        float8_e4m3fn (experts, width, depth), and
+    weight_scales  float32 (experts, ceil(width / 128), ceil(depth / 128)):
+                   quantize_blocks'
+    offsets        int64 (experts + 1,) from sort_ids: expert e has the rows
+                   offsets[e] to offsets[e + 1]
+    dtype          of the result: bfloat16 (default), float16 or float32
+    Sums are held in 32 bits; for a result of 16 each eight products are added up with
+    the smaller cut off at 2^-13 of the largest, as the 8-bit matrix instruction does.
+    Returns (rows, width); rows from offsets[-1] on are zero.  Operands whose rows do not begin at multiples of 16 bytes are copied first.
+
+    The gradient of the rows is the same call on quantize_rows' of the result's
+    gradient, and the weights transposed:
+      weights.transpose(1, 2).contiguous(), weight_scales.transpose(1, 2).contiguous()
+    """
+    args = rows, row_scales, weights, weight_scales, offsets, dtype, out
+    if stream is not None:
+        return _on(stream, "expert_matmul", *args)
+    return _native.expert_matmul(*args)
+
+
+def expert_matmul_dweights(dout: torch.Tensor, rows: torch.Tensor, offsets: torch.Tensor, *,
+                           dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                           accumulate: bool = False, stream=None):
+    """The gradient of expert_matmul in its weights, (experts, width, depth):
+    for each expert the sum over its rows r of dout[r]^T rows[r].
+
+    dout        (rows, width), the gradient of the result
+    rows        (rows, depth) in expert order, of dout's dtype; dispatch's, before
+                they are taken to 8 bits
+    dtype       dout's (default) or float32
+    accumulate  add to ``out``, which is then required
+    Both are taken to 8 bits with a scale for each column and 128 rows of an expert;
+    sums are expert_matmul's.  Rows from offsets[-1] on are not read.
+    """
+    args = dout, rows, offsets, dtype, out, accumulate
+    if stream is not None:
+        return _on(stream, "expert_dweights", *args)
+    return _native.expert_dweights(*args)
+
+
+def verify_drafts(target_logits: torch.Tensor, draft_tokens: torch.Tensor,
+                  draft_offsets: torch.Tensor, accept: torch.Tensor, sample: torch.Tensor, *,
+                  draft_logits: torch.Tensor | None = None,
+                  temperature: float | torch.Tensor = 1.0, stream=None):
+    """Which drafted tokens stand, and the token behind them: (tokens, counts).
+
+    target_logits  (drafts + requests, vocab): each request's rows one behind the
+                   other, one for each of its drafted tokens and one more
+    draft_tokens   int32 or int64 (drafts,)
+    draft_offsets  int64 (requests + 1,), from 0 to drafts: request r drafted
+                   draft_tokens[draft_offsets[r]:draft_offsets[r + 1]]
+    accept         float32 (drafts,), and
+    sample         float32 (requests,): uniform numbers in [0, 1)
+    draft_logits   (drafts, vocab), what the drafted tokens were drawn from; None:
+                   they were certain
+    temperature    of both: a number or float32 (requests,); 0: the largest logit
+    With p and q the target's and the draft's probabilities, token t stands if
+    accept q(t) < p(t).  Behind the last that stands comes one more: drawn from
+    max(p - q, 0) at the first that does not, or from p behind all drafts, as the
+    lowest index whose running sum passes sample times the whole.
+    Returns
+      tokens  draft_tokens' dtype (drafts + requests,): request r's from
+              draft_offsets[r] + r on, -1 behind its last
+      counts  int32 (requests,): how many it gets
+    A logit of -inf is a token ruled out.  A row with NaN or +inf, or nothing but
+    -inf, has no distribution: its draft does not stand, and no token is drawn (-1).
+    """
+    args = (target_logits, draft_tokens, draft_offsets, accept, sample, draft_logits, temperature)
+    if stream is not None:
+        return _on(stream, "verify_drafts", *args)
+    return _native.verify_drafts(*args)
