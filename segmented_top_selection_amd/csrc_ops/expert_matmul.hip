@@ -78,17 +78,42 @@ __device__ inline Sums multiply(const Operand<EXACT> &a, const Operand<EXACT> &b
     }
 }
 
-typedef __attribute__((address_space(3))) void *LdsPtr;
-typedef const __attribute__((address_space(1))) void *GlobalPtr;
-template <int BYTES> __device__ inline void to_lds(const void *from, void *to) {
+// A descriptor of memory from `base` on, `bytes` of it: loads past them give zeros.
+typedef uint32_t Memory __attribute__((ext_vector_type(4)));
+__device__ inline Memory memory(const void *base, int64_t bytes) {
+    const uint64_t at = (uint64_t)(uintptr_t)base;
+    return Memory{(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu,
+                  bytes < 0xFFFFFFFFll ? (uint32_t)bytes : 0xFFFFFFFFu, 0x00020000u};
+}
+// BYTES a lane straight into LDS, lane after lane from `to` on; `to` and `at` are the
+// wave's.  No register is written but m0, which nothing else here uses.  The kernel waits for these loads itself (meet): seen
+// by the compiler, each would be waited for before the next read of LDS.
+template <int BYTES>
+__device__ inline void to_lds(Memory from, uint32_t lane_at, uint32_t at, uint32_t to) {
     static_assert(BYTES == 4 || BYTES == 16, "");
-    if constexpr (BYTES == 16) __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)to, 16, 0, 0);
-    else __builtin_amdgcn_global_load_lds((GlobalPtr)from, (LdsPtr)to, 4, 0, 0);
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                     :: "v"(lane_at), "s"(from), "s"(at), "s"(to) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                     :: "v"(lane_at), "s"(from), "s"(at), "s"(to) : "memory");
+}
+__device__ inline uint32_t lds_address(const void *p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
-// Waits until at most N of the wave's loads are under way.
-template <int N> __device__ inline void loads_left() {
-    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70 | 0xF00);
+// Waits until at most N of the wave's loads are under way, and for all of its LDS
+// instructions; then for the workgroup.  (The compiler's own barrier waits for all loads.)
+template <int N> __device__ inline void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+__device__ inline uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+// A number that is the same for the whole workgroup, by the scalar cache.
+__device__ inline float uniform_float(const float *p) {
+    return *(const __attribute__((address_space(4))) float *)(uintptr_t)p;
 }
 
 // Where the tile in LDS holds piece c of row r: rows are 128 bytes, and a row's 8
@@ -99,18 +124,24 @@ template <int NT> __device__ inline uint32_t swap_of(uint32_t r) {
 }
 
 // ROWS x 128 bytes of an operand into LDS, 8 rows to an instruction of a wave.
-template <int ROWS, int WAVES, int NT>
-__device__ inline void load_tile(const uint8_t *from, int64_t stride, uint32_t last, uint32_t k0,
-                                 uint32_t depth, uint8_t *to) {
-    const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+template <int ROWS, int WAVES, int NT> struct TileLoad {
+    static constexpr int N = ROWS / 8 / WAVES;
+    uint32_t at[N];  // of the lane's pieces in the first block
+
+    __device__ inline TileLoad(uint32_t stride, uint32_t wave) {
+        const uint32_t lane = threadIdx.x % 64;
 #pragma unroll
-    for (int i = 0; i < ROWS / 8 / WAVES; ++i) {
-        const uint32_t r0 = (i * WAVES + wave) * 8, r = r0 + lane / 8;
-        uint32_t at = k0 + ((lane % 8) ^ swap_of<NT>(r)) * 16;
-        if (at >= depth) at = 0;  // past the row's end: anything
-        to_lds<16>(from + (int64_t)(r < last ? r : last) * stride + at, to + r0 * 128);
+        for (int i = 0; i < N; ++i) {
+            const uint32_t r = (i * WAVES + wave) * 8 + lane / 8;
+            at[i] = r * stride + ((lane % 8) ^ swap_of<NT>(r)) * 16;
+        }
     }
-}
+    __device__ inline void load(Memory from, uint32_t k0, const uint8_t *to, uint32_t wave) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            to_lds<16>(from, at[i], k0, lds_address(to) + (i * WAVES + wave) * 1024);
+    }
+};
 
 // Zeros from byte `have` on of each row.
 template <int ROWS, int THREADS, int NT>
@@ -129,10 +160,10 @@ __device__ inline void clear_tail(uint8_t *tile, uint32_t have) {
     }
 }
 
-__device__ inline Frag fragment(const uint8_t *row, uint32_t swap) {
-    const uint32_t g = threadIdx.x % 64 / 16;
-    const Quarter a = *reinterpret_cast<const Quarter *>(row + (g ^ swap) * 16);
-    const Quarter b = *reinterpret_cast<const Quarter *>(row + ((g + 4) ^ swap) * 16);
+// 32 bytes of a row: the pieces g and g + 4 of lane group g, which lie 64 bytes apart.
+__device__ inline Frag fragment(const uint8_t *first, const uint8_t *second) {
+    const Quarter a = *reinterpret_cast<const Quarter *>(first);
+    const Quarter b = *reinterpret_cast<const Quarter *>(second);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -158,170 +189,282 @@ __device__ inline void store(T *p, const float *v, uint32_t have, bool accumulat
     }
 }
 
+// A tile of results: its expert, first row and column, how many rows there are from its
+// first to the expert's (matrix's) last, and the blocks that are summed over.
+struct Spot {
+    uint32_t expert, row, col, rows, first, blocks;
+};
+
+// What a workgroup multiplies for it; all in scalar registers.
+struct Work {
+    Memory rows, cols, row_scales, col_scales;
+    const float *sw;  // the scales of the wave's columns
+    int64_t out;      // the tile's first element
+    uint32_t blocks, depth, last_row, width;  // `width`: columns from its first to the matrix's last
+};
+
 // BM rows by BN columns, by WM x WN waves.  TURNED: the weights' gradient, where both
 // operands are transposed, have a scale for each index, and are summed over the
 // tiles of an expert.
+//
+// A workgroup to a CU (as many as LDS allows) takes tiles in turn; the next tile's first
+// block is on its way while this one's results are stored.
 template <class T, int BM, int BN, int WM, int WN, bool TURNED>
 __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
-    constexpr int kLoads = (BM + BN) / 8 / kWaves;
     constexpr bool kExact = std::is_same<T, float>::value;
     __shared__ __attribute__((aligned(16))) uint8_t row_tile[2][BM * 128];
     __shared__ __attribute__((aligned(16))) uint8_t col_tile[2][BN * 128];
     __shared__ __attribute__((aligned(16))) float row_scale[2][BM];
     __shared__ __attribute__((aligned(16))) float col_scale[2][TURNED ? BN : 4];
 
-    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const uint32_t wm = wave % WM, wn = wave / WM;
-    uint32_t blocks, k_first = 0, row0, expert, have_rows;
-    int64_t first_row = 0;
-    const uint32_t n0 = blockIdx.x % a.col_tiles * BN;
-    if constexpr (TURNED) {
-        const uint32_t rest = blockIdx.x / a.col_tiles;
-        row0 = rest % a.row_tiles * BM;
-        expert = rest / a.row_tiles;
-        // The expert's tiles of 128, and those before it.
-        uint32_t before = 0, own = 0;
-        for (uint32_t e0 = 0; e0 <= expert; e0 += 64) {
-            const uint32_t e = e0 + lane;
-            uint32_t n = 0;
-            if (e <= expert) {
-                const int64_t b = cut_offset(a.seg, e), end = cut_offset(a.seg, e + 1);
-                n = end > b ? (uint32_t)((end - b + 127) / 128) : 0u;
-            }
-            own = __shfl(n, (int)(expert & 63u));
-            if (e < expert) before += n;
-        }
-#pragma unroll
-        for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
-        before = before < a.seg.tiles_most ? before : a.seg.tiles_most;
-        own = own < a.seg.tiles_most - before ? own : a.seg.tiles_most - before;
-        k_first = before * 128;
-        blocks = own;
-        have_rows = a.height - row0;
-    } else {
-        const Tile t = find_tile(a.seg, blockIdx.x / a.col_tiles, BM);
-        expert = t.expert;
-        row0 = 0;
-        first_row = t.begin;
-        if (expert >= a.seg.experts) return;
-        have_rows = (uint32_t)(t.end - t.begin < BM ? t.end - t.begin : BM);
-        blocks = (a.depth + 127) / 128;
-    }
-    expert = __builtin_amdgcn_readfirstlane(expert);
-    blocks = __builtin_amdgcn_readfirstlane(blocks);
-    const uint32_t last_row = (have_rows < BM ? have_rows : BM) - 1;
-    const uint32_t last_col = (a.width - n0 < BN ? a.width - n0 : BN) - 1;
-    const uint8_t *rows = a.rows + (TURNED ? (int64_t)row0 : first_row) * a.row_stride + k_first;
-    const uint8_t *cols = a.cols + (TURNED ? (int64_t)0 : (int64_t)expert * a.col_matrix) +
-                          (int64_t)n0 * a.col_stride + k_first;
+    const uint32_t lane = threadIdx.x % 64;
+    const uint32_t wave = uniform(threadIdx.x / 64);
+    // The waves of one SIMD (0 and 4, say) have different rows: in a tile that is not
+    // full all SIMDs keep the same work.
+    const uint32_t wm = wave / WN, wn = wave % WN;
     const uint32_t depth_blocks = (a.depth + 127) / 128;
-    const uint32_t depth = TURNED ? blocks * 128 : a.depth;
+    Cursor cursor{0, 0};
 
-    Sums acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = Sums{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const auto load = [&](uint32_t b, int s) {
-        load_tile<BM, kWaves, 1>(rows, a.row_stride, last_row, b * 128, depth, row_tile[s]);
-        load_tile<BN, kWaves, NT>(cols, a.col_stride, last_col, b * 128, depth, col_tile[s]);
-        const uint32_t part = wave % ((BM + 63) / 64) * 64;
-        const uint32_t r = part + lane < last_row ? part + lane : last_row;
+    const auto locate = [&](uint32_t at) {
+        Spot s;
         if constexpr (TURNED) {
-            to_lds<4>(a.row_scales + (int64_t)(k_first / 128 + b) * a.height + row0 + r,
-                      row_scale[s] + part);
-            const uint32_t cpart = wave % ((BN + 63) / 64) * 64;
-            const uint32_t c = cpart + lane < last_col ? cpart + lane : last_col;
-            to_lds<4>(a.col_scales + (int64_t)(k_first / 128 + b) * a.width + n0 + c,
-                      col_scale[s] + cpart);
+            s.expert = at / (a.col_tiles * a.row_tiles);
+            const Place p = place_of(at % (a.col_tiles * a.row_tiles), a.row_tiles, a.col_tiles);
+            const Range r = tiles_of(a.seg, s.expert, 128, cursor);
+            // Offsets that are no segments may say anything.
+            s.first = uniform(r.first < a.seg.tiles_most ? r.first : a.seg.tiles_most);
+            const uint32_t count = uniform(r.count);
+            s.blocks = count < a.seg.tiles_most - s.first ? count : a.seg.tiles_most - s.first;
+            s.row = p.down * BM;
+            s.col = p.across * BN;
+            s.rows = a.height - s.row;
         } else {
-            to_lds<4>(a.row_scales + (first_row + r) * depth_blocks + b, row_scale[s] + part);
+            const Tile t = find_tile(a.seg, at, BM, a.col_tiles, cursor);
+            s.expert = uniform(t.expert);
+            s.col = uniform(t.column) * BN;
+            s.row = uniform((uint32_t)t.begin);  // below 2^31
+            s.rows = uniform((uint32_t)t.end) - s.row;
+            s.blocks = depth_blocks;
+            s.first = 0;
+        }
+        return s;
+    };
+    const auto work_of = [&](const Spot &s) {
+        Work w;
+        w.blocks = s.blocks;
+        w.depth = TURNED ? s.blocks * 128 : a.depth;
+        w.last_row = (s.rows < BM ? s.rows : BM) - 1;
+        w.width = a.width - s.col;
+        const uint32_t last_col = (w.width < BN ? w.width : BN) - 1;
+        const uint32_t reach = (w.depth + 15) & ~15u;  // of a row, in bytes
+        w.rows = memory(a.rows + (int64_t)s.row * a.row_stride + (int64_t)s.first * 128,
+                        (int64_t)w.last_row * a.row_stride + reach);
+        w.cols = memory(a.cols + (TURNED ? 0 : (int64_t)s.expert * a.col_matrix) +
+                            (int64_t)s.col * a.col_stride + (int64_t)s.first * 128,
+                        (int64_t)last_col * a.col_stride + reach);
+        if constexpr (TURNED) {
+            const int64_t behind = (int64_t)w.blocks - 1;
+            w.row_scales = memory(a.row_scales + (int64_t)s.first * a.height + s.row,
+                                  (behind * a.height + w.last_row + 1) * 4);
+            w.col_scales = memory(a.col_scales + (int64_t)s.first * a.width + s.col,
+                                  (behind * a.width + last_col + 1) * 4);
+            w.sw = nullptr;
+            w.out = (int64_t)s.expert * a.out_matrix + (int64_t)s.row * a.out_stride + s.col;
+        } else {
+            w.row_scales = memory(a.row_scales + (int64_t)s.row * depth_blocks,
+                                  (int64_t)(w.last_row + 1) * depth_blocks * 4);
+            w.col_scales = w.row_scales;
+            const uint32_t most = (a.width - 1) / 128, nb = (s.col + wn * NT * 16) / 128;
+            w.sw = a.col_scales +
+                   ((int64_t)s.expert * (most + 1) + (nb < most ? nb : most)) * depth_blocks;
+            w.out = (int64_t)s.row * a.out_stride + s.col;
+        }
+        return w;
+    };
+
+    const TileLoad<BM, kWaves, 1> row_load((uint32_t)a.row_stride, wave);
+    const TileLoad<BN, kWaves, NT> col_load((uint32_t)a.col_stride, wave);
+    // The scales of the rows: 64 of them a wave, some twice.
+    const uint32_t part = wave % ((BM + 63) / 64) * 64, cpart = wave % ((BN + 63) / 64) * 64;
+    const uint32_t row_scale_at = (part + lane) * (TURNED ? 4 : depth_blocks * 4);
+    const uint32_t scale_step = TURNED ? a.height * 4 : 4;
+    const auto load_rows = [&](const Work &w, uint32_t b, int s) {
+        row_load.load(w.rows, b * 128, row_tile[s], wave);
+        to_lds<4>(w.row_scales, row_scale_at, b * scale_step, lds_address(row_scale[s] + part));
+        if constexpr (TURNED)
+            to_lds<4>(w.col_scales, (cpart + lane) * 4, b * a.width * 4, lds_address(col_scale[s] + cpart));
+    };
+    const auto load_cols = [&](const Work &w, uint32_t b, int s) {
+        col_load.load(w.cols, b * 128, col_tile[s], wave);
+    };
+    constexpr int kRowLoads = BM / 8 / kWaves + (TURNED ? 2 : 1), kColLoads = BN / 8 / kWaves;
+    const auto start = [&](const Work &w) {
+        if (!w.blocks) return;
+        load_rows(w, 0, 0);
+        load_cols(w, 0, 0);
+        if (w.blocks > 1) load_cols(w, 1, 1);
+    };
+
+    const uint32_t l = lane % 16;
+    // Where the lane's pieces begin.  Four columns on, the pieces of a pair change places.
+    const uint32_t col0 = wn * NT * 16 + l / 4 * (4 * NT) + l % 4;
+    const uint32_t col_at = col0 * 128 + ((lane / 16) ^ swap_of<NT>(col0)) * 16;
+    const uint32_t row_at = (wm * MT * 16 + l) * 128 + ((lane / 16) ^ swap_of<1>(l)) * 16;
+    const auto col_operand = [&](int j, int s) {
+        const uint8_t *at = col_tile[s] + j * 512, *one = at + col_at, *two = at + (col_at ^ 64u);
+        return operand<kExact>(NT > 1 && j % 2 ? fragment(two, one) : fragment(one, two));
+    };
+    const auto row_operand = [&](int i, int s) {
+        const uint8_t *at = row_tile[s] + i * 2048;
+        return operand<kExact>(fragment(at + row_at, at + (row_at ^ 64u)));
+    };
+    Sums acc[MT][NT];
+    Operand<kExact> c[NT];
+    const auto read_cols = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) c[j] = col_operand(j, s);
+    };
+
+    // Block b.  Its columns are in registers, its rows in LDS; the next block's rows are on
+    // their way to the other half of theirs, and the columns of the one after that to the
+    // place of this block's.  Before the last row tile all waves wait for the next block's
+    // columns, which replace this one's in the registers as they are used.  Each product's
+    // sums are added up a product later.
+    constexpr int kAhead = 1;
+    const auto step = [&](const Work &w, uint32_t b, auto half) {
+        constexpr int s = decltype(half)::value;
+        const bool mine = wm * MT * 16 <= w.last_row;
+        const bool ragged = (w.depth & 127u) != 0;
+        const bool one_more = b + 1 < w.blocks, two_more = b + 2 < w.blocks;
+        const float cs = TURNED ? 1.0f : uniform_float(w.sw + b);
+        if (one_more) load_rows(w, b + 1, s ^ 1);
+        if (two_more) load_cols(w, b + 2, s);
+        Sums p[kAhead + 1], cscale[TURNED ? NT : 1];
+        float scale[MT];
+        Operand<kExact> r, next;
+        const auto read_scale = [&](int i) { scale[i] = row_scale[s][(wm * MT + i) * 16 + l]; };
+        const auto add = [&](int t) {
+            const int i = t / NT, j = t % NT;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                acc[i][j][x] = fmaf(p[t % (kAhead + 1)][x],
+                                    TURNED ? scale[i] * cscale[TURNED ? j : 0][x] : scale[i],
+                                    acc[i][j][x]);
+        };
+        if (mine) {
+            r = row_operand(0, s);
+            if constexpr (TURNED)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    cscale[j] = *reinterpret_cast<const Sums *>(
+                        &col_scale[s][wn * NT * 16 + lane / 16 * (4 * NT) + j * 4]);
+            read_scale(0);
+#pragma unroll
+            for (int i = 0; i < MT - 1; ++i) {
+                next = row_operand(i + 1, s);
+                read_scale(i + 1);
+                scale[i] *= cs;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int t = i * NT + j;
+                    p[t % (kAhead + 1)] = multiply<kExact>(c[j], r);
+                    if (t >= kAhead) add(t - kAhead);
+                }
+                r = next;
+            }
+        }
+        if (one_more) {
+            if (two_more) meet<kRowLoads + kColLoads>();
+            else meet<kRowLoads>();
+            if (ragged && b + 2 == w.blocks) {
+                clear_tail<BN, kThreads, NT>(col_tile[s ^ 1], w.depth - (b + 1) * 128);
+                meet<kRowLoads>();
+            }
+        }
+        if (mine) {
+            scale[MT - 1] *= cs;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int t = (MT - 1) * NT + j;
+                p[t % (kAhead + 1)] = multiply<kExact>(c[j], r);
+                c[j] = col_operand(j, s ^ 1);  // behind the last block: anything
+                add(t - kAhead);
+            }
+#pragma unroll
+            for (int t = MT * NT - kAhead; t < MT * NT; ++t) add(t);
+        }
+        if (one_more) {
+            if (two_more) meet<kColLoads>();
+            else meet<0>();
+            if (ragged && b + 2 == w.blocks) {
+                clear_tail<BM, kThreads, 1>(row_tile[s ^ 1], w.depth - (b + 1) * 128);
+                meet<0>();
+            }
         }
     };
-    const float *sw = nullptr;  // of the wave's columns
-    if constexpr (!TURNED) {
-        uint32_t nb = (n0 + wn * NT * 16) / 128;
-        const uint32_t most = (a.width - 1) / 128;
-        nb = __builtin_amdgcn_readfirstlane(nb < most ? nb : most);
-        sw = a.col_scales + ((int64_t)expert * (most + 1) + nb) * depth_blocks;
-    }
 
-    const auto compute = [&](uint32_t b, int s) {
-        const uint32_t l = lane % 16;
-        const float cs = TURNED ? 1.0f : sw[b];
-        Operand<kExact> c[NT];
-        Sums cscale[TURNED ? NT : 1];
+    // Workgroups go to the eight XCDs in turn.  Each XCD has a run of neighbouring tiles, so
+    // that an expert's operands are in one cache, or two.
+    const uint32_t all =
+        TURNED ? a.seg.experts * a.col_tiles * a.row_tiles : uniform(count_tiles(a.seg, BM)) * a.col_tiles;
+    const uint32_t each = (all + 7) / 8, begin = blockIdx.x % 8 * each;
+    const uint32_t end = begin + each < all ? begin + each : all, turn = gridDim.x / 8;
+    uint32_t at = begin + blockIdx.x / 8;
+    Work w;
+    if (at < end) {
+        w = work_of(locate(at));
+        start(w);
+    }
+    while (at < end) {
+        at += turn;
+        Spot next{};
+        if (at < end) next = locate(at);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const uint32_t n = wn * NT * 16 + l / 4 * (4 * NT) + j * 4 + l % 4;
-            c[j] = operand<kExact>(fragment(col_tile[s] + n * 128, swap_of<NT>(n)));
-            if constexpr (TURNED)
-                cscale[j] = *reinterpret_cast<const Sums *>(
-                    &col_scale[s][wn * NT * 16 + lane / 16 * (4 * NT) + j * 4]);
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = Sums{0.0f, 0.0f, 0.0f, 0.0f};
+        if (w.blocks) {
+            meet<0>();
+            if (w.blocks == 1 && (w.depth & 127u)) {
+                clear_tail<BM, kThreads, 1>(row_tile[0], w.depth);
+                clear_tail<BN, kThreads, NT>(col_tile[0], w.depth);
+                meet<0>();
+            }
+            read_cols(0);
+            meet<0>();
         }
+        for (uint32_t b = 0; b < w.blocks; b += 2) {
+            step(w, b, std::integral_constant<int, 0>{});
+            if (b + 1 < w.blocks) step(w, b + 1, std::integral_constant<int, 1>{});
+        }
+        meet<0>();  // nobody reads LDS any more
+        T *out = static_cast<T *>(a.out) + w.out;
+        const uint32_t last_row = w.last_row, width = w.width;
+        if (at < end) {
+            w = work_of(next);
+            start(w);
+        }
+        const uint32_t n = wn * NT * 16 + lane / 16 * (4 * NT);
+        const uint32_t have = n < width ? width - n : 0u;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const uint32_t m = (wm * MT + i) * 16 + l;
-            const Operand<kExact> r =
-                operand<kExact>(fragment(row_tile[s] + m * 128, swap_of<1>(m)));
-            const float scale = row_scale[s][m] * cs;
+            if (m <= last_row && have) {
+                float v[NT * 4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const Sums p = multiply<kExact>(c[j], r);
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    acc[i][j][x] = fmaf(p[x], TURNED ? scale * cscale[TURNED ? j : 0][x] : scale,
-                                        acc[i][j][x]);
+                for (int j = 0; j < NT * 4; ++j) v[j] = acc[i][j / 4][j % 4];
+                store<T, NT * 4>(out + (int64_t)m * a.out_stride + n, v, have, TURNED && a.accumulate);
             }
         }
-    };
-
-    if (blocks) load(0, 0);
-    for (uint32_t b = 0; b < blocks; ++b) {
-        const int s = b & 1;
-        if (b + 1 < blocks) {
-            load(b + 1, s ^ 1);
-            loads_left<kLoads + (TURNED ? 2 : 1)>();
-        } else {
-            loads_left<0>();
-        }
-        __syncthreads();
-        if (b + 1 == blocks && (depth & 127u)) {
-            clear_tail<BM, kThreads, 1>(row_tile[s], depth - b * 128);
-            clear_tail<BN, kThreads, NT>(col_tile[s], depth - b * 128);
-            __syncthreads();
-        }
-        compute(b, s);
-        __syncthreads();
     }
-
-    T *out = static_cast<T *>(a.out) +
-             (TURNED ? (int64_t)expert * a.out_matrix + (int64_t)row0 * a.out_stride
-                     : first_row * a.out_stride);
-    const uint32_t n = n0 + wn * NT * 16 + lane / 16 * (4 * NT);
-    const uint32_t have = n < a.width ? a.width - n : 0u;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const uint32_t m = (wm * MT + i) * 16 + lane % 16;
-        if (m <= last_row && have) {
-            float v[NT * 4];
-#pragma unroll
-            for (int j = 0; j < NT * 4; ++j) v[j] = acc[i][j / 4][j % 4];
-            store<T, NT * 4>(out + (int64_t)m * a.out_stride + n, v, have, TURNED && a.accumulate);
+    if constexpr (!TURNED) {  // the rows behind the last expert's
+        const int64_t first = cut_offset(a.seg, a.seg.experts);
+        for (int64_t r = first + blockIdx.x; r < a.seg.rows; r += gridDim.x) {
+            T *row = static_cast<T *>(a.out) + r * a.out_stride;
+            for (uint32_t n = threadIdx.x; n < a.width; n += kThreads) row[n] = (T)0.0f;
         }
-    }
-}
-
-// The rows behind the last expert's: zeros.
-template <class T>
-__global__ __launch_bounds__(kOpThreads) void clear_rows_kernel(MulArgs a) {
-    const int64_t first = cut_offset(a.seg, a.seg.experts);
-    for (int64_t r = first + blockIdx.x; r < a.seg.rows; r += gridDim.x) {
-        T *row = static_cast<T *>(a.out) + r * a.out_stride;
-        for (uint32_t n = threadIdx.x; n < a.width; n += kOpThreads) row[n] = (T)0.0f;
     }
 }
 
@@ -329,6 +472,16 @@ bool good_sizes(int64_t rows, int64_t experts, int64_t width, int64_t depth) {
     const int64_t most = INT32_MAX - 1024;
     return rows >= 0 && rows < most && experts >= 1 && experts <= 65535 && width >= 1 &&
            width < most && depth >= 1 && depth < most;
+}
+
+// Rows of a tile are found by 32 bits from its first.
+constexpr int64_t kMostStride = (1 << 24) - 1;
+
+// Workgroups for so many tiles: those that the device holds at once, by their LDS, and a
+// multiple of the XCDs.
+unsigned groups_of(int64_t tiles, int bm, int bn) {
+    const int64_t held = 256 * (bm + bn <= 256 ? 2 : 1);
+    return (unsigned)(tiles < held ? (tiles + 7) / 8 * 8 : held);
 }
 
 struct DweightsSpace {
@@ -376,6 +529,7 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
     a.seg = {q.offsets, q.num_rows, (uint32_t)q.num_experts, 0};
     a.width = (uint32_t)q.width;
     a.depth = (uint32_t)q.depth;
+    if (q.rows.stride > kMostStride || q.weights.stride > kMostStride) return SEGTOPK_NOT_SUPPORTED;
     return with_type(q.out.type, [&](auto v) -> int {
         using T = decltype(v);
         const auto go = [&](auto bm, auto bn, auto wm, auto wn) -> int {
@@ -384,13 +538,17 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
             a.col_tiles = (a.width + BN - 1) / BN;
             const int64_t tiles = tiles_most(q.num_rows, q.num_experts, BM);
             if (tiles > kMostBlocks / a.col_tiles) return SEGTOPK_NOT_SUPPORTED;
-            if (launch(product_kernel<T, BM, BN, WM, WN, false>,
-                       dim3((unsigned)(tiles * a.col_tiles)), WM * WN * 64, stream, 0,
-                       a) != hipSuccess)
-                return SEGTOPK_HIP_ERROR;
-            return status(launch(clear_rows_kernel<T>, dim3(256), kOpThreads, stream, 0, a));
+            return status(launch(product_kernel<T, BM, BN, WM, WN, false>,
+                                 dim3(groups_of(tiles * a.col_tiles, BM, BN)), WM * WN * 64, stream,
+                                 0, a));
         };
         using std::integral_constant;
+        if constexpr (sizeof(T) == 4)
+            return go(integral_constant<int, 128>{}, integral_constant<int, 128>{},
+                  integral_constant<int, 2>{}, integral_constant<int, 2>{});
+        if (q.num_rows >= 64 * q.num_experts)
+            return go(integral_constant<int, 256>{}, integral_constant<int, 256>{},
+                      integral_constant<int, 2>{}, integral_constant<int, 4>{});
         return go(integral_constant<int, 128>{}, integral_constant<int, 128>{},
                   integral_constant<int, 2>{}, integral_constant<int, 2>{});
     });
@@ -442,7 +600,7 @@ extern "C" int segtopk_expert_dweights(const segtopk_expert_dweights_args *args,
     a.col_tiles = (a.width + BN - 1) / BN;
     a.row_tiles = (a.height + BM - 1) / BM;
     const int64_t matrix = (int64_t)a.col_tiles * a.row_tiles;
-    if (matrix > kMostBlocks / q.num_experts) return SEGTOPK_NOT_SUPPORTED;
+    if (matrix > kMostBlocks / q.num_experts || s.stride > kMostStride) return SEGTOPK_NOT_SUPPORTED;
     if (s.tiles) {
         int r = queue_quantize_turned(q.dout, dout, seg, stream);
         if (r == SEGTOPK_OK) r = queue_quantize_turned(q.rows, rows, seg, stream);
@@ -451,6 +609,6 @@ extern "C" int segtopk_expert_dweights(const segtopk_expert_dweights_args *args,
     return with_type(d.type, [&](auto v) {
         using T = decltype(v);
         return status(launch(product_kernel<T, BM, BN, 2, 2, true>,
-                             dim3((unsigned)(matrix * q.num_experts)), 256, stream, 0, a));
+                             dim3(groups_of(matrix * q.num_experts, BM, BN)), 256, stream, 0, a));
     });
 }

@@ -150,7 +150,8 @@ __global__ __launch_bounds__(kOpThreads) void quantize_turned_kernel(const T *x,
     __shared__ __attribute__((aligned(16))) uint8_t tile[kTurnCols * kTurnStride];
     const uint32_t cols = (t.width + kTurnCols - 1) / kTurnCols;
     const uint32_t c0 = blockIdx.x % cols * kTurnCols, b = blockIdx.x / cols;
-    const Tile mine = find_tile(seg, b, 128);
+    Cursor cursor{0, 0};
+    const Tile mine = find_tile(seg, b, 128, 1, cursor);
     if (mine.expert >= seg.experts) return;
     const uint32_t i = threadIdx.x, col = i % 8 * 8, row = i / 8 * 4;
     const uint32_t have = c0 + col < t.width ? t.width - c0 - col : 0u;
