@@ -468,6 +468,126 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
     }
 }
 
+// The same for few rows an expert, where reading the weights is all there is: 16 * MT
+// rows by 16 * NT columns, the blocks of 128 shared among the waves, each of which reads
+// its operands into registers; what the waves have is added up in LDS.
+template <class T, int MT, int NT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void thin_kernel(MulArgs a) {
+    constexpr bool kExact = std::is_same<T, float>::value;
+    constexpr int BM = MT * 16, BN = NT * 16, kStride = BN + 4, kAtOnce = 2;
+    __shared__ __attribute__((aligned(16))) float part[WAVES][BM][kStride];
+    const uint32_t lane = threadIdx.x % 64, l = lane % 16, g = lane / 16;
+    const uint32_t wave = uniform(threadIdx.x / 64);
+    Cursor cursor{0, 0};
+    const Tile t = find_tile(a.seg, blockIdx.x, BM, a.col_tiles, cursor);
+    if (t.expert >= a.seg.experts) {  // the rows behind the last expert's
+        const int64_t first = cut_offset(a.seg, a.seg.experts);
+        const uint32_t place = blockIdx.x - cursor.before * a.col_tiles;
+        for (int64_t r = first + place; r < a.seg.rows; r += gridDim.x - cursor.before * a.col_tiles) {
+            T *row = static_cast<T *>(a.out) + r * a.out_stride;
+            for (uint32_t n = threadIdx.x; n < a.width; n += WAVES * 64) row[n] = (T)0.0f;
+        }
+        return;
+    }
+    const uint32_t expert = uniform(t.expert), n0 = uniform(t.column) * BN;
+    const uint32_t row0 = uniform((uint32_t)t.begin);
+    const uint32_t rows = uniform((uint32_t)t.end) - row0, last_row = (rows < BM ? rows : BM) - 1;
+    const uint32_t last_col = (a.width - n0 < BN ? a.width - n0 : BN) - 1;
+    const uint32_t blocks = (a.depth + 127) / 128;
+    const uint8_t *row[MT], *col[NT];
+    const float *row_scale[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const uint32_t m = i * 16 + l < last_row ? i * 16 + l : last_row;
+        row[i] = a.rows + (int64_t)(row0 + m) * a.row_stride;
+        row_scale[i] = a.row_scales + (int64_t)(row0 + m) * blocks;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const uint32_t n = j * 16 + l < last_col ? j * 16 + l : last_col;
+        col[j] = a.cols + (int64_t)expert * a.col_matrix + (int64_t)(n0 + n) * a.col_stride;
+    }
+    const float *sw = a.col_scales + ((int64_t)expert * ((a.width + 127) / 128) + n0 / 128) * blocks;
+
+    // The pieces g and g + 4 of a block; of the last, what is inside the row.
+    const auto read = [&](const uint8_t *p, uint32_t b) {
+        Quarter q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = b * 128 + (g + 4 * h) * 16;
+            if (b * 128 + 128 <= a.depth) {
+                q[h] = *reinterpret_cast<const Quarter *>(p + at);
+            } else {
+                q[h] = *reinterpret_cast<const Quarter *>(p + (at < a.depth ? at : 0u));
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int have = (int)a.depth - (int)(at + w * 4);
+                    q[h][w] &= have >= 4 ? -1 : have <= 0 ? 0 : (int)((1u << (have * 8)) - 1u);
+                }
+            }
+        }
+        return __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    Sums acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = Sums{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto go = [&](uint32_t b, auto count) {
+        constexpr int N = decltype(count)::value;
+        Frag r[N][MT], c[N][NT];
+        float scale[N][MT];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) c[u][j] = read(col[j], b + u * WAVES);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                r[u][i] = read(row[i], b + u * WAVES);
+                scale[u][i] = row_scale[i][b + u * WAVES];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const float cs = uniform_float(sw + b + u * WAVES);
+            Operand<kExact> wide[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wide[j] = operand<kExact>(c[u][j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const Operand<kExact> one = operand<kExact>(r[u][i]);
+                const float s = scale[u][i] * cs;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const Sums p = multiply<kExact>(wide[j], one);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(p[x], s, acc[i][j][x]);
+                }
+            }
+        }
+    };
+    uint32_t b = wave;
+    for (; b + WAVES * (kAtOnce - 1) < blocks; b += WAVES * kAtOnce)
+        go(b, std::integral_constant<int, kAtOnce>{});
+    for (; b < blocks; b += WAVES) go(b, std::integral_constant<int, 1>{});
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<Sums *>(&part[wave][i * 16 + l][j * 16 + g * 4]) = acc[i][j];
+    __syncthreads();
+    T *out = static_cast<T *>(a.out) + (int64_t)row0 * a.out_stride + n0;
+    for (uint32_t u = threadIdx.x; u < BM * BN / 4; u += WAVES * 64) {
+        const uint32_t m = u / (BN / 4), n = u % (BN / 4) * 4;
+        if (m > last_row || n > last_col) continue;
+        Sums s = *reinterpret_cast<const Sums *>(&part[0][m][n]);
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) s += *reinterpret_cast<const Sums *>(&part[w][m][n]);
+        const float v[4] = {s[0], s[1], s[2], s[3]};
+        store<T, 4>(out + (int64_t)m * a.out_stride + n, v, last_col + 1 - n, false);
+    }
+}
+
 bool good_sizes(int64_t rows, int64_t experts, int64_t width, int64_t depth) {
     const int64_t most = INT32_MAX - 1024;
     return rows >= 0 && rows < most && experts >= 1 && experts <= 65535 && width >= 1 &&
@@ -543,6 +663,34 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
                                  0, a));
         };
         using std::integral_constant;
+        const auto thin = [&](auto mt, auto nt) -> int {
+            constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, kWaves = 4;
+            a.col_tiles = (a.width + NT * 16 - 1) / (NT * 16);
+            const int64_t tiles = tiles_most(q.num_rows, q.num_experts, MT * 16) + 1;
+            if (tiles > kMostBlocks / a.col_tiles) return SEGTOPK_NOT_SUPPORTED;
+            return status(launch(thin_kernel<T, MT, NT, kWaves>, dim3((unsigned)(tiles * a.col_tiles)),
+                                 kWaves * 64, stream, 0, a));
+        };
+        const auto thin_by_width = [&](auto mt) -> int {
+            const int64_t tiles = tiles_most(q.num_rows, q.num_experts, decltype(mt)::value * 16);
+            return tiles * ((a.width + 63) / 64) >= 512   ? thin(mt, integral_constant<int, 4>{})
+                   : tiles * ((a.width + 31) / 32) >= 512 ? thin(mt, integral_constant<int, 2>{})
+                                                          : thin(mt, integral_constant<int, 1>{});
+        };
+        // By the rows of an average expert.  64 experts of 4096 to 2048, by 16, 32, 64 rows at a
+        // time and by tiles of 128 x 128: 8 rows each 96, 111, 126, 124 us; 16 rows 104, 114,
+        // 125, 122; 32 rows 192, 128, 135, 123.  Experts are not all alike, and one row too many
+        // reads the weights again, hence 12 and 24.  Where tiles would leave most of the device
+        // idle, the blocks shared among waves are quicker at any number: one expert of 4096 to
+        // 8192, by 16, 32, 64 rows and tiles, 16 rows 11, 15, 16, 29 us; 64 rows 35, 23, 20, 43;
+        // 256 rows (128 tiles) 83, 57, 47, 69; 512 rows 158, 109, 77, 70.
+        const int64_t each = (q.num_rows + q.num_experts - 1) / q.num_experts;
+        const int64_t squares =
+            tiles_most(q.num_rows, q.num_experts, 128) * ((a.width + 127) / 128);
+        const bool few = squares < 200;
+        if (each <= (few ? 16 : 12)) return thin_by_width(integral_constant<int, 1>{});
+        if (each <= (few ? 32 : 24)) return thin_by_width(integral_constant<int, 2>{});
+        if (few) return thin_by_width(integral_constant<int, 4>{});
         if constexpr (sizeof(T) == 4)
             return go(integral_constant<int, 128>{}, integral_constant<int, 128>{},
                   integral_constant<int, 2>{}, integral_constant<int, 2>{});
