@@ -600,7 +600,7 @@ constexpr int64_t kMostStride = (1 << 24) - 1;
 // Workgroups for so many tiles: those that the device holds at once, by their LDS, and a
 // multiple of the XCDs.
 unsigned groups_of(int64_t tiles, int bm, int bn) {
-    const int64_t held = 256 * (bm + bn <= 256 ? 2 : 1);
+    const int64_t held = 256 * (bm + bn <= 192 ? 3 : bm + bn <= 256 ? 2 : 1);
     return (unsigned)(tiles < held ? (tiles + 7) / 8 * 8 : held);
 }
 
@@ -691,14 +691,21 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
         if (each <= (few ? 16 : 12)) return thin_by_width(integral_constant<int, 1>{});
         if (each <= (few ? 32 : 24)) return thin_by_width(integral_constant<int, 2>{});
         if (few) return thin_by_width(integral_constant<int, 4>{});
-        if constexpr (sizeof(T) == 4)
-            return go(integral_constant<int, 128>{}, integral_constant<int, 128>{},
-                  integral_constant<int, 2>{}, integral_constant<int, 2>{});
-        if (q.num_rows >= 64 * q.num_experts)
-            return go(integral_constant<int, 256>{}, integral_constant<int, 256>{},
-                      integral_constant<int, 2>{}, integral_constant<int, 4>{});
-        return go(integral_constant<int, 128>{}, integral_constant<int, 128>{},
-                  integral_constant<int, 2>{}, integral_constant<int, 2>{});
+        // Larger tiles read less for each product, smaller ones fill the device and waste less
+        // of an expert's last tile.  In bf16 by tiles of 64 x 128, 128 x 128 and 256 x 256: 64
+        // experts of 4096 to 2048, 32 rows each 127, 130, 137 us; 128 rows 196, 188, 229; 256
+        // rows 319, 263, 317; 128 experts, 512 rows each 1259, 941, 810.  In f32 1700, 1423 and
+        // (256 x 128) 1406; 37 experts of 1008 to 777, 81 rows each 21, 30, 42.
+        const integral_constant<int, 2> two;
+        const integral_constant<int, 128> middle;
+        if constexpr (sizeof(T) == 2) {
+            const integral_constant<int, 256> large;
+            const int64_t tiles =
+                tiles_most(q.num_rows, q.num_experts, 256) * ((a.width + 255) / 256);
+            if (each >= 384 && tiles >= 256) return go(large, large, two, integral_constant<int, 4>{});
+        }
+        if (squares < 512) return go(integral_constant<int, 64>{}, middle, two, two);
+        return go(middle, middle, two, two);
     });
 }
 
