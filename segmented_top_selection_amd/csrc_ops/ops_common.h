@@ -52,6 +52,36 @@ __device__ inline float wave_sum(float v) {
     return v;
 }
 
+// Lane i's value from the lane that step D of a butterfly pairs it with; the
+// steps below 16 pair lanes whose halves already agree, so that a mirror serves.
+template <int D> __device__ inline uint32_t partner(uint32_t v) {
+    if constexpr (D == 1) return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, false);
+    else if constexpr (D == 2) return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false);
+    else if constexpr (D == 4) return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, false);
+    else if constexpr (D == 8) return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, false);
+    else return __shfl_xor(v, D);
+}
+template <int D> __device__ inline float partner(float v) {
+    return __uint_as_float(partner<D>(__float_as_uint(v)));
+}
+template <int D> __device__ inline double partner(double v) {
+    const uint32_t lo = partner<D>((uint32_t)__double2loint(v));
+    const uint32_t hi = partner<D>((uint32_t)__double2hiint(v));
+    return __hiloint2double((int)hi, (int)lo);
+}
+
+// f over the L lanes (16 or 64) of a lane's own, for all of them.
+template <int L, class X, class F> __device__ inline X join(X v, F f) {
+    v = f(v, partner<1>(v));
+    v = f(v, partner<2>(v));
+    v = f(v, partner<4>(v));
+    v = f(v, partner<8>(v));
+    if constexpr (L > 16) {
+        v = f(v, partner<16>(v));
+        v = f(v, partner<32>(v));
+    }
+    return v;
+}
 // ---- host ---------------------------------------------------------------
 // Workgroups of kOpThreads that one launch holds: fewer than 2^32 threads.
 constexpr int64_t kMostBlocks = (1 << 24) - 1;

@@ -10,8 +10,8 @@
 // The running sum passes a border at each of some 10^5 tokens, a few 10^-6 of the
 // whole apart: sums of 32 bits, 10^-7 off, would pick another token once in a
 // hundred calls.  All is in 64 bits, whose vector rate is that of 32 here: 2^t is
-// a polynomial on [-1/2, 1/2] and a shift of the exponent, some 15 instructions for
-// an element that takes as long to load.
+// a polynomial on [-1/2, 1/2], 5e-11 off, and an addition to the exponent, some 15
+// instructions for an element that takes as long to load.
 //
 //   stats_kernel  every row in chunks: the maximum, the sum of 2^(x - max) (the
 //                 place of the maximum, for temperature 0)
@@ -27,8 +27,9 @@ namespace segtopk_ops {
 namespace {
 
 constexpr double kLog2e = 1.44269504088896340736;
-constexpr double kLn2 = 0.693147180559945309417;
-constexpr int kMostChunks = 64;  // of a row
+constexpr uint32_t kMostChunks = 16;   // of a row for its statistics, one to a lane of 16
+constexpr uint32_t kMostParts = 256;   // of the row that is drawn from, one to a thread
+constexpr uint32_t kPart = kOpThreads * 4;  // the least of its parts
 
 struct RowStat {
     double sum;  // of 2^((x - max) factor); NaN: no distribution
@@ -44,33 +45,51 @@ struct VerifyArgs {
     const float *temperatures, *accept, *sample;
     int32_t *counts;
     RowStat *stats;   // [rows][chunks]: the target's rows, then the drafts'
-    double *sums;     // [requests][chunks][2]: of w and of p
+    double *sums;     // [requests][parts][2]: of w and of p
     uint32_t *arrived;  // [requests]
     double temperature;
     uint32_t drafts, requests, vocab, wide, has_draft;
     uint32_t chunk, chunks;  // elements of a chunk, chunks of a row
+    uint32_t part, parts;    // the same of the row that is drawn from
 };
 
-// 2^t for t <= 0.  The series of 2^f up to f^9: 7e-12 off at most.
-__device__ inline double power2(double t) {
-    if (t < -1100.0) t = -1100.0;
-    const double n = rint(t), f = t - n;
-    constexpr double l = kLn2;
-    constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5,
-                     c6 = c5 * l / 6, c7 = c6 * l / 7, c8 = c7 * l / 8, c9 = c8 * l / 9;
-    double p = fma(f, c9, c8);
-    p = fma(p, f, c7);
-    p = fma(p, f, c6);
-    p = fma(p, f, c5);
-    p = fma(p, f, c4);
-    p = fma(p, f, c3);
-    p = fma(p, f, c2);
-    p = fma(p, f, l);
-    p = fma(p, f, 1.0);
-    return ldexp(p, (int)n);
+// 2^(x factor - shift), `shift` being max factor to the nearest integer, for x <= max: the
+// polynomial of degree 7 that goes through 2^f at the Chebyshev points of [-1/2, 1/2], and an
+// exponent.  Adding 1.5 * 2^52 leaves the nearest integer in the low bits, from where it goes
+// into the exponent.  What is below 2^-1018, -inf too, gives that.
+struct Power {
+    double factor, shift;
+};
+__device__ inline double shift_of(float max, double factor) {
+    return max == -INFINITY ? 0.0 : rint((double)max * factor);
 }
-
-__device__ inline float shift_of(float m) { return m == -INFINITY ? 0.0f : m; }
+__device__ inline Power power_of(float max, double factor) {
+    return {factor, shift_of(max, factor)};
+}
+// What a sum by one maximum is multiplied by to become one by a larger: a power of two.
+// (A sum by -inf is zero, and stays so.)
+__device__ inline double between(float from, float to, double factor) {
+    const double d = shift_of(from, factor) - shift_of(to, factor);
+    const int e = d > 0.0 ? 0 : d < -1020.0 ? -1020 : (int)d;
+    return __hiloint2double((1023 + e) << 20, 0);
+}
+__device__ inline double power(const Power &a, float v) {
+    constexpr double kRound = 6755399441055744.0;
+    const double t = fmax(fma((double)v, a.factor, -a.shift), -1018.0);
+    const double s = t + kRound, f = t - (s - kRound);
+    double p = fma(f, 1.5303700711365693e-05, 0.00015469729214118296);
+    p = fma(p, f, 0.0013333478473685416);
+    p = fma(p, f, 0.009618025613318034);
+    p = fma(p, f, 0.055504109063258665);
+    p = fma(p, f, 0.24022651213498092);
+    p = fma(p, f, 0.6931471805568324);
+    p = fma(p, f, 0.9999999999595618);
+    return __hiloint2double(__double2hiint(p) + (__double2loint(s) << 20), __double2loint(p));
+}
+// The same where what is ruled out, or as good as that, has to be nothing.
+__device__ inline double power_or_zero(const Power &a, float v) {
+    return fma((double)v, a.factor, -a.shift) < -1000.0 ? 0.0 : power(a, v);
+}
 
 __device__ inline int64_t draft_offset(const VerifyArgs &a, uint32_t r) {
     const int64_t v = a.offsets[r];
@@ -84,23 +103,6 @@ __device__ inline int64_t drafted(const VerifyArgs &a, int64_t i) {
 __device__ inline void put(const VerifyArgs &a, int64_t i, int64_t token) {
     if (a.wide) static_cast<int64_t *>(a.tokens)[i] = token;
     else static_cast<int32_t *>(a.tokens)[i] = (int32_t)token;
-}
-
-__device__ inline RowStat join(const RowStat &a, const RowStat &b, double factor, bool greedy) {
-    RowStat r;
-    r.max = a.max > b.max ? a.max : b.max;
-    if (greedy) {
-        r.sum = a.sum + b.sum;
-        r.at = a.max > b.max || (a.max == b.max && a.at < b.at) ? a.at : b.at;
-    } else {
-        const double m = (double)shift_of(r.max);
-        r.sum = a.sum * power2(((double)a.max - m) * factor) + b.sum * power2(((double)b.max - m) * factor);
-        r.at = 0;
-    }
-    return r;
-}
-__device__ inline RowStat from_lane(const RowStat &s, int d) {
-    return {__shfl_xor(s.sum, d), __shfl_xor(s.max, d), __shfl_xor(s.at, d)};
 }
 
 // The request of a row of the target, or of a draft.
@@ -118,11 +120,28 @@ __device__ inline double temperature_of(const VerifyArgs &a, uint32_t request) {
     return a.temperatures ? (double)a.temperatures[request] : a.temperature;
 }
 
+template <int L> __device__ inline float largest(float v) {
+    return join<L>(v, [](float a, float b) { return a > b ? a : b; });
+}
+template <int L> __device__ inline uint32_t lowest(uint32_t v) {
+    return join<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int L> __device__ inline double total_of(double v) {
+    return join<L>(v, [](double a, double b) { return a + b; });
+}
+
+// The statistics of L lanes as one.
+template <int L> __device__ inline RowStat join_lanes(const RowStat &s, double factor, bool greedy) {
+    const float m = largest<L>(s.max);
+    if (greedy) return {total_of<L>(s.sum), m, lowest<L>(s.max == m ? s.at : UINT32_MAX)};
+    return {total_of<L>(s.sum * between(s.max, m, factor)), m, 0u};
+}
+
 template <class T>
 __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, const T *draft,
                                                            VerifyArgs a) {
     using P = Piece<T>;
-    constexpr int kAtOnce = 2;
+    constexpr int kAtOnce = 4, kElements = kAtOnce * P::N;
     __shared__ RowStat part[kOpThreads / 64];
     const uint32_t chunk = blockIdx.x % a.chunks, row = blockIdx.x / a.chunks;
     const uint32_t targets = a.drafts + a.requests, i = threadIdx.x;
@@ -137,32 +156,38 @@ __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, cons
     const T *x = of_draft ? draft + (int64_t)r * a.draft_stride : target + (int64_t)r * a.target_stride;
     const uint32_t begin = chunk * a.chunk;
     const uint32_t end = a.vocab - begin < a.chunk ? a.vocab : begin + a.chunk;
-    RowStat st{0.0, -INFINITY, UINT32_MAX};
     // Pieces from the chunk's begin on; the elements past them one by one.
     const uint32_t pieces = (end - begin) / P::N;
     const T none = (T)-INFINITY;
-    const auto add = [&](const float *v, int n, uint32_t at0, uint32_t step) {
+    RowStat st{0.0, -INFINITY, UINT32_MAX};  // of the thread
+    bool odd = false;
+    const auto add = [&](const float *v, uint32_t at0) {
         float m = st.max;
-        bool odd = false;
-        for (int k = 0; k < n; ++k) {
-            if (greedy) {
-                if (v[k] > m) st.at = at0 + (uint32_t)(k / P::N) * step + (uint32_t)(k % P::N);
-                odd = odd || !(v[k] < INFINITY);
-            }
-            m = v[k] > m ? v[k] : m;
-        }
         if (greedy) {
-            if (odd) st.sum = NAN;
+#pragma unroll
+            for (int k = 0; k < kElements; ++k) {
+                odd = odd || !(v[k] < INFINITY);
+                if (v[k] > m) {
+                    st.at = at0 + (uint32_t)(k / P::N) * kOpThreads * P::N + k % P::N;
+                    m = v[k];
+                }
+            }
         } else {
-            const double o = (double)shift_of(m);
-            double s = st.sum * power2(((double)st.max - o) * factor);
-            for (int k = 0; k < n; ++k) s += power2(((double)v[k] - o) * factor);
+            // This maximum keeps NaN.
+#pragma unroll
+            for (int k = 0; k < kElements; k += 2)
+                m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, v[k]), v[k + 1]);
+            odd = odd || !(m < INFINITY);
+            const Power e = power_of(m, factor);
+            double s = st.sum * between(st.max, m, factor);
+#pragma unroll
+            for (int k = 0; k < kElements; ++k) s += power(e, v[k]);
             st.sum = s;
         }
         st.max = m;
     };
     for (uint32_t u0 = i; u0 < pieces; u0 += kOpThreads * kAtOnce) {
-        float v[kAtOnce * P::N];
+        float v[kElements];
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const uint32_t u = u0 + j * kOpThreads;
@@ -172,49 +197,92 @@ __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, cons
 #pragma unroll
             for (int k = 0; k < P::N; ++k) v[j * P::N + k] = f[k];
         }
-        add(v, kAtOnce * P::N, begin + u0 * P::N, kOpThreads * P::N);
+        add(v, begin + u0 * P::N);
     }
     const uint32_t single = begin + pieces * P::N + i;
     if (single < end) {
-        const float v[1] = {(float)x[single]};
-        add(v, 1, single, 0);
-    }
+        float v[kElements];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) st = join(st, from_lane(st, d), factor, greedy);
+        for (int k = 0; k < kElements; ++k) v[k] = -INFINITY;
+        v[0] = (float)x[single];
+        add(v, single);
+    }
+    if (odd) st.sum = NAN;
+    st = join_lanes<64>(st, factor, greedy);
     if (i % 64 == 0) part[i / 64] = st;
     __syncthreads();
-    if (i) return;
-    for (int w = 1; w < kOpThreads / 64; ++w) st = join(st, part[w], factor, greedy);
-    a.stats[(int64_t)row * a.chunks + chunk] = st;
+    if (i >= 16) return;
+    if (i < kOpThreads / 64) st = part[i];
+    else st = {0.0, -INFINITY, UINT32_MAX};
+    st = join_lanes<16>(st, factor, greedy);
+    if (i == 0) a.stats[(int64_t)row * a.chunks + chunk] = st;
 }
 
-// A row's statistics from those of its chunks.
+// A row's statistics from those of its chunks, by 16 lanes.
 __device__ inline RowStat row_stat(const VerifyArgs &a, int64_t row, double factor, bool greedy) {
-    const RowStat *s = a.stats + row * a.chunks;
-    RowStat st = s[0];
-    for (uint32_t c = 1; c < a.chunks; ++c) st = join(st, s[c], factor, greedy);
-    return st;
+    const uint32_t lane = threadIdx.x % 16;
+    RowStat s{0.0, -INFINITY, UINT32_MAX};
+    if (lane < a.chunks) s = a.stats[row * a.chunks + lane];
+    return join_lanes<16>(s, factor, greedy);
 }
 // Some logit is above -inf, and none is NaN or +inf.
 __device__ inline bool good(const RowStat &s) { return s.max > -INFINITY && s.sum == s.sum; }
 
 // What a request's token is drawn from.
 struct Source {
-    double max, inverse, draft_max, draft_inverse;  // of the rows
+    Power power, draft_power;
+    double inverse, draft_inverse;  // of the rows' sums
     int64_t row, draft;  // draft -1: none
     int64_t certain;     // the token that was certain and does not stand, or -1
+    uint32_t at;         // temperature 0: the token
 };
+
+// v of the lanes that come before by the DPP step, nothing for the others.
+template <int STEP, int ROWS> __device__ inline double from_before(double v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), STEP, ROWS, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), STEP, ROWS, 0xF, false);
+    return __hiloint2double(hi, lo);
+}
+// The sum of all threads' numbers before each, and of all.
+struct Scan {
+    double before, all;
+};
+// The sum of the wave's numbers up to each lane's.
+__device__ inline double scan_wave(double s) {
+    s += from_before<0x111, 0xF>(s);  // 1, 2, 4, 8 lanes before, within rows of 16
+    s += from_before<0x112, 0xF>(s);
+    s += from_before<0x114, 0xF>(s);
+    s += from_before<0x118, 0xF>(s);
+    s += from_before<0x142, 0xA>(s);  // the last of the row before, to rows 1 and 3
+    s += from_before<0x143, 0xC>(s);  // lane 31, to rows 2 and 3
+    return s;
+}
+__device__ inline Scan scan_threads(double v, double *part) {
+    const uint32_t i = threadIdx.x, lane = i % 64;
+    const double s = scan_wave(v);
+    __syncthreads();  // the last call's numbers have been read
+    if (lane == 63) part[i / 64] = s;
+    __syncthreads();
+    Scan r{s - v, 0.0};
+#pragma unroll
+    for (uint32_t w = 0; w < kOpThreads / 64; ++w) {
+        if (w < i / 64) r.before += part[w];
+        r.all += part[w];
+    }
+    return r;
+}
 
 template <class T>
 __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const T *draft,
                                                           VerifyArgs a) {
     using P = Piece<T>;
-    __shared__ uint32_t stop, arrival, chosen;
+    constexpr uint32_t kAtOnce = kOpThreads / 32;  // drafts
+    __shared__ uint32_t stop, arrival, chosen, last;
     __shared__ Source src;
-    __shared__ double scan[kOpThreads];
-    __shared__ double base, goal;
-    __shared__ uint32_t plain;
-    const uint32_t chunk = blockIdx.x % a.chunks, r = blockIdx.x / a.chunks, i = threadIdx.x;
+    __shared__ RowStat seen[kAtOnce][2];
+    __shared__ double likely[kAtOnce][2];
+    __shared__ double scan[kOpThreads / 64];
+    const uint32_t part = blockIdx.x % a.parts, r = blockIdx.x / a.parts, i = threadIdx.x;
     const int64_t first = draft_offset(a, r);
     const int64_t after = draft_offset(a, r + 1);
     const uint32_t n = after > first ? (uint32_t)(after - first) : 0u;
@@ -225,206 +293,234 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
     const int64_t targets = (int64_t)a.drafts + a.requests;
     const bool certain = greedy || !a.has_draft;
 
-    if (i == 0) stop = n;
-    __syncthreads();
-    for (uint32_t j0 = 0; j0 < n && stop == n; j0 += kOpThreads) {
-        const uint32_t j = j0 + i;
-        bool stands = true;
-        if (j < n) {
-            const int64_t t = drafted(a, first + j);
-            const RowStat s = row_stat(a, row0 + j, factor, greedy);
-            stands = t >= 0 && t < (int64_t)a.vocab && good(s);
-            if (stands && greedy) {
-                stands = t == (int64_t)s.at;
-            } else if (stands) {
-                const double x = (double)(float)target[(row0 + j) * a.target_stride + t];
-                const double p = power2((x - (double)s.max) * factor) / s.sum;
-                double q = 1.0;
-                if (!certain) {
-                    const RowStat d = row_stat(a, targets + first + j, factor, false);
-                    const double y = (double)(float)draft[(first + j) * a.draft_stride + t];
-                    q = power2((y - (double)d.max) * factor) / d.sum;
-                    stands = good(d);
-                }
-                stands = stands && (double)a.accept[first + j] * q < p;
-            }
+    // 16 lanes a row, the target's and the draft's of several drafts at once, until one does
+    // not stand; behind the last draft, its row.
+    const uint32_t local = i / 32, of_draft = i / 16 % 2;
+    for (uint32_t j0 = 0;; j0 += kAtOnce) {
+        const uint32_t j = j0 + local;
+        if (i == 0) stop = n;
+        const bool asked = j <= n && (!of_draft || (j < n && !certain));
+        RowStat s{0.0, -INFINITY, 0u};
+        int64_t t = -1;
+        if (asked) {
+            s = row_stat(a, of_draft ? targets + first + j : row0 + j, factor, greedy);
+            if (j < n) t = drafted(a, first + j);
         }
-        __syncthreads();  // everyone has looked at `stop`
-        if (!stands) atomicMin(&stop, j);
+        const bool inside = t >= 0 && t < (int64_t)a.vocab;
+        if (i % 16 == 0) {
+            double p = of_draft ? 1.0 : 0.0;  // of a draft that was certain
+            if (asked && inside && greedy) {
+                p = t == (int64_t)s.at ? 1.0 : 0.0;
+            } else if (asked && inside) {
+                const T v = of_draft ? draft[(first + j) * a.draft_stride + t]
+                                     : target[(row0 + j) * a.target_stride + t];
+                p = power_or_zero(power_of(s.max, factor), (float)v) / s.sum;
+            }
+            seen[local][of_draft] = s;
+            likely[local][of_draft] = p;
+        }
         __syncthreads();
-    }
-    const uint32_t stood = stop;
-    if (i == 0) {
-        const RowStat s = row_stat(a, row0 + stood, factor, greedy);
-        src.row = row0 + stood;
-        src.max = (double)s.max;
-        src.inverse = good(s) ? 1.0 / s.sum : NAN;
-        src.draft = src.certain = -1;
-        if (stood < n) {
-            if (certain) {
-                src.certain = drafted(a, first + stood);
-            } else {
-                src.draft = first + stood;
-                const RowStat d = row_stat(a, targets + first + stood, factor, false);
-                src.draft_max = (double)d.max;
-                src.draft_inverse = 1.0 / d.sum;
-                if (!good(d)) src.inverse = NAN;
-            }
+        if (i % 32 == 0 && j < n) {
+            const bool known = good(seen[local][0]) && (certain || good(seen[local][1]));
+            if (!(known && inside && (double)a.accept[first + j] * likely[local][1] < likely[local][0]))
+                atomicMin(&stop, j);
         }
-        if (greedy) chosen = s.at;
+        __syncthreads();
+        const uint32_t here = stop;
+        if (here < j0 + kAtOnce) {  // it has been looked at: a draft, or the row behind all
+            if (i == 0) {
+                const RowStat of_row = seen[here - j0][0], of_q = seen[here - j0][1];
+                src.row = row0 + here;
+                src.power = power_of(of_row.max, factor);
+                src.inverse = good(of_row) ? 1.0 / of_row.sum : NAN;
+                src.draft = src.certain = -1;
+                src.at = of_row.at;
+                if (here < n && certain) {
+                    src.certain = drafted(a, first + here);
+                } else if (here < n) {
+                    src.draft = first + here;
+                    src.draft_power = power_of(of_q.max, factor);
+                    src.draft_inverse = 1.0 / of_q.sum;
+                    if (!good(of_q)) src.inverse = NAN;
+                }
+            }
+            break;
+        }
     }
     __syncthreads();
-    const bool none = src.inverse != src.inverse;
-    if (chunk == 0) {
+    const uint32_t stood = (uint32_t)(src.row - row0);
+    const Source from = src;
+    const bool none = from.inverse != from.inverse;
+    if (part == 0) {
         for (uint32_t j = i; j <= n; j += kOpThreads)
             if (j < stood) put(a, row0 + j, drafted(a, first + j));
             else if (j > stood || none) put(a, row0 + j, -1);
-            else if (greedy) put(a, row0 + j, chosen);
+            else if (greedy) put(a, row0 + j, from.at);
         if (i == 0) a.counts[r] = (int32_t)(stood + (none ? 0u : 1u));
     }
     if (greedy || none) return;
 
-    const T *x = target + src.row * a.target_stride;
-    const T *y = src.draft >= 0 ? draft + src.draft * a.draft_stride : nullptr;
-    const auto probability = [&](float v) { return power2(((double)v - src.max) * factor) * src.inverse; };
+    const T *x = target + from.row * a.target_stride;
+    const T *y = from.draft >= 0 ? draft + from.draft * a.draft_stride : nullptr;
+    const auto probability = [&](float v) {
+        return power_or_zero(from.power, v) * from.inverse;
+    };
     const auto weight = [&](double p, float v, uint32_t c) {
-        if (y) p -= power2(((double)v - src.draft_max) * factor) * src.draft_inverse;
-        else if ((int64_t)c == src.certain) p = 0.0;
+        if (y) p -= power_or_zero(from.draft_power, v) * from.draft_inverse;
+        else if ((int64_t)c == from.certain) p = 0.0;
         return p > 0.0 ? p : 0.0;
     };
-    {
-        const uint32_t begin = chunk * a.chunk;
-        const uint32_t end = a.vocab - begin < a.chunk ? a.vocab : begin + a.chunk;
-        const uint32_t pieces = (end - begin) / P::N;
-        double w = 0.0, p = 0.0;
-        for (uint32_t u = i; u < pieces; u += kOpThreads) {
-            const uint32_t at = begin + u * P::N;
-            const typename P::f32 f = widen<T>(load_piece(x + at));
-            typename P::f32 g = f;
-            if (y) g = widen<T>(load_piece(y + at));
+    // What is added up of element c.
+    struct Both {
+        double w, p;
+    };
+    const auto both = [&](uint32_t c, float v, float g) {
+        const double p = probability(v);
+        return Both{weight(p, g, c), p};
+    };
+    // Twice the same code: the workgroup's own part, and, by the last to arrive, the part that
+    // the token is in.  A thread has a run of the part's elements, four at a time.
+    const uint32_t each = a.part / kOpThreads;
+    uint32_t which = part;
+    bool plain = false;
+    double base = 0.0, goal = 0.0;
+#pragma unroll 1
+    for (uint32_t pass = 0;; ++pass) {
+        const uint32_t begin = which * a.part;
+        const uint32_t end = a.vocab - begin < a.part ? a.vocab : begin + a.part;
+        const uint32_t run = begin + i * each, run_end = run + each < end ? run + each : end;
+        Both sum{0.0, 0.0};
+        typedef T four __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+        const auto read = [&](uint32_t c, four &one, four &two) {
+            one = two = (four)(T)-INFINITY;
+            if (c + 4 <= run_end) {
+                one = *reinterpret_cast<const four *>(x + c);
+                if (y) two = *reinterpret_cast<const four *>(y + c);
+            } else {
 #pragma unroll
-            for (int k = 0; k < P::N; ++k) {
-                const double one = probability(f[k]);
-                p += one;
-                w += weight(one, g[k], at + k);
+                for (int k = 0; k < 3; ++k)
+                    if (c + k < run_end) {
+                        one[k] = x[c + k];
+                        if (y) two[k] = y[c + k];
+                    }
             }
-        }
-        const uint32_t single = begin + pieces * P::N + i;
-        if (single < end) {
-            const double one = probability((float)x[single]);
-            p += one;
-            w += weight(one, y ? (float)y[single] : 0.0f, single);
-        }
+        };
+        four one, two;
+        read(run, one, two);
+#pragma unroll 1
+        for (uint32_t c = run; c < run_end; c += 4) {
+            four next_one, next_two;
+            read(c + 4, next_one, next_two);
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            w += __shfl_xor(w, d);
-            p += __shfl_xor(p, d);
+            for (int k = 0; k < 4; ++k) {
+                const Both e = both(c + k, (float)one[k], (float)two[k]);
+                sum.w += e.w;
+                sum.p += e.p;
+            }
+            one = next_one;
+            two = next_two;
         }
-        if (i % 64 == 0) {
-            scan[i / 64] = w;
-            scan[4 + i / 64] = p;
+        if (pass) {
+            // Whose run passes the goal; where rounding alone keeps it out of reach, the last
+            // with anything in it.
+            const double m = plain ? sum.p : sum.w;
+            const Scan s = scan_threads(m, scan);
+            if (m > 0.0) {
+                atomicMax(&last, i);
+                if (base + s.before + m > goal) atomicMin(&chosen, i);
+            }
+            __syncthreads();
+            const uint32_t owner = chosen < last ? chosen : last;
+            if (i == owner) scan[0] = base + s.before;
+            __syncthreads();
+            if (i >= 64) return;
+            // A wave looks at that run's elements, one to a lane.
+            double before = scan[0];
+            uint32_t token = 0;
+            const uint32_t from_here = begin + owner * each;
+            for (uint32_t at = 0; at < each; at += 64) {
+                const uint32_t c = from_here + at + i;
+                const bool mine = at + i < each && c < end;
+                double e = 0.0;
+                if (mine) {
+                    const Both one = both(c, (float)x[c], y ? (float)y[c] : 0.0f);
+                    e = plain ? one.p : one.w;
+                }
+                const double upto = scan_wave(e);
+                const uint64_t over = __ballot(e > 0.0 && before + upto > goal);
+                const uint64_t any = __ballot(e > 0.0);
+                if (any) token = from_here + at + 63u - (uint32_t)__builtin_clzll(any);
+                if (over) {
+                    token = from_here + at + (uint32_t)__builtin_ctzll(over);
+                    break;
+                }
+                before += __shfl(upto, 63);
+            }
+            if (i == 0) put(a, from.row, token);
+            return;
         }
-        __syncthreads();
+        sum.w = scan_threads(sum.w, scan).all;
+        sum.p = scan_threads(sum.p, scan).all;
         if (i == 0) {
-            for (int k = 1; k < kOpThreads / 64; ++k) {
-                w += scan[k];
-                p += scan[4 + k];
-            }
-            double *s = a.sums + ((int64_t)r * a.chunks + chunk) * 2;
-            __hip_atomic_store(s, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __hip_atomic_store(s + 1, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            // Both are past this XCD's cache before the chunk counts as done.
+            double *s = a.sums + ((int64_t)r * a.parts + part) * 2;
+            __hip_atomic_store(s, sum.w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(s + 1, sum.p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            // Both are past this XCD's cache before the part counts as done.
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             arrival = __hip_atomic_fetch_add(&a.arrived[r], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            chosen = UINT32_MAX;
+            last = 0u;
         }
-    }
-    __syncthreads();
-    if (arrival + 1u != a.chunks) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    if (i == 0) {
-        const double *s = a.sums + (int64_t)r * a.chunks * 2;
-        const auto sum_of = [&](uint32_t c, uint32_t which) {
-            return __hip_atomic_load(s + c * 2 + which, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        };
-        double total = 0.0;
-        for (uint32_t c = 0; c < a.chunks; ++c) total += sum_of(c, 0);
-        plain = total > 0.0 ? 0u : 1u;  // p is nowhere above q: p itself
-        if (plain)
-            for (uint32_t c = 0; c < a.chunks; ++c) total += sum_of(c, 1);
-        goal = (double)a.sample[r] * total;
-        // The first chunk that passes the goal, or the last with anything in it.
-        double before = 0.0;
-        chosen = 0;
-        base = 0.0;
-        for (uint32_t c = 0; c < a.chunks; ++c) {
-            const double v = sum_of(c, plain);
-            if (v > 0.0) {
-                chosen = c;
-                base = before;
-            }
-            before += v;
-            if (before > goal) break;
+        __syncthreads();
+        if (arrival + 1u != a.parts) return;
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        double w = 0.0, p = 0.0;  // of part i
+        if (i < a.parts) {
+            const double *s = a.sums + ((int64_t)r * a.parts + i) * 2;
+            w = __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            p = __hip_atomic_load(s + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-    }
-    __syncthreads();
-    const uint32_t begin = chosen * a.chunk;
-    const uint32_t end = a.vocab - begin < a.chunk ? a.vocab : begin + a.chunk;
-    const uint32_t each = (end - begin + kOpThreads - 1) / kOpThreads;
-    const uint32_t b = begin + i * each < end ? begin + i * each : end;
-    const uint32_t e = b + each < end ? b + each : end;
-    const auto weight_at = [&](uint32_t c) {
-        const double p = probability((float)x[c]);
-        return plain ? p : weight(p, y ? (float)y[c] : 0.0f, c);
-    };
-    double mine = 0.0;
-    for (uint32_t c = b; c < e; ++c) mine += weight_at(c);
-    scan[i] = mine;
-    __syncthreads();
-    double before = base;
-    for (uint32_t k = 0; k < i; ++k) before += scan[k];
-    __syncthreads();
-    if (i == 0) chosen = UINT32_MAX;
-    __syncthreads();
-    if (before + mine > goal) {  // here, or in a thread before
-        for (uint32_t c = b; c < e; ++c) {
-            const double w = weight_at(c);
-            before += w;
-            if (w > 0.0 && before > goal) {
-                atomicMin(&chosen, c);
-                break;
-            }
+        Scan sums = scan_threads(w, scan);
+        plain = !(sums.all > 0.0);  // p is nowhere above q: p itself
+        if (plain) {
+            sums = scan_threads(p, scan);
+            w = p;
         }
+        goal = (double)a.sample[r] * sums.all;
+        // The first part that passes the goal, or the last with anything in it.
+        if (w > 0.0 && sums.before + w > goal) atomicMin(&chosen, i);
+        if (w > 0.0) atomicMax(&last, i);
+        __syncthreads();
+        which = chosen < last ? chosen : last;
+        __syncthreads();
+        if (i == which) scan[0] = sums.before;
+        if (i == 0) chosen = UINT32_MAX;
+        if (i == 1) last = 0u;
+        __syncthreads();
+        base = scan[0];
     }
-    __syncthreads();
-    if (chosen == UINT32_MAX) {
-        // Rounding alone keeps the goal out of reach: the last of any weight.
-        __syncthreads();
-        if (i == 0) arrival = 0;
-        __syncthreads();
-        for (uint32_t c = e; c-- > b;)
-            if (weight_at(c) > 0.0) {
-                atomicMax(&arrival, c);
-                break;
-            }
-        __syncthreads();
-        if (i == 0) chosen = arrival;
-    }
-    if (i == 0) put(a, src.row, chosen);
 }
 
 struct Cut {
-    uint32_t chunk, chunks;
+    uint32_t chunk, chunks, part, parts;
 };
 
-// Chunks of 16384 elements, or less where there are few rows: a quarter is what a
-// workgroup takes at one go.
+// Chunks of 65536 elements, or less where there are few rows; parts of 1024 elements, or more
+// where there are many requests, so that all workgroups run at once.
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
-    int64_t chunk = 16384;
-    while (chunk > 4096 && rows * ((vocab + chunk - 1) / chunk) < 1024) chunk /= 2;
-    const int64_t least = (vocab + kMostChunks - 1) / kMostChunks;
-    if (chunk < least) chunk = (least + 4095) / 4096 * 4096;
-    return {(uint32_t)chunk, (uint32_t)((vocab + chunk - 1) / chunk)};
+    int64_t chunk = 65536;
+    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 2048) chunk /= 2;
+    const auto least = [&](int64_t size, int64_t most, int64_t unit) {
+        const int64_t n = (vocab + most - 1) / most;
+        return size < n ? (n + unit - 1) / unit * unit : size;
+    };
+    chunk = least(chunk, kMostChunks, 2048);
+    int64_t part = kPart;
+    while (requests * ((vocab + part - 1) / part) > 2048 && part < 16384) part *= 2;
+    part = least(part, kMostParts, kPart);
+    return {(uint32_t)chunk, (uint32_t)((vocab + chunk - 1) / chunk), (uint32_t)part,
+            (uint32_t)((vocab + part - 1) / part)};
 }
 
 bool good_verify_sizes(int64_t drafts, int64_t requests, int64_t vocab) {
@@ -439,7 +535,7 @@ VerifySpace verify_space(int64_t drafts, int64_t requests, const Cut &c) {
     VerifySpace s;
     s.stats = 0;
     s.sums = s.stats + (2 * drafts + requests) * c.chunks * (int64_t)sizeof(RowStat);
-    s.arrived = s.sums + requests * c.chunks * 16;
+    s.arrived = s.sums + requests * c.parts * 16;
     s.bytes = s.arrived + requests * 4;
     return s;
 }
@@ -475,7 +571,9 @@ extern "C" int segtopk_verify_drafts(const segtopk_verify_args *args, void *work
     if (has_draft && (!good_rows(&q.draft, q.vocab) || q.draft.type != q.target.type))
         return SEGTOPK_INVALID_ARGUMENT;
     const Cut cut = cut_of(q.num_drafts, q.num_requests, q.vocab);
-    if ((2 * q.num_drafts + q.num_requests) * cut.chunks > kMostBlocks) return SEGTOPK_NOT_SUPPORTED;
+    if ((2 * q.num_drafts + q.num_requests) * cut.chunks > kMostBlocks ||
+        q.num_requests * cut.parts > kMostBlocks)
+        return SEGTOPK_NOT_SUPPORTED;
     const VerifySpace s = verify_space(q.num_drafts, q.num_requests, cut);
     if (workspace_bytes < s.bytes) return SEGTOPK_SCRATCH_TOO_SMALL;
     if (!workspace || !aligned(workspace, 256)) return SEGTOPK_INVALID_ARGUMENT;
@@ -501,6 +599,8 @@ extern "C" int segtopk_verify_drafts(const segtopk_verify_args *args, void *work
     a.has_draft = has_draft;
     a.chunk = cut.chunk;
     a.chunks = cut.chunks;
+    a.part = cut.part;
+    a.parts = cut.parts;
     const unsigned rows = a.drafts + a.requests + (has_draft ? a.drafts : 0u);
     return with_type(q.target.type, [&](auto v) -> int {
         using T = decltype(v);
@@ -509,7 +609,7 @@ extern "C" int segtopk_verify_drafts(const segtopk_verify_args *args, void *work
         if (launch(stats_kernel<T>, dim3(rows * a.chunks), kOpThreads, stream, 0, target, draft,
                    a) != hipSuccess)
             return SEGTOPK_HIP_ERROR;
-        return status(launch(pick_kernel<T>, dim3(a.requests * a.chunks), kOpThreads, stream, 0,
+        return status(launch(pick_kernel<T>, dim3(a.requests * a.parts), kOpThreads, stream, 0,
                              target, draft, a));
     });
 }
