@@ -5,10 +5,11 @@
 //   their one or two best s;  the k best s of those;  w = scale p / (sum p | 1)
 //
 // Which experts are chosen has to be right to the last: s of two experts may be as
-// near as the inputs make them, so s is in 64 bits (2^-52 against the 2^-24 by
-// which 32 bits would swap neighbours among millions of pairs).  Where no bias and
-// no sum of two scores is asked for, s orders the experts as x does, and x itself
-// is compared.
+// near as the inputs make them.  Scores of 32 bits, as whole numbers with the expert's
+// place behind them, are compared first, and settle it where all that the choice hangs
+// on is further apart than they are off; else a wave compares them in 64 bits (2^-52).
+// Where no bias and no sum of two scores is asked for, s orders the experts as x does,
+// and x itself is compared.
 //
 // A token belongs to L lanes (16, so that four tokens share a wave's instructions,
 // or 64), and each group of experts to a power of two of them, V neighbouring
@@ -35,7 +36,10 @@ struct RouteArgs {
     double scale;
 };
 
-template <class X> __device__ inline X larger(X a, X b) { return a > b ? a : b; }
+// Of numbers without NaN.
+__device__ inline float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ inline double larger(double a, double b) { return a > b ? a : b; }
+__device__ inline uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 __device__ inline uint32_t lower(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 // The two best of a group, kept through a butterfly.
@@ -53,171 +57,349 @@ __device__ inline double log_sigmoid(double x) {
     return (x < 0.0 ? x : 0.0) - log1p(exp(-fabs(x)));
 }
 
-// S: the type that scores are compared in; float: they are the logits.
-template <class T, class S, int L, int V>
-__global__ __launch_bounds__(kOpThreads) void route_kernel(const T *logits, RouteArgs a) {
-    constexpr bool kWide = sizeof(S) == 8;
-    constexpr int kTokens = kOpThreads / L;
+// What a lane has of its token: its experts' logits, and where they are.
+template <int V> struct Mine {
+    float x[V];
+    uint32_t first, count, group;
+    float top;  // the softmax's shift
+};
+
+// V neighbouring numbers, of which there are `count`.
+template <int V, class T>
+__device__ inline void load_some(const T *from, uint32_t count, float otherwise, float *to) {
+    typedef T mem __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    if (count == (uint32_t)V) {
+        const mem v = *reinterpret_cast<const mem *>(from);
+#pragma unroll
+        for (int j = 0; j < V; ++j) to[j] = (float)v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) to[j] = (uint32_t)j < count ? (float)from[j] : otherwise;
+    }
+}
+// What lane `lane` of a token's has.
+template <int V, class T>
+__device__ inline Mine<V> mine_of(const T *row, const RouteArgs &a, uint32_t group_lanes,
+                                  uint32_t lane, bool live) {
+    Mine<V> m;
+    m.group = lane / group_lanes;
+    const uint32_t in_group = (lane % group_lanes) * V;
+    m.first = m.group * a.per_group + in_group;
+    m.count = !live || m.group >= a.groups || in_group >= a.per_group ? 0u
+              : a.per_group - in_group < (uint32_t)V               ? a.per_group - in_group
+                                                                   : (uint32_t)V;
+    load_some<V>(row + m.first, m.count, -INFINITY, m.x);
+    m.top = 0.0f;
+    return m;
+}
+
+// How scores are made: as the logits, or as p + bias in 32 or 64 bits.
+enum { kByLogits, kBy32, kBy64 };
+template <int HOW> struct ScoreType { using type = float; };
+template <> struct ScoreType<kBy64> { using type = double; };
+
+__device__ inline float exponential(float v) { return __expf(v); }
+__device__ inline double exponential(double v) { return exp(v); }
+
+// The scores of a lane's experts; what is ruled out has -inf, a NaN the lowest number.
+// Returns how far a score p of 32 bits is off at most: 4e-7 for the sigmoid, by its slope
+// times the exponential's error, |x| 2^-24 p (1 - p) and 2^-22 p (1 - p), and its own
+// roundings; 1.5e-6 of the largest p for the softmax, by the exponent's, (x - top) 2^-23 p, at
+// most 0.37 of it, the exponential's, and those of a sum of up to 32 + 6 terms and a quotient.
+template <int HOW, int L, int V, class S>
+__device__ inline float make_scores(const Mine<V> &a, const RouteArgs &q, S *s) {
+    float off = 0.0f;
+    if constexpr (HOW == kByLogits) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = a.x[j];
+    } else {
+        if (q.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const S d = (S)1 + exponential(-(S)a.x[j]);
+                if constexpr (HOW == kBy64) s[j] = 1.0 / d;
+                else s[j] = __builtin_amdgcn_rcpf(d);
+            }
+            off = 4e-7f;
+        } else {
+            S total = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) total += s[j] = exponential((S)a.x[j] - (S)a.top);
+            total = join<L>(total, [](S p, S r) { return p + r; });
+            const S one = (S)1 / total;
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] *= one;
+            off = 1.5e-6f * (float)one;
+        }
+        if (q.bias) {
+            float b[V];
+            load_some<V>(q.bias + a.first, a.count, 0.0f, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] += (S)b[j];
+        }
+    }
+    constexpr S kLowest = sizeof(S) == 8 ? (S)-1.7976931348623157e308 : (S)-3.4028234663852886e38f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (s[j] != s[j]) s[j] = kLowest;
+        if (a.x[j] == -INFINITY) s[j] = (S)-INFINITY;
+    }
+    return off;
+}
+
+// Rules out the experts of groups that are not kept.  With `off` (scores of 32 bits): whether
+// scores so far off, and by their sum's rounding, could make another choice.
+template <int L, int V, class S>
+__device__ inline bool keep_groups(const Mine<V> &a, const RouteArgs &q, S *s, float off) {
     constexpr S kNone = (S)-INFINITY;
-    __shared__ float chosen_x[kTokens][kMaxK];
+    if (q.kept >= q.groups) return false;
+    Best<S> b{kNone, kNone};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        b.second = larger(b.second, b.first < s[j] ? b.first : s[j]);
+        b.first = larger(b.first, s[j]);
+    }
+    if (q.group_lanes > 1) join_best<1>(b);
+    if (q.group_lanes > 2) join_best<2>(b);
+    if (q.group_lanes > 4) join_best<4>(b);
+    if (q.group_lanes > 8) join_best<8>(b);
+    if constexpr (L > 16) {
+        if (q.group_lanes > 16) join_best<16>(b);
+        if (q.group_lanes > 32) join_best<32>(b);
+    }
+    S score = b.first;
+    if (q.best > 1 && b.second != kNone) score += b.second;
+    uint32_t before = 0, perhaps = 0;
+    for (uint32_t g = 0; g < q.groups; ++g) {
+        const S other = __shfl(score, (int)(g * q.group_lanes), L);
+        if (off > 0.0f) {
+            // Two sums of two scores, each off by that, by a bias's rounding and its own.
+            const S by = (S)(4.0f * off + 0x1p-21f * (fabsf((float)score) + fabsf((float)other)));
+            const bool real = score != kNone && other != kNone;
+            before += real ? other > score + by : other > score || (other == score && g < a.group);
+            perhaps += real && g != a.group && other >= score - by;
+        } else {
+            before += other > score || (other == score && g < a.group);
+        }
+    }
+    if (before >= q.kept)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = kNone;
+    return off > 0.0f && a.group < q.groups && before < q.kept && perhaps >= q.kept;
+}
+
+// The k best by comparing scores, equal ones by their index.
+template <int HOW, int L, int V>
+__device__ inline void choose_exactly(const Mine<V> &a, const RouteArgs &q, int32_t *chosen) {
+    using S = typename ScoreType<HOW>::type;
+    constexpr S kNone = (S)-INFINITY;
+    S s[V];
+    make_scores<HOW, L>(a, q, s);
+    keep_groups<L>(a, q, s, 0.0f);
+#pragma unroll 1
+    for (uint32_t i = 0; i < q.k; ++i) {
+        S m = s[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = larger(m, s[j]);
+        m = join<L>(m, [](S p, S r) { return larger(p, r); });
+        uint32_t e = UINT32_MAX;
+#pragma unroll
+        for (int j = V - 1; j >= 0; --j)
+            if (s[j] == m) e = a.first + j;
+        if (m == kNone) e = UINT32_MAX;
+        const uint32_t won = join<L>(e, [](uint32_t p, uint32_t r) { return lower(p, r); });
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (won == a.first + j) s[j] = kNone;
+        if (threadIdx.x % L == 0) chosen[i] = (int32_t)won;  // -1: none
+    }
+}
+
+// The k best by keys that no two experts share: the score in the high bits, 0 for what is
+// ruled out, and the place among the token's lanes in the low ones, the first place highest.
+// The next best is the largest key below the last: key - last, as an unsigned number, is the
+// larger the nearer the key is below, and under 2^31 where it is not below.  A step is a
+// subtraction and half a maximum of three for each expert.
+// Returns whether two scores that the choice hangs on are within `near` of each other.
+template <int L, int V>
+__device__ inline bool choose_by_keys(const uint32_t *key, const RouteArgs &q, uint32_t near,
+                                      bool inexact, int32_t *chosen) {
+    constexpr int kPlaces = L * V, kBits = __builtin_ctz(kPlaces);
+    bool unsure = false;
+    uint32_t last = 1u << 31;
+#pragma unroll 1
+    for (uint32_t i = 0; i < q.k + (inexact ? 1u : 0u); ++i) {
+        uint32_t below = key[0] - last;
+#pragma unroll
+        for (int j = 1; j < V; ++j) below = larger(below, key[j] - last);
+        below = join<L>(below, [](uint32_t p, uint32_t r) { return larger(p, r); });
+        const uint32_t next = last ? last + below : 0u;
+        unsure = unsure || (i && next && (last >> kBits) - (next >> kBits) <= near);
+        last = next;
+        if (i < q.k && threadIdx.x % L == 0) {
+            const uint32_t place = kPlaces - 1 - next % kPlaces, lane = place / V;
+            const uint32_t group = lane / q.group_lanes;
+            chosen[i] = next ? (int32_t)(group * q.per_group + (lane % q.group_lanes) * V + place % V) : -1;
+        }
+    }
+    return inexact && unsure;
+}
+
+// The k best by scores of 32 bits, as whole numbers over the range of the token's scores.
+template <int HOW, int L, int V>
+__device__ inline bool choose_nearly(const Mine<V> &a, const RouteArgs &q, int32_t *chosen) {
+    constexpr int kPlaces = L * V, kBits = __builtin_ctz(kPlaces);
+    constexpr float kSteps = (float)((1u << (31 - kBits)) - 8u);
+    float s[V];
+    const float off = make_scores<HOW, L>(a, q, s);
+    bool unsure = keep_groups<L>(a, q, s, HOW == kBy32 ? off : 0.0f);
+    float high = s[0], low = INFINITY;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        high = larger(high, s[j]);
+        low = fminf(low, s[j] == -INFINITY ? INFINITY : s[j]);
+    }
+    high = join<L>(high, [](float p, float r) { return larger(p, r); });
+    low = join<L>(low, [](float p, float r) { return fminf(p, r); });
+    // Nothing but one number, or numbers too far apart: all of them are near each other.
+    const float steps = high > low ? kSteps / (high - low) : 0.0f;
+    uint32_t key[V];
+    const uint32_t place = threadIdx.x % L * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const uint32_t n = 1u + (uint32_t)((s[j] == -INFINITY ? 0.0f : s[j] - low) * steps);
+        key[j] = s[j] == -INFINITY ? 0u : n << kBits | (kPlaces - 1 - place - j);
+    }
+    // Each is off by `off` and by the bias's rounding, and by less than 2 steps in the product.
+    const float by = 2.0f * off + 0x1p-22f * (fabsf(high) + fabsf(low));
+    const uint32_t near = HOW == kBy32 ? (uint32_t)fminf(by * steps, 1e9f) + 4u : 4u;
+    return choose_by_keys<L, V>(key, q, near, true, chosen) || unsure;
+}
+
+// The k best by logits of 16 bits, whose order is that of whole numbers.
+template <class T, int L, int V>
+__device__ inline void choose_by_16(const Mine<V> &a, const RouteArgs &q, int32_t *chosen) {
+    constexpr int kPlaces = L * V, kBits = __builtin_ctz(kPlaces);
+    static_assert(kBits + 17 <= 31, "");
+    float s[V];
+    make_scores<kByLogits, L>(a, q, s);
+    keep_groups<L>(a, q, s, 0.0f);
+    uint32_t key[V];
+    const uint32_t place = threadIdx.x % L * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        // The zeros are equal, and the lowest number stands for NaN.
+        const float v = larger(s[j] + 0.0f, std::is_same<T, __bf16>::value ? -3.3895313892515355e38f : -65504.0f);
+        const uint32_t bits = __builtin_bit_cast(uint16_t, (T)v);
+        const uint32_t order = (bits & 0x8000u ? 0xFFFFu - bits : bits + 0x8000u) + 1u;
+        key[j] = s[j] == -INFINITY ? 0u : order << kBits | (kPlaces - 1 - place - j);
+    }
+    choose_by_keys<L, V>(key, q, 0, false, chosen);
+}
+
+template <class T, bool BY_LOGITS, int L, int V>
+__global__ __launch_bounds__(kOpThreads) void route_kernel(const T *logits, RouteArgs a) {
+    constexpr int kTokens = kOpThreads / L;
     __shared__ int32_t chosen[kTokens][kMaxK];
     const uint32_t lane = threadIdx.x % L, local = threadIdx.x / L;
     const uint32_t token = blockIdx.x * kTokens + local;
     // All lanes of a wave stay for the butterflies; lanes without a token have none to choose from.
     const bool live = token < a.tokens;
-    const uint32_t group = lane / a.group_lanes, in_group = (lane % a.group_lanes) * V;
-    const uint32_t first = group * a.per_group + in_group;
-    const uint32_t mine = !live || group >= a.groups || in_group >= a.per_group
-                              ? 0u
-                              : (a.per_group - in_group < (uint32_t)V ? a.per_group - in_group : (uint32_t)V);
-    float x[V];
-    {
-        typedef T mem __attribute__((ext_vector_type(V), aligned(sizeof(T))));
-        const T *row = logits + (int64_t)(live ? token : 0) * a.stride + first;
-        if (mine == (uint32_t)V) {
-            const mem v = *reinterpret_cast<const mem *>(row);
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = (float)v[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = (uint32_t)j < mine ? (float)row[j] : -INFINITY;
-        }
-    }
-    // The softmax's shift and sum, over all experts.
-    float top = 0.0f;
+    const T *const row = logits + (int64_t)(live ? token : 0) * a.stride;
+    Mine<V> mine = mine_of<V>(row, a, a.group_lanes, lane, live);
+    // The softmax's shift and sum, over all experts; a NaN or +inf leaves it no distribution.
     double total = 0.0;
-    if (!a.sigmoid && (kWide || !a.renormalize)) {
-        float m = x[0];
-#pragma unroll
-        for (int j = 1; j < V; ++j) m = larger(m, x[j]);
-        m = join<L>(m, [](float p, float q) { return larger(p, q); });
-        top = m == -INFINITY || m != m ? 0.0f : m;
-    }
-    // A NaN or +inf leaves the softmax no distribution.
     bool odd = false;
     if (!a.sigmoid) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) odd = odd || !(x[j] < INFINITY);
-        odd = join<L>((uint32_t)odd, [](uint32_t p, uint32_t q) { return p | q; });
-    }
-    S s[V];
-    if constexpr (kWide) {
-        if (a.sigmoid) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = 1.0 / (1.0 + exp(-(double)x[j]));
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) total += s[j] = exp((double)x[j] - (double)top);
-            total = join<L>(total, [](double p, double q) { return p + q; });
-            const double one = 1.0 / total;
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] *= one;
-        }
-        if (a.bias)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if ((uint32_t)j < mine) s[j] += (double)a.bias[first + j];
-    } else {
-        if (!a.sigmoid && !a.renormalize) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum += expf(x[j] - top);
-            total = join<L>((double)sum, [](double p, double q) { return p + q; });
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = x[j];
-    }
-    constexpr S kLowest = kWide ? (S)-1.7976931348623157e308 : (S)-3.4028234663852886e38f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (s[j] != s[j]) s[j] = kLowest;
-        if (x[j] == -INFINITY) s[j] = kNone;
-    }
-    if (a.kept < a.groups) {
-        Best<S> b{kNone, kNone};
+        float m = mine.x[0];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            b.second = larger(b.second, b.first < s[j] ? b.first : s[j]);
-            b.first = larger(b.first, s[j]);
+            m = fmaxf(m, mine.x[j]);
+            odd = odd || !(mine.x[j] < INFINITY);
         }
-        if (a.group_lanes > 1) join_best<1>(b);
-        if (a.group_lanes > 2) join_best<2>(b);
-        if (a.group_lanes > 4) join_best<4>(b);
-        if (a.group_lanes > 8) join_best<8>(b);
-        if constexpr (L > 16) {
-            if (a.group_lanes > 16) join_best<16>(b);
-            if (a.group_lanes > 32) join_best<32>(b);
-        }
-        S score = b.first;
-        if (a.best > 1 && b.second != kNone) score += b.second;
-        uint32_t before = 0;
-        for (uint32_t g = 0; g < a.groups; ++g) {
-            const S other = __shfl(score, (int)(g * a.group_lanes), L);
-            before += other > score || (other == score && g < group);
-        }
-        if (before >= a.kept)
+        odd = join<L>((uint32_t)odd, [](uint32_t p, uint32_t q) { return p | q; });
+        m = join<L>(m, [](float p, float q) { return fmaxf(p, q); });
+        mine.top = m == -INFINITY || odd ? 0.0f : m;
+        if (!a.renormalize) {
+            float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = kNone;
+            for (int j = 0; j < V; ++j) sum += expf(mine.x[j] - mine.top);
+            total = join<L>((double)sum, [](double p, double q) { return p + q; });
+        }
     }
-    for (uint32_t i = 0; i < a.k; ++i) {
-        S m = s[0];
-#pragma unroll
-        for (int j = 1; j < V; ++j) m = larger(m, s[j]);
-        m = join<L>(m, [](S p, S q) { return larger(p, q); });
-        uint32_t e = UINT32_MAX;
-#pragma unroll
-        for (int j = V - 1; j >= 0; --j)
-            if (s[j] == m) e = first + j;
-        if (m == kNone) e = UINT32_MAX;
-        const uint32_t won = join<L>(e, [](uint32_t p, uint32_t q) { return lower(p, q); });
-        if (won == UINT32_MAX) {
-            if (lane == 0) chosen[local][i] = -1;
-        } else if (won == e) {
-            float at = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (won == first + j) {
-                    at = x[j];
-                    s[j] = kNone;
-                }
-            chosen[local][i] = (int32_t)won;
-            chosen_x[local][i] = at;
+    // In 32 bits first, which nearly always settles it.
+    if constexpr (BY_LOGITS && sizeof(T) == 2) {
+        choose_by_16<T, L, V>(mine, a, chosen[local]);
+    } else {
+        constexpr int kNearly = BY_LOGITS ? kByLogits : kBy32, kExactly = BY_LOGITS ? kByLogits : kBy64;
+        const bool unsure = choose_nearly<kNearly, L, V>(mine, a, chosen[local]);
+        // The whole wave for each token that is not settled.
+        for (uint64_t left = __ballot(unsure && live); left;) {
+            const uint32_t which = (uint32_t)__builtin_ctzll(left) / L;  // of the wave's tokens
+            left &= ~((L == 64 ? ~0ull : (1ull << (L % 64)) - 1) << which * L % 64);
+            const uint32_t there = threadIdx.x / 64 * (64 / L) + which;
+            constexpr int kFew = V * L / 64;
+            RouteArgs wave = a;
+            wave.group_lanes = a.group_lanes * (64 / L);
+            Mine<kFew> m = mine_of<kFew>(logits + (int64_t)(blockIdx.x * kTokens + there) * a.stride, a,
+                                         wave.group_lanes, threadIdx.x % 64, true);
+            m.top = __shfl(mine.top, (int)(which * L));
+            choose_exactly<kExactly, 64, kFew>(m, wave, chosen[there]);
         }
     }
     __syncthreads();
     // Lane j has the slots j, j + L, ...
-    double shift = -INFINITY;
-    if (a.renormalize) {
-        for (uint32_t i = lane; i < a.k; i += L)
-            if (chosen[local][i] >= 0) {
-                const double v = a.sigmoid ? log_sigmoid(chosen_x[local][i]) : (double)chosen_x[local][i];
-                if (!(v <= shift)) shift = v;  // NaN too
-            }
-        shift = join<L>(shift, [](double p, double q) { return q != q || q > p ? q : p; });
-    }
-    double weight[(kMaxK + L - 1) / L], sum = 0.0;
+    constexpr int kSlots = (kMaxK + L - 1) / L;
+    double x[kSlots], shift = -INFINITY, sum = 0.0;
+    int32_t expert[kSlots];
 #pragma unroll
-    for (int n = 0; n < (kMaxK + L - 1) / L; ++n) {
+    for (int n = 0; n < kSlots; ++n) {
         const uint32_t i = lane + n * L;
-        double w = 0.0;
-        if (i < a.k && chosen[local][i] >= 0) {
-            const double v = (double)chosen_x[local][i];
-            if (a.renormalize) w = exp((a.sigmoid ? log_sigmoid(v) : v) - shift);
-            else w = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top) / total;
-        }
-        weight[n] = w;
-        sum += w;
+        expert[n] = i < a.k ? chosen[local][i] : -1;
+        x[n] = expert[n] >= 0 ? (double)(float)row[expert[n]] : 0.0;
     }
+    if (a.renormalize) {
+        // Sigmoids that underflow are compared by their logarithms.
+        bool far = false;
+        if (a.sigmoid) {
+#pragma unroll
+            for (int n = 0; n < kSlots; ++n) far = far || (expert[n] >= 0 && x[n] < -300.0);
+            far = __ballot(far);
+        }
+        if (!a.sigmoid || far) {
+#pragma unroll
+            for (int n = 0; n < kSlots; ++n) {
+                if (n * L >= a.k) continue;
+                if (far) x[n] = log_sigmoid(x[n]);
+                if (expert[n] >= 0 && !(x[n] <= shift)) shift = x[n];  // NaN too
+            }
+            shift = join<L>(shift, [](double p, double q) { return q != q || q > p ? q : p; });
+#pragma unroll
+            for (int n = 0; n < kSlots; ++n)
+                if (n * L < a.k) x[n] = exp(x[n] - shift);
+        } else {
+#pragma unroll
+            for (int n = 0; n < kSlots; ++n)
+                if (n * L < a.k) x[n] = 1.0 / (1.0 + exp(-x[n]));
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < kSlots; ++n)
+            if (n * L < a.k)
+                x[n] = a.sigmoid ? 1.0 / (1.0 + exp(-x[n])) : exp(x[n] - (double)mine.top) / total;
+    }
+#pragma unroll
+    for (int n = 0; n < kSlots; ++n)
+        if (expert[n] >= 0) sum += x[n];
     double factor = odd ? (double)NAN : a.scale;
     if (a.renormalize) factor /= join<L>(sum, [](double p, double q) { return p + q; });
     if (!live) return;
 #pragma unroll
-    for (int n = 0; n < (kMaxK + L - 1) / L; ++n) {
+    for (int n = 0; n < kSlots; ++n) {
         const uint32_t i = lane + n * L;
         if (i < a.k) {
-            const int32_t e = chosen[local][i];
-            a.experts[(int64_t)token * a.k + i] = e;
-            a.weights[(int64_t)token * a.k + i] = e >= 0 ? (float)(weight[n] * factor) : 0.0f;
+            a.experts[(int64_t)token * a.k + i] = expert[n];
+            a.weights[(int64_t)token * a.k + i] = expert[n] >= 0 ? (float)(x[n] * factor) : 0.0f;
         }
     }
 }
@@ -247,8 +429,8 @@ __global__ __launch_bounds__(kOpThreads) void route_grad_kernel(const T *logits,
     double m = 0.0, total = 1.0;
     if (whole) {
         float top = -INFINITY;
-        for (uint32_t e = lane; e < a.num_experts; e += 64) top = larger(top, (float)row[e]);
-        top = join<64>(top, [](float p, float q) { return larger(p, q); });
+        for (uint32_t e = lane; e < a.num_experts; e += 64) top = fmaxf(top, (float)row[e]);
+        top = join<64>(top, [](float p, float q) { return fmaxf(p, q); });
         m = top == -INFINITY ? 0.0 : (double)top;
         float sum = 0.0f;
         for (uint32_t e = lane; e < a.num_experts; e += 64) sum += expf((float)row[e] - (float)m);
@@ -346,11 +528,11 @@ extern "C" int segtopk_route(const segtopk_route_args *args, hipStream_t stream)
             constexpr int L = decltype(lanes)::value, V = decltype(each)::value;
             a.group_lanes = (uint32_t)L / groups;
             const unsigned per = kOpThreads / L;
-            return status(launch(route_kernel<T, decltype(score), L, V>,
+            return status(launch(route_kernel<T, decltype(score)::value, L, V>,
                                  dim3((a.tokens + per - 1) / per), kOpThreads, stream, 0, in, a));
         };
         const auto by_score = [&](auto lanes, auto each) {
-            return wide ? go(double{}, lanes, each) : go(float{}, lanes, each);
+            return wide ? go(std::false_type{}, lanes, each) : go(std::true_type{}, lanes, each);
         };
         using std::integral_constant;
         if (per_lane(16) <= 16) {
