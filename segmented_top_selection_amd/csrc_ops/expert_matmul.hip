@@ -226,17 +226,23 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
     const uint32_t wm = wave / WN, wn = wave % WN;
     const uint32_t depth_blocks = (a.depth + 127) / 128;
     Cursor cursor{0, 0};
+    uint32_t known = UINT32_MAX, known_first = 0, known_blocks = 0;  // the last expert's blocks
 
     const auto locate = [&](uint32_t at) {
         Spot s;
         if constexpr (TURNED) {
             s.expert = at / (a.col_tiles * a.row_tiles);
             const Place p = place_of(at % (a.col_tiles * a.row_tiles), a.row_tiles, a.col_tiles);
-            const Range r = tiles_of(a.seg, s.expert, 128, cursor);
-            // Offsets that are no segments may say anything.
-            s.first = uniform(r.first < a.seg.tiles_most ? r.first : a.seg.tiles_most);
-            const uint32_t count = uniform(r.count);
-            s.blocks = count < a.seg.tiles_most - s.first ? count : a.seg.tiles_most - s.first;
+            if (s.expert != known) {
+                known = s.expert;
+                const Range r = tiles_of(a.seg, known, 128, cursor);
+                // Offsets that are no segments may say anything.
+                known_first = uniform(r.first < a.seg.tiles_most ? r.first : a.seg.tiles_most);
+                const uint32_t count = uniform(r.count), left = a.seg.tiles_most - known_first;
+                known_blocks = count < left ? count : left;
+            }
+            s.first = known_first;
+            s.blocks = known_blocks;
             s.row = p.down * BM;
             s.col = p.across * BN;
             s.rows = a.height - s.row;
@@ -412,6 +418,11 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
     const uint32_t each = (all + 7) / 8, begin = blockIdx.x % 8 * each;
     const uint32_t end = begin + each < all ? begin + each : all, turn = gridDim.x / 8;
     uint32_t at = begin + blockIdx.x / 8;
+    // Workgroups of large tiles that begin at up to eight different times, 2 us apart, do not
+    // all store or all multiply at once (128 experts of 2048 x 4096, 65536 rows: 915 -> 850 us,
+    // their weights' gradient 1649 -> 1595 us).  A start of 13 us later pays for some tiles each.
+    if (BM * BN == 65536 && each >= 4 * turn)
+        for (uint32_t i = blockIdx.x / 8 % 8; i; --i) __builtin_amdgcn_s_sleep(64);
     Work w;
     if (at < end) {
         w = work_of(locate(at));
@@ -738,7 +749,6 @@ extern "C" int segtopk_expert_dweights(const segtopk_expert_dweights_args *args,
                       (uint32_t)q.width};
     const Turned rows{ws + s.rows, reinterpret_cast<float *>(ws + s.rows_scales), s.stride,
                       (uint32_t)q.depth};
-    constexpr int BM = 128, BN = 128;
     MulArgs a{};
     a.rows = dout.q;
     a.cols = rows.q;
@@ -752,18 +762,34 @@ extern "C" int segtopk_expert_dweights(const segtopk_expert_dweights_args *args,
     a.width = (uint32_t)q.depth;
     a.height = (uint32_t)q.width;
     a.accumulate = q.accumulate != 0;
-    a.col_tiles = (a.width + BN - 1) / BN;
-    a.row_tiles = (a.height + BM - 1) / BM;
-    const int64_t matrix = (int64_t)a.col_tiles * a.row_tiles;
-    if (matrix > kMostBlocks / q.num_experts || s.stride > kMostStride) return SEGTOPK_NOT_SUPPORTED;
+    const auto tiles_of_size = [&](int64_t size) {
+        return (a.width + size - 1) / size * ((a.height + size - 1) / size);
+    };
+    if (tiles_of_size(128) > kMostBlocks / q.num_experts || s.stride > kMostStride)
+        return SEGTOPK_NOT_SUPPORTED;
     if (s.tiles) {
         int r = queue_quantize_turned(q.dout, dout, seg, stream);
         if (r == SEGTOPK_OK) r = queue_quantize_turned(q.rows, rows, seg, stream);
         if (r != SEGTOPK_OK) return r;
     }
-    return with_type(d.type, [&](auto v) {
+    return with_type(d.type, [&](auto v) -> int {
         using T = decltype(v);
-        return status(launch(product_kernel<T, BM, BN, 2, 2, true>,
-                             dim3(groups_of(matrix * q.num_experts, BM, BN)), 256, stream, 0, a));
+        using std::integral_constant;
+        const auto go = [&](auto size, auto waves) -> int {
+            constexpr int kSize = decltype(size)::value, kAcross = decltype(waves)::value;
+            a.col_tiles = (a.width + kSize - 1) / kSize;
+            a.row_tiles = (a.height + kSize - 1) / kSize;
+            const int64_t tiles = (int64_t)a.col_tiles * a.row_tiles * q.num_experts;
+            return status(launch(product_kernel<T, kSize, kSize, 2, kAcross, true>,
+                                 dim3(groups_of(tiles, kSize, kSize)), kAcross * 128, stream, 0, a));
+        };
+        // As above, by tiles of 128 and 256, quantization included: 128 experts of 2048 x 4096,
+        // 512 rows each 1743 and 1659 us, 128 rows 912 and 957; 16 of 2048 x 2048, 1024 rows 207
+        // and 191, 128 rows 71 and 76; 8 of 4096 x 14336, 2048 rows 3278 and 2605; 60 of 336 x
+        // 1410, 78 rows 46 and 55.
+        if constexpr (sizeof(T) == 2)
+            if (q.num_rows / q.num_experts >= 384 && tiles_of_size(256) * q.num_experts >= 512)
+                return go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+        return go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
     });
 }
