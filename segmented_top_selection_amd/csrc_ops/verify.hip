@@ -45,7 +45,7 @@ struct VerifyArgs {
     const float *temperatures, *accept, *sample;
     int32_t *counts;
     RowStat *stats;   // [rows][chunks]: the target's rows, then the drafts'
-    double *sums;     // [requests][parts][2]: of w and of p
+    double *sums;     // [requests][parts][waves][2]: of w and of p
     uint32_t *arrived;  // [requests]
     double temperature;
     uint32_t drafts, requests, vocab, wide, has_draft;
@@ -272,12 +272,29 @@ __device__ inline Scan scan_threads(double v, double *part) {
     return r;
 }
 
+// The first thread whose sum is over the goal; where rounding alone keeps it out of reach, the
+// last with anything to add.  `found` was last read before a barrier.
+__device__ inline uint32_t find_thread(bool over, bool any, uint32_t *found) {
+    const uint64_t o = __ballot(over), n = __ballot(any);
+    constexpr uint32_t kOver = 1u << 16, kAny = 1u << 17;
+    if (threadIdx.x % 64 == 0)
+        found[threadIdx.x / 64] = o   ? kOver + threadIdx.x + (uint32_t)__builtin_ctzll(o)
+                                  : n ? kAny + threadIdx.x + 63u - (uint32_t)__builtin_clzll(n)
+                                      : 0u;
+    __syncthreads();
+    uint32_t at = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kOpThreads / 64; ++w)
+        if (found[w] && !(at & kOver)) at = found[w];
+    return at & (kOver - 1);
+}
+
 template <class T>
 __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const T *draft,
                                                           VerifyArgs a) {
     using P = Piece<T>;
     constexpr uint32_t kAtOnce = kOpThreads / 32;  // drafts
-    __shared__ uint32_t stop, arrival, chosen, last;
+    __shared__ uint32_t stop, arrival, found[kOpThreads / 64];
     __shared__ Source src;
     __shared__ RowStat seen[kAtOnce][2];
     __shared__ double likely[kAtOnce][2];
@@ -378,19 +395,18 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
         const double p = probability(v);
         return Both{weight(p, g, c), p};
     };
-    // Twice the same code: the workgroup's own part, and, by the last to arrive, the part that
-    // the token is in.  A thread has a run of the part's elements, four at a time.
-    const uint32_t each = a.part / kOpThreads;
-    uint32_t which = part;
+    // The same code for the workgroup's own part and, by the last to arrive, for what one wave
+    // had of the part that the token is in, and for one thread's run of that: code that comes
+    // into the cache as it is needed costs more time than the elements.  A thread has a run of
+    // elements, four at a time.
+    constexpr uint32_t kWaves = kOpThreads / 64;
+    uint32_t each = a.part / kOpThreads, begin = part * a.part, end = a.vocab;
     bool plain = false;
     double base = 0.0, goal = 0.0;
+    typedef T four __attribute__((ext_vector_type(4), aligned(sizeof(T))));
 #pragma unroll 1
     for (uint32_t pass = 0;; ++pass) {
-        const uint32_t begin = which * a.part;
-        const uint32_t end = a.vocab - begin < a.part ? a.vocab : begin + a.part;
         const uint32_t run = begin + i * each, run_end = run + each < end ? run + each : end;
-        Both sum{0.0, 0.0};
-        typedef T four __attribute__((ext_vector_type(4), aligned(sizeof(T))));
         const auto read = [&](uint32_t c, four &one, four &two) {
             one = two = (four)(T)-INFINITY;
             if (c + 4 <= run_end) {
@@ -405,6 +421,7 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
                     }
             }
         };
+        Both sum{0.0, 0.0};
         four one, two;
         read(run, one, two);
 #pragma unroll 1
@@ -421,83 +438,81 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
             two = next_two;
         }
         if (pass) {
-            // Whose run passes the goal; where rounding alone keeps it out of reach, the last
-            // with anything in it.
             const double m = plain ? sum.p : sum.w;
             const Scan s = scan_threads(m, scan);
-            if (m > 0.0) {
-                atomicMax(&last, i);
-                if (base + s.before + m > goal) atomicMin(&chosen, i);
+            const uint32_t owner =
+                find_thread(m > 0.0 && base + s.before + m > goal, m > 0.0, found);
+            if (each == 1) {
+                if (i == owner) put(a, from.row, run);
+                return;
             }
             __syncthreads();
-            const uint32_t owner = chosen < last ? chosen : last;
             if (i == owner) scan[0] = base + s.before;
             __syncthreads();
-            if (i >= 64) return;
-            // A wave looks at that run's elements, one to a lane.
-            double before = scan[0];
-            uint32_t token = 0;
-            const uint32_t from_here = begin + owner * each;
-            for (uint32_t at = 0; at < each; at += 64) {
-                const uint32_t c = from_here + at + i;
-                const bool mine = at + i < each && c < end;
-                double e = 0.0;
-                if (mine) {
-                    const Both one = both(c, (float)x[c], y ? (float)y[c] : 0.0f);
-                    e = plain ? one.p : one.w;
-                }
-                const double upto = scan_wave(e);
-                const uint64_t over = __ballot(e > 0.0 && before + upto > goal);
-                const uint64_t any = __ballot(e > 0.0);
-                if (any) token = from_here + at + 63u - (uint32_t)__builtin_clzll(any);
-                if (over) {
-                    token = from_here + at + (uint32_t)__builtin_ctzll(over);
-                    break;
-                }
-                before += __shfl(upto, 63);
-            }
-            if (i == 0) put(a, from.row, token);
-            return;
+            base = scan[0];
+            begin += owner * each;
+            end = begin + each < end ? begin + each : end;
+            each = (each + kOpThreads - 1) / kOpThreads;
+            continue;
         }
-        sum.w = scan_threads(sum.w, scan).all;
-        sum.p = scan_threads(sum.p, scan).all;
-        if (i == 0) {
-            double *s = a.sums + ((int64_t)r * a.parts + part) * 2;
+        sum.w = total_of<64>(sum.w);
+        sum.p = total_of<64>(sum.p);
+        if (i % 64 == 0) {
+            double *s = a.sums + (((int64_t)r * a.parts + part) * kWaves + i / 64) * 2;
             __hip_atomic_store(s, sum.w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __hip_atomic_store(s + 1, sum.p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            // Both are past this XCD's cache before the part counts as done.
+            // All are past this XCD's cache before the part counts as done.
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            arrival = __hip_atomic_fetch_add(&a.arrived[r], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            chosen = UINT32_MAX;
-            last = 0u;
         }
+        __syncthreads();
+        if (i == 0)
+            arrival = __hip_atomic_fetch_add(&a.arrived[r], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
         if (arrival + 1u != a.parts) return;
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-        double w = 0.0, p = 0.0;  // of part i
-        if (i < a.parts) {
-            const double *s = a.sums + ((int64_t)r * a.parts + i) * 2;
-            w = __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            p = __hip_atomic_load(s + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        double w[kWaves], p[kWaves], w_all = 0.0, p_all = 0.0;  // of part i
+#pragma unroll
+        for (uint32_t k = 0; k < kWaves; ++k) {
+            w[k] = p[k] = 0.0;
+            if (i < a.parts) {
+                const double *s = a.sums + (((int64_t)r * a.parts + i) * kWaves + k) * 2;
+                w[k] = __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                p[k] = __hip_atomic_load(s + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            w_all += w[k];
+            p_all += p[k];
         }
-        Scan sums = scan_threads(w, scan);
+        Scan sums = scan_threads(w_all, scan);
         plain = !(sums.all > 0.0);  // p is nowhere above q: p itself
         if (plain) {
-            sums = scan_threads(p, scan);
-            w = p;
+            sums = scan_threads(p_all, scan);
+            w_all = p_all;
         }
         goal = (double)a.sample[r] * sums.all;
-        // The first part that passes the goal, or the last with anything in it.
-        if (w > 0.0 && sums.before + w > goal) atomicMin(&chosen, i);
-        if (w > 0.0) atomicMax(&last, i);
+        const uint32_t which =
+            find_thread(w_all > 0.0 && sums.before + w_all > goal, w_all > 0.0, found);
         __syncthreads();
-        which = chosen < last ? chosen : last;
-        __syncthreads();
-        if (i == which) scan[0] = sums.before;
-        if (i == 0) chosen = UINT32_MAX;
-        if (i == 1) last = 0u;
+        if (i == which) {  // the same among its waves
+            double before = sums.before;
+            uint32_t wave = 0;
+            bool over = false;
+#pragma unroll
+            for (uint32_t k = 0; k < kWaves; ++k) {
+                const double e = plain ? p[k] : w[k];
+                if (e > 0.0 && !over) {
+                    wave = k;
+                    scan[0] = before;
+                    over = before + e > goal;
+                }
+                before += e;
+            }
+            stop = wave;
+        }
         __syncthreads();
         base = scan[0];
+        begin = which * a.part + stop * 64 * each;
+        end = begin + 64 * each < end ? begin + 64 * each : end;
+        each /= kWaves;  // a part is some 1024 elements
     }
 }
 
@@ -535,7 +550,7 @@ VerifySpace verify_space(int64_t drafts, int64_t requests, const Cut &c) {
     VerifySpace s;
     s.stats = 0;
     s.sums = s.stats + (2 * drafts + requests) * c.chunks * (int64_t)sizeof(RowStat);
-    s.arrived = s.sums + requests * c.parts * 16;
+    s.arrived = s.sums + requests * c.parts * (kOpThreads / 64) * 16;
     s.bytes = s.arrived + requests * 4;
     return s;
 }
