@@ -118,13 +118,13 @@ __device__ inline float uniform_float(const float *p) {
 
 // Where the tile in LDS holds piece c of row r: rows are 128 bytes, and a row's 8
 // pieces are swapped so that the lanes that read one piece of several rows meet
-// different banks.  Lanes 4 apart read columns 4 * NT apart.
-template <int NT> __device__ inline uint32_t swap_of(uint32_t r) {
-    return NT == 1 ? r & 7u : (r ^ ((r / NT) & 4u)) & 7u;
+// different banks.  Lanes 4 apart read rows 4 * RUN apart.
+template <int RUN> __device__ inline uint32_t swap_of(uint32_t r) {
+    return RUN == 1 ? r & 7u : (r ^ ((r / RUN) & 4u)) & 7u;
 }
 
 // ROWS x 128 bytes of an operand into LDS, 8 rows to an instruction of a wave.
-template <int ROWS, int WAVES, int NT> struct TileLoad {
+template <int ROWS, int WAVES, int RUN> struct TileLoad {
     static constexpr int N = ROWS / 8 / WAVES;
     uint32_t at[N];  // of the lane's pieces in the first block
 
@@ -133,7 +133,7 @@ template <int ROWS, int WAVES, int NT> struct TileLoad {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const uint32_t r = (i * WAVES + wave) * 8 + lane / 8;
-            at[i] = r * stride + ((lane % 8) ^ swap_of<NT>(r)) * 16;
+            at[i] = r * stride + ((lane % 8) ^ swap_of<RUN>(r)) * 16;
         }
     }
     __device__ inline void load(Memory from, uint32_t k0, const uint8_t *to, uint32_t wave) const {
@@ -144,12 +144,12 @@ template <int ROWS, int WAVES, int NT> struct TileLoad {
 };
 
 // Zeros from byte `have` on of each row.
-template <int ROWS, int THREADS, int NT>
+template <int ROWS, int THREADS, int RUN>
 __device__ inline void clear_tail(uint8_t *tile, uint32_t have) {
     for (uint32_t u = threadIdx.x; u < ROWS * 8; u += THREADS) {
         const uint32_t r = u / 8, c = u % 8;
         if (c * 16 + 16 <= have) continue;
-        Quarter *p = reinterpret_cast<Quarter *>(tile + r * 128 + (c ^ swap_of<NT>(r)) * 16);
+        Quarter *p = reinterpret_cast<Quarter *>(tile + r * 128 + (c ^ swap_of<RUN>(r)) * 16);
         Quarter v = *p;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -213,6 +213,12 @@ template <class T, int BM, int BN, int WM, int WN, bool TURNED>
 __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
     constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+    // A lane's results of RUN products are neighbours, 16 bytes of a row, and four lanes' 64.  In
+    // f32 a row's results all in one lane, 64 bytes in four stores, take longer: weights' gradient
+    // of 60 experts of 336 x 1410, 4662 rows, 68 against 55 us.  In 16 bits (one store or two) 16
+    // experts of 2048 x 2048 are alike; 8 bytes a lane lose: 128 experts of 2048 x 4096 1616
+    // and 1736.
+    constexpr int RUN = sizeof(T) == 4 ? 1 : 2;
     constexpr bool kExact = std::is_same<T, float>::value;
     __shared__ __attribute__((aligned(16))) uint8_t row_tile[2][BM * 128];
     __shared__ __attribute__((aligned(16))) uint8_t col_tile[2][BN * 128];
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
     };
 
     const TileLoad<BM, kWaves, 1> row_load((uint32_t)a.row_stride, wave);
-    const TileLoad<BN, kWaves, NT> col_load((uint32_t)a.col_stride, wave);
+    const TileLoad<BN, kWaves, RUN> col_load((uint32_t)a.col_stride, wave);
     // The scales of the rows: 64 of them a wave, some twice.
     const uint32_t part = wave % ((BM + 63) / 64) * 64, cpart = wave % ((BN + 63) / 64) * 64;
     const uint32_t row_scale_at = (part + lane) * (TURNED ? 4 : depth_blocks * 4);
@@ -315,12 +321,13 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
 
     const uint32_t l = lane % 16;
     // Where the lane's pieces begin.  Four columns on, the pieces of a pair change places.
-    const uint32_t col0 = wn * NT * 16 + l / 4 * (4 * NT) + l % 4;
-    const uint32_t col_at = col0 * 128 + ((lane / 16) ^ swap_of<NT>(col0)) * 16;
+    const uint32_t col0 = wn * NT * 16 + l / 4 * (4 * RUN) + l % 4;
+    const uint32_t col_at = col0 * 128 + ((lane / 16) ^ swap_of<RUN>(col0)) * 16;
+    const auto col_of = [](int j) { return j / RUN * RUN * 16 + j % RUN * 4; };
     const uint32_t row_at = (wm * MT * 16 + l) * 128 + ((lane / 16) ^ swap_of<1>(l)) * 16;
     const auto col_operand = [&](int j, int s) {
-        const uint8_t *at = col_tile[s] + j * 512, *one = at + col_at, *two = at + (col_at ^ 64u);
-        return operand<kExact>(NT > 1 && j % 2 ? fragment(two, one) : fragment(one, two));
+        const uint8_t *at = col_tile[s] + col_of(j) * 128, *one = at + col_at, *two = at + (col_at ^ 64u);
+        return operand<kExact>(RUN > 1 && j % 2 ? fragment(two, one) : fragment(one, two));
     };
     const auto row_operand = [&](int i, int s) {
         const uint8_t *at = row_tile[s] + i * 2048;
@@ -365,7 +372,7 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     cscale[j] = *reinterpret_cast<const Sums *>(
-                        &col_scale[s][wn * NT * 16 + lane / 16 * (4 * NT) + j * 4]);
+                        &col_scale[s][wn * NT * 16 + lane / 16 * (4 * RUN) + col_of(j)]);
             read_scale(0);
 #pragma unroll
             for (int i = 0; i < MT - 1; ++i) {
@@ -385,7 +392,7 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
             if (two_more) meet<kRowLoads + kColLoads>();
             else meet<kRowLoads>();
             if (ragged && b + 2 == w.blocks) {
-                clear_tail<BN, kThreads, NT>(col_tile[s ^ 1], w.depth - (b + 1) * 128);
+                clear_tail<BN, kThreads, RUN>(col_tile[s ^ 1], w.depth - (b + 1) * 128);
                 meet<kRowLoads>();
             }
         }
@@ -440,7 +447,7 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
             meet<0>();
             if (w.blocks == 1 && (w.depth & 127u)) {
                 clear_tail<BM, kThreads, 1>(row_tile[0], w.depth);
-                clear_tail<BN, kThreads, NT>(col_tile[0], w.depth);
+                clear_tail<BN, kThreads, RUN>(col_tile[0], w.depth);
                 meet<0>();
             }
             read_cols(0);
@@ -457,16 +464,19 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
             w = work_of(next);
             start(w);
         }
-        const uint32_t n = wn * NT * 16 + lane / 16 * (4 * NT);
-        const uint32_t have = n < width ? width - n : 0u;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const uint32_t m = (wm * MT + i) * 16 + l;
-            if (m <= last_row && have) {
-                float v[NT * 4];
 #pragma unroll
-                for (int j = 0; j < NT * 4; ++j) v[j] = acc[i][j / 4][j % 4];
-                store<T, NT * 4>(out + (int64_t)m * a.out_stride + n, v, have, TURNED && a.accumulate);
+            for (int j0 = 0; j0 < NT; j0 += RUN) {
+                const uint32_t n = wn * NT * 16 + lane / 16 * (4 * RUN) + col_of(j0);
+                if (m <= last_row && n < width) {
+                    float v[RUN * 4];
+#pragma unroll
+                    for (int j = 0; j < RUN * 4; ++j) v[j] = acc[i][j0 + j / 4][j % 4];
+                    store<T, RUN * 4>(out + (int64_t)m * a.out_stride + n, v, width - n,
+                                      TURNED && a.accumulate);
+                }
             }
         }
     }
@@ -768,8 +778,7 @@ extern "C" int segtopk_expert_dweights(const segtopk_expert_dweights_args *args,
     if (tiles_of_size(128) > kMostBlocks / q.num_experts || s.stride > kMostStride)
         return SEGTOPK_NOT_SUPPORTED;
     if (s.tiles) {
-        int r = queue_quantize_turned(q.dout, dout, seg, stream);
-        if (r == SEGTOPK_OK) r = queue_quantize_turned(q.rows, rows, seg, stream);
+        const int r = queue_quantize_turned(q.dout, dout, q.rows, rows, seg, stream);
         if (r != SEGTOPK_OK) return r;
     }
     return with_type(d.type, [&](auto v) -> int {

@@ -144,12 +144,20 @@ __global__ __launch_bounds__(kOpThreads) void quantize_blocks_kernel(const T *x,
 constexpr uint32_t kTurnCols = 64, kTurnStride = 144;
 
 template <class T>
-__global__ __launch_bounds__(kOpThreads) void quantize_turned_kernel(const T *x, int64_t stride,
-                                                                     Turned t, Segments seg) {
+__global__ __launch_bounds__(kOpThreads) void quantize_turned_kernel(const T *one, int64_t one_stride,
+                                                                     Turned one_turned, const T *two,
+                                                                     int64_t two_stride,
+                                                                     Turned two_turned, Segments seg) {
     __shared__ uint32_t part[kOpThreads / 64][kTurnCols];
     __shared__ __attribute__((aligned(16))) uint8_t tile[kTurnCols * kTurnStride];
-    const uint32_t cols = (t.width + kTurnCols - 1) / kTurnCols;
-    const uint32_t c0 = blockIdx.x % cols * kTurnCols, b = blockIdx.x / cols;
+    const uint32_t ones = (one_turned.width + kTurnCols - 1) / kTurnCols;
+    const uint32_t cols = ones + (two_turned.width + kTurnCols - 1) / kTurnCols;
+    const uint32_t b = blockIdx.x / cols, group = blockIdx.x % cols;
+    const bool first = group < ones;
+    const T *x = first ? one : two;
+    const int64_t stride = first ? one_stride : two_stride;
+    const Turned t = first ? one_turned : two_turned;
+    const uint32_t c0 = (first ? group : group - ones) * kTurnCols;
     Cursor cursor{0, 0};
     const Tile mine = find_tile(seg, b, 128, 1, cursor);
     if (mine.expert >= seg.experts) return;
@@ -204,14 +212,17 @@ bool good_matrices(const segtopk_matrices *m, int64_t matrices, int64_t rows, in
 
 }  // namespace
 
-int queue_quantize_turned(const segtopk_rows &x, const Turned &t, const Segments &seg,
-                          hipStream_t stream) {
-    const int64_t cols = (t.width + kTurnCols - 1) / kTurnCols;
+int queue_quantize_turned(const segtopk_rows &one, const Turned &one_turned, const segtopk_rows &two,
+                          const Turned &two_turned, const Segments &seg, hipStream_t stream) {
+    const int64_t cols = ((int64_t)one_turned.width + kTurnCols - 1) / kTurnCols +
+                         ((int64_t)two_turned.width + kTurnCols - 1) / kTurnCols;
     if (cols * (int64_t)seg.tiles_most > kMostBlocks) return SEGTOPK_NOT_SUPPORTED;
-    return with_type(x.type, [&](auto v) {
+    return with_type(one.type, [&](auto v) {
         using T = decltype(v);
         return status(launch(quantize_turned_kernel<T>, dim3((unsigned)(cols * seg.tiles_most)),
-                             kOpThreads, stream, 0, static_cast<const T *>(x.data), x.stride, t, seg));
+                             kOpThreads, stream, 0, static_cast<const T *>(one.data), one.stride,
+                             one_turned, static_cast<const T *>(two.data), two.stride, two_turned,
+                             seg));
     });
 }
 
