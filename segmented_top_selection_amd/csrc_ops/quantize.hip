@@ -56,9 +56,9 @@ constexpr uint32_t kRowBlocks = kOpThreads / 16;  // blocks of a workgroup
 
 template <class T>
 __global__ __launch_bounds__(kOpThreads) void quantize_rows_kernel(const T *x, RowsArgs a) {
-    const uint64_t unit = (uint64_t)blockIdx.x * kRowBlocks + threadIdx.x / 16;
-    if (unit >= (uint64_t)a.tokens * a.blocks) return;  // 16 lanes at once
-    const uint32_t token = (uint32_t)(unit / a.blocks), block = (uint32_t)(unit % a.blocks);
+    const uint32_t unit = blockIdx.x * kRowBlocks + threadIdx.x / 16;  // below 2^28
+    if (unit >= a.tokens * a.blocks) return;                           // 16 lanes at once
+    const uint32_t token = unit / a.blocks, block = unit % a.blocks;
     const uint32_t lane = threadIdx.x % 16, at = block * 128 + lane * 8;
     const uint32_t have = at < a.width ? a.width - at : 0u;
     float v[8];
@@ -66,8 +66,7 @@ __global__ __launch_bounds__(kOpThreads) void quantize_rows_kernel(const T *x, R
     uint32_t m = kLeast;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = larger(m, magnitude(v[j]));
-#pragma unroll
-    for (int d = 8; d; d >>= 1) m = larger(m, __shfl_xor(m, d));
+    m = join<16>(m, [](uint32_t p, uint32_t q) { return larger(p, q); });
     const float most = __uint_as_float(m), inverse = kMost / most, scale = most / kMost;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= inverse;
@@ -78,14 +77,19 @@ __global__ __launch_bounds__(kOpThreads) void quantize_rows_kernel(const T *x, R
         if (lane == 0) a.scales[(int64_t)token * a.blocks + block] = scale;
         return;
     }
+    // The places of 16 slots at once, one to a lane: loads between the stores would each be waited
+    // for (8192 tokens of 4096 in bf16, 8 slots each: 68 -> 60 us).
     const int64_t slots = (int64_t)a.tokens * a.k, kept = a.kept ? *a.kept : slots;
-    for (uint32_t j = 0; j < a.k; ++j) {
-        const int64_t p = a.position[(int64_t)token * a.k + j];
-        if (p < 0 || p >= slots) continue;
-        const bool keep = p < kept;
-        if (writes)
-            *reinterpret_cast<uint2 *>(a.q + p * a.qstride + at) = keep ? bits : uint2{0u, 0u};
-        if (lane == 0) a.scales[p * a.blocks + block] = keep ? scale : 0.0f;
+    for (uint32_t j0 = 0; j0 < a.k; j0 += 16) {
+        const int32_t own = j0 + lane < a.k ? a.position[(int64_t)token * a.k + j0 + lane] : -1;
+        for (uint32_t j = 0; j < 16 && j0 + j < a.k; ++j) {
+            const int64_t p = __shfl(own, (int)j, 16);
+            if (p < 0 || p >= slots) continue;
+            const bool keep = p < kept;
+            if (writes)
+                *reinterpret_cast<uint2 *>(a.q + p * a.qstride + at) = keep ? bits : uint2{0u, 0u};
+            if (lane == 0) a.scales[p * a.blocks + block] = keep ? scale : 0.0f;
+        }
     }
 }
 
@@ -141,15 +145,16 @@ __global__ __launch_bounds__(kOpThreads) void quantize_blocks_kernel(const T *x,
 // A workgroup 128 rows of an expert by 64 columns: each thread 4 neighbouring rows
 // of 8 columns, so that a column's four values are one word of the transposed
 // tile, which is written from LDS in pieces of 16 bytes.
-constexpr uint32_t kTurnCols = 64, kTurnStride = 144;
+constexpr uint32_t kTurnCols = 64;
 
 template <class T>
 __global__ __launch_bounds__(kOpThreads) void quantize_turned_kernel(const T *one, int64_t one_stride,
                                                                      Turned one_turned, const T *two,
                                                                      int64_t two_stride,
                                                                      Turned two_turned, Segments seg) {
-    __shared__ uint32_t part[kOpThreads / 64][kTurnCols];
-    __shared__ __attribute__((aligned(16))) uint8_t tile[kTurnCols * kTurnStride];
+    __shared__ __attribute__((aligned(16))) uint32_t part[kOpThreads / 16][kTurnCols];
+    __shared__ __attribute__((aligned(16))) float factor[kTurnCols];
+    __shared__ __attribute__((aligned(16))) uint8_t tile[kTurnCols * 128];
     const uint32_t ones = (one_turned.width + kTurnCols - 1) / kTurnCols;
     const uint32_t cols = ones + (two_turned.width + kTurnCols - 1) / kTurnCols;
     const uint32_t b = blockIdx.x / cols, group = blockIdx.x % cols;
@@ -175,32 +180,36 @@ __global__ __launch_bounds__(kOpThreads) void quantize_turned_kernel(const T *on
         m[j] = kLeast;
 #pragma unroll
         for (int r = 0; r < 4; ++r) m[j] = larger(m[j], magnitude(v[r][j]));
-#pragma unroll
-        for (int d = 8; d < 64; d <<= 1) m[j] = larger(m[j], __shfl_xor(m[j], d));
+        m[j] = larger(m[j], __builtin_amdgcn_update_dpp(m[j], m[j], 0x128, 0xF, 0xF, false));  // 8 lanes on
     }
-    if (i % 64 < 8)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) part[i / 64][col + j] = m[j];
+    if (i % 16 < 8) {
+        uint4 *to = reinterpret_cast<uint4 *>(&part[i / 16][col]);
+        to[0] = uint4{m[0], m[1], m[2], m[3]};
+        to[1] = uint4{m[4], m[5], m[6], m[7]};
+    }
     __syncthreads();
+    if (i < kTurnCols) {
+        uint32_t most = kLeast;
+#pragma unroll
+        for (uint32_t w = 0; w < kOpThreads / 16; ++w) most = larger(most, part[w][i]);
+        factor[i] = kMost / __uint_as_float(most);
+        if (c0 + i < t.width) t.scales[(int64_t)b * t.width + c0 + i] = __uint_as_float(most) / kMost;
+    }
+    __syncthreads();
+    // Column c's 16-byte piece p is at piece p ^ (c / 8): neighbouring lanes write neighbouring
+    // columns' groups, and each piece meets other banks.
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int w = 0; w < kOpThreads / 64; ++w) m[j] = larger(m[j], part[w][col + j]);
-        const float inverse = kMost / __uint_as_float(m[j]);
-        *reinterpret_cast<uint32_t *>(tile + (col + j) * kTurnStride + row) =
-            pack4(v[0][j] * inverse, v[1][j] * inverse, v[2][j] * inverse, v[3][j] * inverse);
+        const float f = factor[col + j];
+        *reinterpret_cast<uint32_t *>(tile + (col + j) * 128 + (((row / 16) ^ (col / 8)) * 16 + row % 16)) =
+            pack4(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f);
     }
-    if (i < 8)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + col + j < t.width)
-                t.scales[(int64_t)b * t.width + c0 + col + j] = __uint_as_float(m[j]) / kMost;
     __syncthreads();
     for (uint32_t p = i; p < kTurnCols * 8; p += kOpThreads) {
         const uint32_t c = p / 8, piece = p % 8;
         if (c0 + c < t.width)
             *reinterpret_cast<uint4 *>(t.q + (int64_t)(c0 + c) * t.stride + (int64_t)b * 128 + piece * 16) =
-                *reinterpret_cast<const uint4 *>(tile + c * kTurnStride + piece * 16);
+                *reinterpret_cast<const uint4 *>(tile + c * 128 + (piece ^ (c / 8)) * 16);
     }
 }
 
