@@ -24,6 +24,7 @@
 namespace segtopk_ops {
 namespace {
 
+constexpr uint32_t kExpert = 1u << 31;  // marks an expert's number among keys
 constexpr int kMaxK = 64, kMaxExperts = 1024, kMaxGroups = 64;
 
 struct RouteArgs {
@@ -101,7 +102,7 @@ template <> struct ScoreType<kBy64> { using type = double; };
 __device__ inline float exponential(float v) { return __expf(v); }
 __device__ inline double exponential(double v) { return exp(v); }
 
-// The scores of a lane's experts; what is ruled out has -inf, a NaN the lowest number.
+// The scores of a lane's experts, whatever they are where x is -inf or NaN.
 // Returns how far a score p of 32 bits is off at most: 4e-7 for the sigmoid, by its slope
 // times the exponential's error, |x| 2^-24 p (1 - p) and 2^-22 p (1 - p), and its own
 // roundings; 1.5e-6 of the largest p for the softmax, by the exponent's, (x - top) 2^-23 p, at
@@ -138,13 +139,17 @@ __device__ inline float make_scores(const Mine<V> &a, const RouteArgs &q, S *s) 
             for (int j = 0; j < V; ++j) s[j] += (S)b[j];
         }
     }
+    return off;
+}
+
+// A lane's scores with what is ruled out at -inf, and a NaN at the lowest number.
+template <int V, class S> __device__ inline void rule_out(const Mine<V> &a, S *s) {
     constexpr S kLowest = sizeof(S) == 8 ? (S)-1.7976931348623157e308 : (S)-3.4028234663852886e38f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (s[j] != s[j]) s[j] = kLowest;
         if (a.x[j] == -INFINITY) s[j] = (S)-INFINITY;
     }
-    return off;
 }
 
 // Rules out the experts of groups that are not kept.  With `off` (scores of 32 bits): whether
@@ -169,32 +174,41 @@ __device__ inline bool keep_groups(const Mine<V> &a, const RouteArgs &q, S *s, f
     }
     S score = b.first;
     if (q.best > 1 && b.second != kNone) score += b.second;
-    uint32_t before = 0, perhaps = 0;
-    for (uint32_t g = 0; g < q.groups; ++g) {
-        const S other = __shfl(score, (int)(g * q.group_lanes), L);
-        if (off > 0.0f) {
-            // Two sums of two scores, each off by that, by a bias's rounding and its own.
-            const S by = (S)(4.0f * off + 0x1p-21f * (fabsf((float)score) + fabsf((float)other)));
-            const bool real = score != kNone && other != kNone;
-            before += real ? other > score + by : other > score || (other == score && g < a.group);
-            perhaps += real && g != a.group && other >= score - by;
-        } else {
+    uint32_t before = 0;
+    bool unsure = false;
+    if (off > 0.0f) {
+        // Two sums of two scores, each off by that, by a bias's rounding and its own.
+        const S most = join<L>(score == kNone ? (S)0 : (S)fabsf((float)score),
+                               [](S p, S r) { return larger(p, r); });
+        const S by = (S)4 * (S)off + (S)0x1p-20 * most;
+        const S over = score + by, under = score - by;
+        uint32_t perhaps = 0;  // its own too
+        for (uint32_t g = 0; g < q.groups; ++g) {
+            const S other = __shfl(score, (int)(g * q.group_lanes), L);
+            before += other > over;
+            perhaps += other >= under;
+        }
+        unsure = a.group < q.groups && score != kNone && before < q.kept && perhaps > q.kept;
+    } else {
+        for (uint32_t g = 0; g < q.groups; ++g) {
+            const S other = __shfl(score, (int)(g * q.group_lanes), L);
             before += other > score || (other == score && g < a.group);
         }
     }
     if (before >= q.kept)
 #pragma unroll
         for (int j = 0; j < V; ++j) s[j] = kNone;
-    return off > 0.0f && a.group < q.groups && before < q.kept && perhaps >= q.kept;
+    return unsure;
 }
 
 // The k best by comparing scores, equal ones by their index.
 template <int HOW, int L, int V>
-__device__ inline void choose_exactly(const Mine<V> &a, const RouteArgs &q, int32_t *chosen) {
+__device__ inline void choose_exactly(const Mine<V> &a, const RouteArgs &q, uint32_t *chosen) {
     using S = typename ScoreType<HOW>::type;
     constexpr S kNone = (S)-INFINITY;
     S s[V];
     make_scores<HOW, L>(a, q, s);
+    rule_out<V>(a, s);
     keep_groups<L>(a, q, s, 0.0f);
 #pragma unroll 1
     for (uint32_t i = 0; i < q.k; ++i) {
@@ -211,7 +225,7 @@ __device__ inline void choose_exactly(const Mine<V> &a, const RouteArgs &q, int3
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (won == a.first + j) s[j] = kNone;
-        if (threadIdx.x % L == 0) chosen[i] = (int32_t)won;  // -1: none
+        if (threadIdx.x % L == 0) chosen[i] = kExpert | won;
     }
 }
 
@@ -223,8 +237,8 @@ __device__ inline void choose_exactly(const Mine<V> &a, const RouteArgs &q, int3
 // Returns whether two scores that the choice hangs on are within `near` of each other.
 template <int L, int V>
 __device__ inline bool choose_by_keys(const uint32_t *key, const RouteArgs &q, uint32_t near,
-                                      bool inexact, int32_t *chosen) {
-    constexpr int kPlaces = L * V, kBits = __builtin_ctz(kPlaces);
+                                      bool inexact, uint32_t *chosen) {
+    constexpr int kBits = __builtin_ctz(L * V);
     bool unsure = false;
     uint32_t last = 1u << 31;
 #pragma unroll 1
@@ -234,41 +248,66 @@ __device__ inline bool choose_by_keys(const uint32_t *key, const RouteArgs &q, u
         for (int j = 1; j < V; ++j) below = larger(below, key[j] - last);
         below = join<L>(below, [](uint32_t p, uint32_t r) { return larger(p, r); });
         const uint32_t next = last ? last + below : 0u;
-        unsure = unsure || (i && next && (last >> kBits) - (next >> kBits) <= near);
+        unsure = unsure || (i && next >> kBits && (last >> kBits) - (next >> kBits) <= near);
         last = next;
-        if (i < q.k && threadIdx.x % L == 0) {
-            const uint32_t place = kPlaces - 1 - next % kPlaces, lane = place / V;
-            const uint32_t group = lane / q.group_lanes;
-            chosen[i] = next ? (int32_t)(group * q.per_group + (lane % q.group_lanes) * V + place % V) : -1;
-        }
+        if (i < q.k && threadIdx.x % L == 0) chosen[i] = next;
     }
     return inexact && unsure;
+}
+// The expert of what has been chosen, -1: none.
+template <int L, int V> __device__ inline int32_t expert_of(uint32_t chosen, const RouteArgs &q) {
+    constexpr uint32_t kPlaces = L * V;
+    if (chosen & kExpert) return chosen == UINT32_MAX ? -1 : (int32_t)(chosen & ~kExpert);
+    if (chosen < kPlaces) return -1;
+    const uint32_t place = kPlaces - 1 - chosen % kPlaces, lane = place / V;
+    const uint32_t group = lane >> __builtin_ctz(q.group_lanes);  // a power of two
+    return (int32_t)(group * q.per_group + (lane & (q.group_lanes - 1)) * V + place % V);
 }
 
 // The k best by scores of 32 bits, as whole numbers over the range of the token's scores.
 template <int HOW, int L, int V>
-__device__ inline bool choose_nearly(const Mine<V> &a, const RouteArgs &q, int32_t *chosen) {
+__device__ inline bool choose_nearly(const Mine<V> &a, const RouteArgs &q, uint32_t *chosen) {
     constexpr int kPlaces = L * V, kBits = __builtin_ctz(kPlaces);
     constexpr float kSteps = (float)((1u << (31 - kBits)) - 8u);
     float s[V];
     const float off = make_scores<HOW, L>(a, q, s);
-    bool unsure = keep_groups<L>(a, q, s, HOW == kBy32 ? off : 0.0f);
-    float high = s[0], low = INFINITY;
+    // These keep NaN.
+    float high = s[0], low = s[0], least = a.x[0];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 1; j < V; ++j) {
         high = larger(high, s[j]);
-        low = fminf(low, s[j] == -INFINITY ? INFINITY : s[j]);
+        low = __builtin_elementwise_minimum(low, s[j]);
+        if constexpr (HOW != kByLogits) least = __builtin_elementwise_minimum(least, a.x[j]);
+    }
+    // Where none of a wave's scores is ruled out or NaN, nobody looks at each for that.
+    const bool clean = !__any(!(high < INFINITY) || !(low > -INFINITY) || !(least > -INFINITY));
+    if (!clean) {
+        rule_out<V>(a, s);
+        high = low = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            high = larger(high, s[j]);
+            const float v = s[j] == -INFINITY ? INFINITY : s[j];
+            low = j ? fminf(low, v) : v;
+        }
     }
     high = join<L>(high, [](float p, float r) { return larger(p, r); });
     low = join<L>(low, [](float p, float r) { return fminf(p, r); });
+    const bool unsure = keep_groups<L>(a, q, s, HOW == kBy32 ? off : 0.0f);
     // Nothing but one number, or numbers too far apart: all of them are near each other.
     const float steps = high > low ? kSteps / (high - low) : 0.0f;
     uint32_t key[V];
     const uint32_t place = threadIdx.x % L * V;
+    if (clean && !__any(steps == 0.0f)) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const uint32_t n = 1u + (uint32_t)((s[j] == -INFINITY ? 0.0f : s[j] - low) * steps);
-        key[j] = s[j] == -INFINITY ? 0u : n << kBits | (kPlaces - 1 - place - j);
+        for (int j = 0; j < V; ++j)  // groups that are not kept become 0
+            key[j] = (uint32_t)fmaxf(fmaf(s[j] - low, steps, 1.0f), 0.0f) << kBits | (kPlaces - 1 - place - j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t n = 1u + (uint32_t)((s[j] == -INFINITY ? 0.0f : s[j] - low) * steps);
+            key[j] = s[j] == -INFINITY ? 0u : n << kBits | (kPlaces - 1 - place - j);
+        }
     }
     // Each is off by `off` and by the bias's rounding, and by less than 2 steps in the product.
     const float by = 2.0f * off + 0x1p-22f * (fabsf(high) + fabsf(low));
@@ -278,11 +317,12 @@ __device__ inline bool choose_nearly(const Mine<V> &a, const RouteArgs &q, int32
 
 // The k best by logits of 16 bits, whose order is that of whole numbers.
 template <class T, int L, int V>
-__device__ inline void choose_by_16(const Mine<V> &a, const RouteArgs &q, int32_t *chosen) {
+__device__ inline void choose_by_16(const Mine<V> &a, const RouteArgs &q, uint32_t *chosen) {
     constexpr int kPlaces = L * V, kBits = __builtin_ctz(kPlaces);
     static_assert(kBits + 17 <= 31, "");
     float s[V];
     make_scores<kByLogits, L>(a, q, s);
+    rule_out<V>(a, s);
     keep_groups<L>(a, q, s, 0.0f);
     uint32_t key[V];
     const uint32_t place = threadIdx.x % L * V;
@@ -300,7 +340,7 @@ __device__ inline void choose_by_16(const Mine<V> &a, const RouteArgs &q, int32_
 template <class T, bool BY_LOGITS, int L, int V>
 __global__ __launch_bounds__(kOpThreads) void route_kernel(const T *logits, RouteArgs a) {
     constexpr int kTokens = kOpThreads / L;
-    __shared__ int32_t chosen[kTokens][kMaxK];
+    __shared__ uint32_t chosen[kTokens][kMaxK];
     const uint32_t lane = threadIdx.x % L, local = threadIdx.x / L;
     const uint32_t token = blockIdx.x * kTokens + local;
     // All lanes of a wave stay for the butterflies; lanes without a token have none to choose from.
@@ -355,7 +395,7 @@ __global__ __launch_bounds__(kOpThreads) void route_kernel(const T *logits, Rout
 #pragma unroll
     for (int n = 0; n < kSlots; ++n) {
         const uint32_t i = lane + n * L;
-        expert[n] = i < a.k ? chosen[local][i] : -1;
+        expert[n] = i < a.k ? expert_of<L, V>(chosen[local][i], a) : -1;
         x[n] = expert[n] >= 0 ? (double)(float)row[expert[n]] : 0.0;
     }
     if (a.renormalize) {
