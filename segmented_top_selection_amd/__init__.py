@@ -7,9 +7,10 @@ pointers and the current HIP stream to ``batched_topk``.  Every step of the
 selection runs in the library's HIP kernels; there is no other code path, and
 the binding raises if the library is missing.
 
-The operators around the selection (expert sort, dispatch and combine, embedding
-rows, policy loss, and their gradients) are bound in ``model_ops``, through a
-compiled module, and reached from here.
+The operators around the selection (routing, expert sort, dispatch and combine,
+the experts' products in 8 bits, embedding rows, policy loss, their gradients, and
+the verification of drafted tokens) are bound in ``model_ops``, through a compiled
+module, and reached from here.
 """
 from __future__ import annotations
 

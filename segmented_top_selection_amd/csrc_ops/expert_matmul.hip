@@ -17,6 +17,15 @@
 // The operand whose index is the result's fast one ("columns": n) is the
 // instruction's first, so that a lane holds neighbouring columns of one row: it
 // needs one scale a row tile, and stores pieces of a row.
+//
+// Measured in bf16, 128 experts of 4096 to 2048 unless said: 512 rows an expert, 8192 tokens'
+// 8 slots shared unevenly, 810 us, 1360 TFLOP/s (a fifth of the tiles' rows are nobody's); one
+// matrix of 8192 x 8192 and 8192 rows 555 us, 1980.  The matrix units are busy 38% of that at
+// the 1.95 GHz that the device keeps under them; a block of 256 x 256 results needs 2060 clocks
+// of them, 64 KiB from L2 (23 bytes a clock and CU: 2850) and 192 KiB out of LDS (1540), which
+// the two waves of a SIMD overlap in part.  Few rows (64 experts, 8 each): 97 us, 5.5 TB/s of
+// weights.  The weights' gradient, 65536 rows: 1260 us behind 275 of quantization, 500 of them
+// the 2.1 GB of results.
 #include <type_traits>
 
 #include "quantize.h"

@@ -18,6 +18,11 @@
 //   pick_kernel   a request in chunks: each workgroup sees from the statistics
 //                 which drafts stand, and adds up its chunk of the one row that is
 //                 drawn from; the last of a request to arrive finds the token
+//
+// 64 requests of up to seven drafts over 131072 entries in bf16: 47 us for the statistics, in
+// which the vector units are busy 87% (27 us without the powers of two, 38 without the loads),
+// and 32 for the pick.  One request of 32003: 12.2 us, two launches and the pick's chain of
+// offsets, drafts, statistics, parts and places.
 #include <cmath>
 #include <type_traits>
 
