@@ -68,8 +68,17 @@ struct Power {
 __device__ inline double shift_of(float max, double factor) {
     return max == -INFINITY ? 0.0 : rint((double)max * factor);
 }
+// Past 2^50 the product is no whole number to the half any more.  Two logits are 2^-24 of the
+// larger apart at least, so that all others than the largest are nothing there, and are with the
+// factor that makes the product 2^40 too.
 __device__ inline Power power_of(float max, double factor) {
+    if (fabs((double)max * factor) > 0x1p50 && max != -INFINITY) factor = 0x1p40 / fabs((double)max);
     return {factor, shift_of(max, factor)};
+}
+// log2(e) / temperature; from 2^830 on any two logits are as far apart as can be, and products
+// with a logit stay finite.
+__device__ inline double factor_of(double temperature) {
+    return fmin(kLog2e / temperature, 0x1p830);
 }
 // What a sum by one maximum is multiplied by to become one by a larger: a power of two.
 // (A sum by -inf is zero, and stays so.)
@@ -157,7 +166,7 @@ __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, cons
         a.temperatures ? temperature_of(a, request_of(a, r, of_draft)) : a.temperature;
     const bool greedy = !(temperature > 0.0);
     if (greedy && of_draft) return;  // not asked for
-    const double factor = greedy ? 1.0 : kLog2e / temperature;
+    const double factor = greedy ? 1.0 : factor_of(temperature);
     const T *x = of_draft ? draft + (int64_t)r * a.draft_stride : target + (int64_t)r * a.target_stride;
     const uint32_t begin = chunk * a.chunk;
     const uint32_t end = a.vocab - begin < a.chunk ? a.vocab : begin + a.chunk;
@@ -311,7 +320,7 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
     const int64_t row0 = first + r;
     const double temperature = temperature_of(a, r);
     const bool greedy = !(temperature > 0.0);
-    const double factor = greedy ? 1.0 : kLog2e / temperature;
+    const double factor = greedy ? 1.0 : factor_of(temperature);
     const int64_t targets = (int64_t)a.drafts + a.requests;
     const bool certain = greedy || !a.has_draft;
 

@@ -72,6 +72,25 @@ def test_verify_large(lengths, vocab, dtype):
     drafts.check(drafts.inputs(drafts.gen(vocab), lengths, vocab, dtype))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=NAMES.get)
+@pytest.mark.parametrize("size,temperature", [(1e17, 1.0), (1e30, 1.0), (-1e30, 0.7), (3e37, 2.0), (10.0, 1e-18),
+                                              (10.0, 1e-40), (1.0, 1e-290), (1e-42, 1e-290), (1e30, 1e-300)])
+def test_verify_logits_far_past_their_temperature(size, temperature, dtype, monkeypatch):
+    # max / temperature is past 2^52: all is on the largest logits, of which there are several.
+    # The quotient itself may overflow, a difference's to nothing but the infinity that it stands for.
+    plain = drafts.distribution
+    monkeypatch.setattr(drafts, "distribution", lambda x, t: plain((x.double() - x.double().max()) / t, 1.0))
+    g = drafts.gen(21)
+    s = drafts.inputs(g, [3, 0, 2, 1], 2500, dtype, temperature=temperature)
+    for name in ("target", "draft"):
+        x = torch.randint(0, 40, s[name].shape, generator=g, device=DEV).float()
+        s[name] = ((1.0 + x / 64) * size).to(dtype)
+    # All but the last row of the first request: nothing but the lowest number.
+    s["target"][:3] = torch.finfo(dtype).min
+    s["tokens"] = torch.where(torch.arange(6, device=DEV) % 2 == 0, s["draft"].float().argmax(1), s["tokens"])
+    drafts.check(s)
+
+
 @pytest.mark.parametrize("experts,k", [(64, 8), (160, 6), (256, 8), (1000, 3)])
 def test_route_where_32_bits_settle_nothing(experts, k):
     # All of a token's scores within a few steps of 32 bits, in every token of a wave.
