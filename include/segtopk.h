@@ -432,6 +432,7 @@ int segtopk_policy_loss(const segtopk_policy_loss_args *args, void *workspace,
  * logits: rows of num_experts.  1 <= num_experts <= 1024, 1 <= groups <= 64 and a
  * divisor of num_experts, 1 <= kept_groups <= groups,
  * 1 <= k <= min(64, kept_groups * num_experts / groups), 0 <= tokens < 2^31 - 1.
+ * SEGTOPK_NOT_SUPPORTED: more than 2^26 - 4 tokens.
  */
 typedef struct segtopk_route_args {
     segtopk_rows logits;

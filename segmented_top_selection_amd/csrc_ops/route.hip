@@ -526,6 +526,7 @@ bool good_route(const segtopk_rows *logits, int64_t tokens, int64_t experts, int
            k <= kMaxK && k <= experts && (scoring == SEGTOPK_SOFTMAX || scoring == SEGTOPK_SIGMOID) &&
            std::isfinite(scale) && (!tokens || good_rows(logits, experts));
 }
+constexpr int64_t kMostTokens = kMostBlocks * (kOpThreads / 64);  // a wave each
 
 }  // namespace
 }  // namespace segtopk_ops
@@ -544,6 +545,7 @@ extern "C" int segtopk_route(const segtopk_route_args *args, hipStream_t stream)
     if (!q.tokens) return SEGTOPK_OK;
     if (!q.weights || !aligned(q.weights, 4) || !q.experts || !aligned(q.experts, 4))
         return SEGTOPK_INVALID_ARGUMENT;
+    if (q.tokens > kMostTokens) return SEGTOPK_NOT_SUPPORTED;
     RouteArgs a{};
     a.stride = q.logits.stride;
     a.bias = q.bias;
@@ -605,6 +607,7 @@ extern "C" int segtopk_route_backward(const segtopk_rows *logits, const segtopk_
     if (!good_rows(dlogits, num_experts) || dlogits->type != logits->type || !experts ||
         !aligned(experts, 4) || !dweights || !aligned(dweights, 4))
         return SEGTOPK_INVALID_ARGUMENT;
+    if (tokens > kMostTokens) return SEGTOPK_NOT_SUPPORTED;
     RouteGradArgs a{logits->stride, dlogits->stride, experts, dweights, (uint32_t)tokens,
                     (uint32_t)num_experts, (uint32_t)k, scoring == SEGTOPK_SIGMOID,
                     renormalize != 0, scale};

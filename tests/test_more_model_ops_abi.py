@@ -71,6 +71,11 @@ def test_route_backward_refusals(kw):
     assert route_backward(tokens=0) == OK
 
 
+def test_routing_of_more_than_one_launch_holds():
+    for tokens in (2 ** 26 - 3, 2 ** 31 - 2):
+        assert route(tokens=tokens) == route_backward(tokens=tokens) == NOT_SUPPORTED
+
+
 def quantize(x=None, q=None, scales=C, tokens=10, k=2, width=64, position=D, kept=WS):
     return mo.entry("segtopk_quantize_rows")(x or rows(), q or rows8(B), scales, tokens, k, width, position, kept,
                                              None)
