@@ -429,8 +429,12 @@ __global__ __launch_bounds__(WM *WN * 64) void product_kernel(MulArgs a) {
 
     // Workgroups go to the eight XCDs in turn.  Each XCD has a run of neighbouring tiles, so
     // that an expert's operands are in one cache, or two.
-    const uint32_t all =
-        TURNED ? a.seg.experts * a.col_tiles * a.row_tiles : uniform(count_tiles(a.seg, BM)) * a.col_tiles;
+    uint32_t all = a.seg.experts * a.col_tiles * a.row_tiles;
+    if constexpr (!TURNED) {
+        // Offsets that are no segments may say anything.
+        const uint32_t count = uniform(count_tiles(a.seg, BM));
+        all = (count < a.seg.tiles_most ? count : a.seg.tiles_most) * a.col_tiles;
+    }
     const uint32_t each = (all + 7) / 8, begin = blockIdx.x % 8 * each;
     const uint32_t end = begin + each < all ? begin + each : all, turn = gridDim.x / 8;
     uint32_t at = begin + blockIdx.x / 8;
@@ -688,6 +692,7 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
             a.col_tiles = (a.width + BN - 1) / BN;
             const int64_t tiles = tiles_most(q.num_rows, q.num_experts, BM);
             if (tiles > kMostBlocks / a.col_tiles) return SEGTOPK_NOT_SUPPORTED;
+            a.seg.tiles_most = (uint32_t)tiles;
             return status(launch(product_kernel<T, BM, BN, WM, WN, false>,
                                  dim3(groups_of(tiles * a.col_tiles, BM, BN)), WM * WN * 64, stream,
                                  0, a));
