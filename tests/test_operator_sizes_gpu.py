@@ -159,3 +159,45 @@ def test_two_graphs_in_turn():
         want, want_counts = verify()
         assert torch.equal(tokens, want) and torch.equal(again, want) and torch.equal(counts, want_counts)
         assert torch.equal(one, gradient()) and torch.equal(two, one)
+
+
+def far(memory, like, *strides):
+    """A copy of `like` in `memory`, its neighbours so many elements apart."""
+    t = memory[:memory.numel() // 16 * 16].view(like.dtype).as_strided(like.shape, strides)
+    t.copy_(like)
+    return t
+
+
+def test_places_past_32_bits():
+    g = products.gen(7)
+    memory = torch.empty(9 << 30, dtype=torch.uint8, device=DEV)
+    # Matrices 4.5 GiB apart: weights, and their gradient.
+    rows, rs, w, ws = products.operands(g, 60, 2, 130, 256)
+    off = products.offsets_of([25, 35])
+    want = st.expert_matmul(rows, rs, w, ws, off)
+    assert torch.equal(st.expert_matmul(rows, rs, far(memory, w, 9 << 29, 256, 1), ws, off), want)
+    d, x = products.randn(g, 60, 130, dtype=torch.bfloat16), products.randn(g, 60, 70, dtype=torch.bfloat16)
+    want = st.expert_matmul_dweights(d, x, off)
+    out = far(memory, want, 9 << 28, 80, 1).zero_()
+    assert torch.equal(st.expert_matmul_dweights(d, x, off, out=out), want)
+    q, s = st.quantize_blocks(far(memory, w.float().bfloat16(), 9 << 28, 256, 1))
+    want_q, want_s = st.quantize_blocks(w.float().bfloat16())
+    assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(s, want_s)
+    # Rows 4.5 GiB or 300 MiB apart: results, inputs, logits.
+    want = st.expert_matmul(*(t[:2] for t in (rows, rs)), w, ws, products.offsets_of([1, 1]))
+    out = far(memory, want, 9 << 28, 1).zero_()
+    st.expert_matmul(*(t[:2] for t in (rows, rs)), w, ws, products.offsets_of([1, 1]), out=out)
+    assert torch.equal(out, want)
+    wide = far(memory, x[:30], 150 << 20, 1)
+    for got, want in zip(st.quantize_rows(wide), st.quantize_rows(x[:30])):
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    assert torch.equal(st.expert_matmul_dweights(d[:30], wide, off.clamp(max=30)),
+                       st.expert_matmul_dweights(d[:30], x[:30], off.clamp(max=30)))
+    want = st.route(x[:30], 4)
+    got = st.route(wide, 4)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dw = products.randn(g, 30, 4)
+    assert torch.equal(st.route_backward(dw, wide, want[1]), st.route_backward(dw, x[:30], want[1]))
+    s = drafts.inputs(g, [3, 2], 5000, torch.bfloat16)
+    s["target"] = far(memory, s["target"], 9 << 26, 1)
+    drafts.check(s)
