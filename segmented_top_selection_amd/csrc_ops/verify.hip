@@ -10,8 +10,9 @@
 // The running sum passes a border at each of some 10^5 tokens, a few 10^-6 of the
 // whole apart: sums of 32 bits, 10^-7 off, would pick another token once in a
 // hundred calls.  All is in 64 bits, whose vector rate is that of 32 here: 2^t is
-// a polynomial on [-1/2, 1/2], 5e-11 off, and an addition to the exponent, some 15
-// instructions for an element that takes as long to load.
+// one of 32 roots in LDS, a polynomial of degree 3 on [-1/64, 1/64], 7e-11 off, and
+// an addition to the exponent, some 13 instructions for an element that takes as long
+// to load.  (Without roots it is a polynomial of degree 7 and 15 instructions.)
 //
 //   stats_kernel  every row in chunks: the maximum, the sum of 2^(x - max) (the
 //                 place of the maximum, for temperature 0)
@@ -19,9 +20,9 @@
 //                 which drafts stand, and adds up its chunk of the one row that is
 //                 drawn from; the last of a request to arrive finds the token
 //
-// 64 requests of up to seven drafts over 131072 entries in bf16: 47 us for the statistics, in
-// which the vector units are busy 87% (27 us without the powers of two, 38 without the loads),
-// and 32 for the pick.  One request of 32003: 12.2 us, two launches and the pick's chain of
+// 64 requests of up to seven drafts over 131072 entries in bf16: 73 us, of which 44 are the
+// statistics (27 without the powers; by the polynomial of degree 7 48, and then 38 without the
+// loads) and 31 the pick.  One request of 32003: 12.4 us, two launches and the pick's chain of
 // offsets, drafts, statistics, parts and places.
 #include <cmath>
 #include <type_traits>
@@ -58,22 +59,47 @@ struct VerifyArgs {
     uint32_t part, parts;    // the same of the row that is drawn from
 };
 
-// 2^(x factor - shift), `shift` being max factor to the nearest integer, for x <= max: the
-// polynomial of degree 7 that goes through 2^f at the Chebyshev points of [-1/2, 1/2], and an
-// exponent.  Adding 1.5 * 2^52 leaves the nearest integer in the low bits, from where it goes
-// into the exponent.  What is below 2^-1018, -inf too, gives that.
+// 2^(j / 32).
+__device__ const double kRoots[32] = {
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
+// They in LDS as words: the high one without j << 15, see power().  32 of 8 bytes are all the
+// banks once, so that lanes meet only where they read the same.
+struct Roots {
+    uint2 of[32];
+};
+__device__ inline void fill(Roots &roots) {
+    const uint32_t j = threadIdx.x;
+    if (j < 32) {
+        const double v = kRoots[j];
+        roots.of[j] = uint2{(uint32_t)__double2loint(v), (uint32_t)__double2hiint(v) - (j << 15)};
+    }
+}
+
+// 2^(x factor - shift), `shift` being max factor to the nearest integer, for x <= max.  What is
+// below 2^-1000, -inf too, gives that.
 struct Power {
-    double factor, shift;
+    double factor, round, low;  // 1.5 * 2^47 - shift, and the x of 2^-1000
 };
 __device__ inline double shift_of(float max, double factor) {
     return max == -INFINITY ? 0.0 : rint((double)max * factor);
 }
-// Past 2^50 the product is no whole number to the half any more.  Two logits are 2^-24 of the
-// larger apart at least, so that all others than the largest are nothing there, and are with the
-// factor that makes the product 2^40 too.
-__device__ inline Power power_of(float max, double factor) {
-    if (fabs((double)max * factor) > 0x1p50 && max != -INFINITY) factor = 0x1p40 / fabs((double)max);
-    return {factor, shift_of(max, factor)};
+// Past 2^40 the product leaves no 32nds of a whole number.  Two logits are 2^-24 of the larger
+// apart at least, so that all others than the largest are nothing there, and are with the factor
+// that makes the product 2^40 too.
+// `span` is 1000 / factor.
+__device__ inline Power power_of(float max, double factor, double span) {
+    if (fabs((double)max * factor) > 0x1p40 && max != -INFINITY) {
+        factor = 0x1p40 / fabs((double)max);
+        span = 1000.0 / factor;
+    }
+    return {factor, 0x1.8p47 - shift_of(max, factor), (max == -INFINITY ? 0.0 : (double)max) - span};
 }
 // log2(e) / temperature; from 2^830 on any two logits are as far apart as can be, and products
 // with a logit stay finite.
@@ -87,22 +113,32 @@ __device__ inline double between(float from, float to, double factor) {
     const int e = d > 0.0 ? 0 : d < -1020.0 ? -1020 : (int)d;
     return __hiloint2double((1023 + e) << 20, 0);
 }
-__device__ inline double power(const Power &a, float v) {
-    constexpr double kRound = 6755399441055744.0;
-    const double t = fmax(fma((double)v, a.factor, -a.shift), -1018.0);
-    const double s = t + kRound, f = t - (s - kRound);
-    double p = fma(f, 1.5303700711365693e-05, 0.00015469729214118296);
-    p = fma(p, f, 0.0013333478473685416);
-    p = fma(p, f, 0.009618025613318034);
-    p = fma(p, f, 0.055504109063258665);
-    p = fma(p, f, 0.24022651213498092);
-    p = fma(p, f, 0.6931471805568324);
-    p = fma(p, f, 0.9999999999595618);
-    return __hiloint2double(__double2hiint(p) + (__double2loint(s) << 20), __double2loint(p));
+// Its exponent is n + j / 32 + f: an addition that leaves 32nds the last bit has n and j in the
+// low word, f is what is over, and 2^f the polynomial of degree 3 that goes through it at the
+// Chebyshev points of [-1/64, 1/64].  The whole low word goes 15 bits up to the root's high
+// word, n into the exponent, and takes back j << 15.
+struct Factors {
+    double root, poly;  // their product is the power
+};
+__device__ inline Factors factors(const Power &a, double x, const Roots &roots) {
+    const double s = fma(x, a.factor, a.round), f = fma(x, a.factor, a.round - s);
+    const uint32_t k = (uint32_t)__double2loint(s);
+    const uint2 r = roots.of[k % 32];
+    double p = fma(f, 0.055504434191939005, 0.24022885514318595);
+    p = fma(p, f, 0.693147180550011);
+    p = fma(p, f, 0.9999999999283391);
+    return {__hiloint2double((int)(r.y + (k << 15)), (int)r.x), p};
 }
-// The same where what is ruled out, or as good as that, has to be nothing.
-__device__ inline double power_or_zero(const Power &a, float v) {
-    return fma((double)v, a.factor, -a.shift) < -1000.0 ? 0.0 : power(a, v);
+// The sum so far and one power more.
+__device__ inline double add_power(const Power &a, float v, const Roots &roots, double sum) {
+    const Factors p = factors(a, fmax((double)v, a.low), roots);
+    return fma(p.root, p.poly, sum);
+}
+// A power, where what is ruled out, or as good as that, has to be nothing.
+__device__ inline double power_or_zero(const Power &a, float v, const Roots &roots) {
+    const double x = fmax((double)v, a.low);
+    const Factors p = factors(a, x, roots);
+    return x <= a.low ? 0.0 : p.root * p.poly;
 }
 
 __device__ inline int64_t draft_offset(const VerifyArgs &a, uint32_t r) {
@@ -151,12 +187,14 @@ template <int L> __device__ inline RowStat join_lanes(const RowStat &s, double f
     return {total_of<L>(s.sum * between(s.max, m, factor)), m, 0u};
 }
 
-template <class T>
+template <class T, int AT_ONCE>
 __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, const T *draft,
                                                            VerifyArgs a) {
     using P = Piece<T>;
-    constexpr int kAtOnce = 4, kElements = kAtOnce * P::N;
+    constexpr int kAtOnce = AT_ONCE, kElements = kAtOnce * P::N;
     __shared__ RowStat part[kOpThreads / 64];
+    __shared__ Roots roots;
+    fill(roots);
     const uint32_t chunk = blockIdx.x % a.chunks, row = blockIdx.x / a.chunks;
     const uint32_t targets = a.drafts + a.requests, i = threadIdx.x;
     if (i == 0 && chunk == 0 && row < a.requests) a.arrived[row] = 0u;
@@ -166,7 +204,7 @@ __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, cons
         a.temperatures ? temperature_of(a, request_of(a, r, of_draft)) : a.temperature;
     const bool greedy = !(temperature > 0.0);
     if (greedy && of_draft) return;  // not asked for
-    const double factor = greedy ? 1.0 : factor_of(temperature);
+    const double factor = greedy ? 1.0 : factor_of(temperature), span = 1000.0 / factor;
     const T *x = of_draft ? draft + (int64_t)r * a.draft_stride : target + (int64_t)r * a.target_stride;
     const uint32_t begin = chunk * a.chunk;
     const uint32_t end = a.vocab - begin < a.chunk ? a.vocab : begin + a.chunk;
@@ -192,15 +230,21 @@ __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, cons
             for (int k = 0; k < kElements; k += 2)
                 m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, v[k]), v[k + 1]);
             odd = odd || !(m < INFINITY);
-            const Power e = power_of(m, factor);
+            const Power e = power_of(m, factor, span);
             double s = st.sum * between(st.max, m, factor);
 #pragma unroll
-            for (int k = 0; k < kElements; ++k) s += power(e, v[k]);
+            for (int k = 0; k < kElements; ++k) s = add_power(e, v[k], roots, s);
             st.sum = s;
         }
         st.max = m;
     };
-    for (uint32_t u0 = i; u0 < pieces; u0 += kOpThreads * kAtOnce) {
+    // The last turn is theirs, if there are any: the same code, which comes into the cache as it is
+    // needed.
+    const uint32_t whole = (pieces + kOpThreads * kAtOnce - 1) / (kOpThreads * kAtOnce);
+    const uint32_t turns = whole + (begin + pieces * P::N < end ? 1u : 0u);
+#pragma unroll 1
+    for (uint32_t turn = 0; turn < turns; ++turn) {
+        const uint32_t u0 = turn * kOpThreads * kAtOnce + i, single = begin + pieces * P::N + i;
         float v[kElements];
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
@@ -211,15 +255,9 @@ __global__ __launch_bounds__(kOpThreads) void stats_kernel(const T *target, cons
 #pragma unroll
             for (int k = 0; k < P::N; ++k) v[j * P::N + k] = f[k];
         }
-        add(v, begin + u0 * P::N);
-    }
-    const uint32_t single = begin + pieces * P::N + i;
-    if (single < end) {
-        float v[kElements];
-#pragma unroll
-        for (int k = 0; k < kElements; ++k) v[k] = -INFINITY;
-        v[0] = (float)x[single];
-        add(v, single);
+        if (turn == whole && single < end) v[0] = (float)x[single];
+        if (!turn) __syncthreads();  // the roots are there, behind the first loads
+        add(v, turn == whole ? single : begin + u0 * P::N);
     }
     if (odd) st.sum = NAN;
     st = join_lanes<64>(st, factor, greedy);
@@ -313,6 +351,8 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
     __shared__ RowStat seen[kAtOnce][2];
     __shared__ double likely[kAtOnce][2];
     __shared__ double scan[kOpThreads / 64];
+    __shared__ Roots roots;
+    fill(roots);
     const uint32_t part = blockIdx.x % a.parts, r = blockIdx.x / a.parts, i = threadIdx.x;
     const int64_t first = draft_offset(a, r);
     const int64_t after = draft_offset(a, r + 1);
@@ -338,6 +378,7 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
             if (j < n) t = drafted(a, first + j);
         }
         const bool inside = t >= 0 && t < (int64_t)a.vocab;
+        __syncthreads();  // the roots are there
         if (i % 16 == 0) {
             double p = of_draft ? 1.0 : 0.0;  // of a draft that was certain
             if (asked && inside && greedy) {
@@ -345,7 +386,7 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
             } else if (asked && inside) {
                 const T v = of_draft ? draft[(first + j) * a.draft_stride + t]
                                      : target[(row0 + j) * a.target_stride + t];
-                p = power_or_zero(power_of(s.max, factor), (float)v) / s.sum;
+                p = power_or_zero(power_of(s.max, factor, 1000.0 / factor), (float)v, roots) / s.sum;
             }
             seen[local][of_draft] = s;
             likely[local][of_draft] = p;
@@ -362,7 +403,7 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
             if (i == 0) {
                 const RowStat of_row = seen[here - j0][0], of_q = seen[here - j0][1];
                 src.row = row0 + here;
-                src.power = power_of(of_row.max, factor);
+                src.power = power_of(of_row.max, factor, 1000.0 / factor);
                 src.inverse = good(of_row) ? 1.0 / of_row.sum : NAN;
                 src.draft = src.certain = -1;
                 src.at = of_row.at;
@@ -370,7 +411,7 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
                     src.certain = drafted(a, first + here);
                 } else if (here < n) {
                     src.draft = first + here;
-                    src.draft_power = power_of(of_q.max, factor);
+                    src.draft_power = power_of(of_q.max, factor, 1000.0 / factor);
                     src.draft_inverse = 1.0 / of_q.sum;
                     if (!good(of_q)) src.inverse = NAN;
                 }
@@ -394,10 +435,10 @@ __global__ __launch_bounds__(kOpThreads) void pick_kernel(const T *target, const
     const T *x = target + from.row * a.target_stride;
     const T *y = from.draft >= 0 ? draft + from.draft * a.draft_stride : nullptr;
     const auto probability = [&](float v) {
-        return power_or_zero(from.power, v) * from.inverse;
+        return power_or_zero(from.power, v, roots) * from.inverse;
     };
     const auto weight = [&](double p, float v, uint32_t c) {
-        if (y) p -= power_or_zero(from.draft_power, v) * from.draft_inverse;
+        if (y) p -= power_or_zero(from.draft_power, v, roots) * from.draft_inverse;
         else if ((int64_t)c == from.certain) p = 0.0;
         return p > 0.0 ? p : 0.0;
     };
@@ -534,12 +575,13 @@ struct Cut {
     uint32_t chunk, chunks, part, parts;
 };
 
-// Chunks of 65536 elements, or less where there are few rows; parts of 1024 elements, or more
+// Chunks of 65536 elements, or less where there are few rows (4096 workgroups, two rounds of
+// them, 73 us on the above, 2048 77, 8192 77); parts of 1024 elements, or more
 // where there are many requests, so that all workgroups run at once.
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
     int64_t chunk = 65536;
-    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 2048) chunk /= 2;
+    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 4096) chunk /= 2;
     const auto least = [&](int64_t size, int64_t most, int64_t unit) {
         const int64_t n = (vocab + most - 1) / most;
         return size < n ? (n + unit - 1) / unit * unit : size;
@@ -635,8 +677,13 @@ extern "C" int segtopk_verify_drafts(const segtopk_verify_args *args, void *work
         using T = decltype(v);
         const T *target = static_cast<const T *>(q.target.data);
         const T *draft = has_draft ? static_cast<const T *>(q.draft.data) : nullptr;
-        if (launch(stats_kernel<T>, dim3(rows * a.chunks), kOpThreads, stream, 0, target, draft,
-                   a) != hipSuccess)
+        // Four pieces a thread at once; one where a chunk has no more than two, so that nobody
+        // adds up nothing (one request of 32003: 14.7 against 12.4 us a call).
+        const auto stats = [&](auto kernel) {
+            return launch(kernel, dim3(rows * a.chunks), kOpThreads, stream, 0, target, draft, a);
+        };
+        const bool few = a.chunk <= 2 * kOpThreads * Piece<T>::N;
+        if ((few ? stats(stats_kernel<T, 1>) : stats(stats_kernel<T, 4>)) != hipSuccess)
             return SEGTOPK_HIP_ERROR;
         return status(launch(pick_kernel<T>, dim3(a.requests * a.parts), kOpThreads, stream, 0,
                              target, draft, a));
