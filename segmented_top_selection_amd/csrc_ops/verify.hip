@@ -576,8 +576,11 @@ struct Cut {
 };
 
 // Chunks of 65536 elements, or less where there are few rows (4096 workgroups, two rounds of
-// them, 73 us on the above, 2048 77, 8192 77); parts of 1024 elements, or more
-// where there are many requests, so that all workgroups run at once.
+// them, 73 us on the above, 2048 77, 8192 77).  Parts of 1024 elements, or more where there are
+// many requests, since each workgroup finds out for itself where the drafts stop: by 512, 1024,
+// 2048 workgroups at most 16 requests of 131072 29, 35, 45 us, 22 of 60179 18, 21, 27, 256 of
+// 32000 60, 67, 88, but 64 of 131072 77, 73, 74: two rounds of 64 elements a thread leave more
+// of the device idle at the end.
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
     int64_t chunk = 65536;
@@ -588,7 +591,8 @@ Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     };
     chunk = least(chunk, kMostChunks, 2048);
     int64_t part = kPart;
-    while (requests * ((vocab + part - 1) / part) > 2048 && part < 16384) part *= 2;
+    while (part < 16384 && requests * ((vocab + part - 1) / part) > (part < 8192 ? 512 : 1024))
+        part *= 2;
     part = least(part, kMostParts, kPart);
     return {(uint32_t)chunk, (uint32_t)((vocab + chunk - 1) / chunk), (uint32_t)part,
             (uint32_t)((vocab + part - 1) / part)};
