@@ -12,7 +12,7 @@
 // bytes a lane; a token is read once for all of its slots.  65536 rows of 4096 in bf16
 // 139 us, 5.8 TB/s; 8192 tokens of 4096 to 8 slots each 60 us, 5.7; 128 matrices of 2048 x
 // 4096 588 us, 5.5.  Transposed, 65536 rows of 2048 and 4096 columns 275 us, 4.4: the vector
-// units are busy 63% of that, and what is written goes to as many places as there are columns.
+// units are busy 59% of that, and what is written goes to as many places as there are columns.
 #include "quantize.h"
 
 namespace segtopk_ops {

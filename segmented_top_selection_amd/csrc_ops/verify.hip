@@ -20,9 +20,9 @@
 //                 which drafts stand, and adds up its chunk of the one row that is
 //                 drawn from; the last of a request to arrive finds the token
 //
-// 64 requests of up to seven drafts over 131072 entries in bf16: 73 us, of which 44 are the
+// 64 requests of up to seven drafts over 131072 entries in bf16: 72 us, of which 44 are the
 // statistics (27 without the powers; by the polynomial of degree 7 48, and then 38 without the
-// loads) and 31 the pick.  One request of 32003: 12.4 us, two launches and the pick's chain of
+// loads) and 30 the pick.  One request of 32003: 12.4 us, two launches and the pick's chain of
 // offsets, drafts, statistics, parts and places.
 #include <cmath>
 #include <type_traits>
