@@ -19,8 +19,9 @@
 //
 // Bound by the vector units, 88% busy: a wave's four tokens take some 1100 instructions,
 // 400 of them for eight picks and 200 for the gates in 64 bits.  32768 tokens, 8 of 256
-// experts in 4 of 8 groups, f32 by the sigmoid with a bias: 22.5 us, 1.6 TB/s, against 45.5
-// with all scores in 64 bits.  One token of 64 experts: 5.5 us a call, 4.4 of it the kernel.
+// experts in 4 of 8 groups, f32 by the sigmoid with a bias: 21.9 us, 1.6 TB/s, against 45.5
+// with all scores in 64 bits; 18.4 if no token were left for them, since all waves run at once
+// and wait for the one that has such a token.  One token of 64 experts: 5.5 us a call, 4.4 of it the kernel.
 #include <cmath>
 #include <type_traits>
 
@@ -157,6 +158,16 @@ template <int V, class S> __device__ inline void rule_out(const Mine<V> &a, S *s
     }
 }
 
+// What lane `lane` of the token's has; the wave's own is a scalar.
+template <int L> __device__ inline float score_of(float score, uint32_t lane) {
+    if constexpr (L < 64) return __shfl(score, (int)lane, L);
+    else return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(score), (int)lane));
+}
+template <int L> __device__ inline double score_of(double score, uint32_t lane) {
+    if constexpr (L < 64) return __shfl(score, (int)lane, L);
+    else return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(score), (int)lane),
+                                 __builtin_amdgcn_readlane(__double2loint(score), (int)lane));
+}
 // Rules out the experts of groups that are not kept.  With `off` (scores of 32 bits): whether
 // scores so far off, and by their sum's rounding, could make another choice.
 template <int L, int V, class S>
@@ -189,14 +200,14 @@ __device__ inline bool keep_groups(const Mine<V> &a, const RouteArgs &q, S *s, f
         const S over = score + by, under = score - by;
         uint32_t perhaps = 0;  // its own too
         for (uint32_t g = 0; g < q.groups; ++g) {
-            const S other = __shfl(score, (int)(g * q.group_lanes), L);
+            const S other = score_of<L>(score, g * q.group_lanes);
             before += other > over;
             perhaps += other >= under;
         }
         unsure = a.group < q.groups && score != kNone && before < q.kept && perhaps > q.kept;
     } else {
         for (uint32_t g = 0; g < q.groups; ++g) {
-            const S other = __shfl(score, (int)(g * q.group_lanes), L);
+            const S other = score_of<L>(score, g * q.group_lanes);
             before += other > score || (other == score && g < a.group);
         }
     }
@@ -206,31 +217,34 @@ __device__ inline bool keep_groups(const Mine<V> &a, const RouteArgs &q, S *s, f
     return unsure;
 }
 
-// The k best by comparing scores, equal ones by their index.
-template <int HOW, int L, int V>
+// The k best by comparing scores, equal ones by their index, by a whole wave.  A batch's waves
+// may all run at once, and one such token is then the last to be done.
+template <int HOW, int V>
 __device__ inline void choose_exactly(const Mine<V> &a, const RouteArgs &q, uint32_t *chosen) {
     using S = typename ScoreType<HOW>::type;
     constexpr S kNone = (S)-INFINITY;
     S s[V];
-    make_scores<HOW, L>(a, q, s);
+    make_scores<HOW, 64>(a, q, s);
     rule_out<V>(a, s);
-    keep_groups<L>(a, q, s, 0.0f);
+    keep_groups<64>(a, q, s, 0.0f);
 #pragma unroll 1
     for (uint32_t i = 0; i < q.k; ++i) {
         S m = s[0];
 #pragma unroll
         for (int j = 1; j < V; ++j) m = larger(m, s[j]);
-        m = join<L>(m, [](S p, S r) { return larger(p, r); });
-        uint32_t e = UINT32_MAX;
+        const S own = m;
+        m = join<64>(m, [](S p, S r) { return larger(p, r); });
+        // The lowest lane's lowest place.
+        const int first = __builtin_ctzll(__ballot(own == m));
+        uint32_t e = 0;
 #pragma unroll
         for (int j = V - 1; j >= 0; --j)
             if (s[j] == m) e = a.first + j;
-        if (m == kNone) e = UINT32_MAX;
-        const uint32_t won = join<L>(e, [](uint32_t p, uint32_t r) { return lower(p, r); });
+        const uint32_t won = m == kNone ? UINT32_MAX : (uint32_t)__builtin_amdgcn_readlane((int)e, first);
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (won == a.first + j) s[j] = kNone;
-        if (threadIdx.x % L == 0) chosen[i] = kExpert | won;
+        if (threadIdx.x % 64 == 0) chosen[i] = kExpert | won;
     }
 }
 
@@ -389,7 +403,7 @@ __global__ __launch_bounds__(kOpThreads) void route_kernel(const T *logits, Rout
             Mine<kFew> m = mine_of<kFew>(logits + (int64_t)(blockIdx.x * kTokens + there) * a.stride, a,
                                          wave.group_lanes, threadIdx.x % 64, true);
             m.top = __shfl(mine.top, (int)(which * L));
-            choose_exactly<kExactly, 64, kFew>(m, wave, chosen[there]);
+            choose_exactly<kExactly, kFew>(m, wave, chosen[there]);
         }
     }
     __syncthreads();
