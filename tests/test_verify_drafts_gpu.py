@@ -1,8 +1,8 @@
 """Verified drafts against a plain implementation in 64 bits.
 
-All results are whole numbers and have to be equal.  The kernels' probabilities are
-7e-12 off at most; a random uniform number is nearer than that to one of the borders of
-a row of 10^5 tokens once in 10^6 calls.
+All results are whole numbers and have to be equal.  The kernels' powers are 7e-11 off
+at most; a random uniform number is nearer than that to one of the borders of a row of
+10^5 tokens once in 10^5 calls.
 """
 import math
 
