@@ -46,6 +46,27 @@ def test_expert_matmul_many_large_tiles():
                            products.offsets_of([4001, 2303, 2696]), dtype=torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("rows,experts,width,depth", [
+    (900, 5, 130, 200), (2850, 1, 719, 1123),                     # few tiles
+    (3000, 70, 300, 400), (5000, 3, 1300, 1100), (60, 64, 257, 300)])  # many
+def test_dweights_forms(rows, experts, width, depth, dtype):
+    g = products.gen(rows + width)
+    off = products.offsets_of(shared(g, rows, experts) if experts > 1 else [rows])
+    dout = products.randn(g, rows, width, dtype=dtype, scale=0.1)
+    x = products.randn(g, rows, depth, dtype=dtype)
+    want, size = products.plain_dweights(dout, x, off)
+    for out_type in {dtype, torch.float32}:
+        inner = products.inner_of(off, size, out_type)
+        got = st.expert_matmul_dweights(dout, x, off, dtype=out_type)
+        products.close(got, want, inner)
+        before = products.randn(g, *want.shape, dtype=out_type)
+        out = before.clone()
+        st.expert_matmul_dweights(dout, x, off, out=out, accumulate=True)
+        both = want + before.double()
+        products.close(out, both, inner + products.STEP / 2 * (both.abs() + inner))
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_dweights_large_tiles(accumulate):
     g = products.gen(2)
