@@ -716,13 +716,17 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
         // time and by tiles of 128 x 128: 8 rows each 96, 111, 126, 124 us; 16 rows 104, 114,
         // 125, 122; 32 rows 192, 128, 135, 123.  Experts are not all alike, and one row too many
         // reads the weights again, hence 12 and 24.  Where tiles would leave most of the device
-        // idle, the blocks shared among waves are quicker at any number: one expert of 4096 to
-        // 8192, by 16, 32, 64 rows and tiles, 16 rows 11, 15, 16, 29 us; 64 rows 35, 23, 20, 43;
-        // 256 rows (128 tiles) 83, 57, 47, 69; 512 rows 158, 109, 77, 70.
+        // idle, the blocks shared among waves are quicker: one expert of 4096 to 8192, by 16, 32,
+        // 64 rows, 16 rows 11, 15, 16 us; 64 rows 35, 23, 20; 256 rows 83, 57, 47.  By 64 rows
+        // and by tiles of 64 x 128, with the squares below, in bf16 that one (192) 47 and 26; 2048
+        // to 2048, 256 rows (48) 17 and 15; 1024 to 1024, 512 rows (40) 10 and 10, 8 experts to
+        // 256, 128 rows each (32) 7 and 10.  In f32, whose products take twice as long, 192 squares
+        // 56 and 36, 72 35 and 34, 64 17 and 20; 16 experts of 2048 to 768, 40 rows each (126) 17
+        // and 19.
         const int64_t each = (q.num_rows + q.num_experts - 1) / q.num_experts;
         const int64_t squares =
             tiles_most(q.num_rows, q.num_experts, 128) * ((a.width + 127) / 128);
-        const bool few = squares < 200;
+        const bool few = squares < (each < 96 ? 200 : sizeof(T) == 2 ? 44 : 72);
         if (each <= (few ? 16 : 12)) return thin_by_width(integral_constant<int, 1>{});
         if (each <= (few ? 32 : 24)) return thin_by_width(integral_constant<int, 2>{});
         if (few) return thin_by_width(integral_constant<int, 4>{});

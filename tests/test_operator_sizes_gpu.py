@@ -30,6 +30,8 @@ def shared(g, rows, experts):
     (200, 40, 300, 129), (200, 40, 515, 260), (200, 40, 1000, 640),     # few rows an expert
     (800, 40, 200, 384), (800, 40, 300, 1001), (800, 40, 777, 515),     # twice as many
     (1000, 8, 500, 520), (1000, 8, 800, 515), (1000, 8, 1500, 130),     # few large tiles
+    (640, 8, 300, 129), (640, 8, 1000, 515), (640, 8, 1900, 260),       # fewer rows of them
+    (300, 2, 257, 400), (500, 3, 900, 200),                             # very few
     (1500, 20, 1000, 515),                                              # some
     (5000, 70, 700, 390),                                               # many
     (3000, 2, 5200, 330), (3000, 2, 5200, 128)])                        # of many rows an expert
