@@ -280,7 +280,9 @@ template <int L, int V> __device__ inline int32_t expert_of(uint32_t chosen, con
     if (chosen < kPlaces) return -1;
     const uint32_t place = kPlaces - 1 - chosen % kPlaces, lane = place / V;
     const uint32_t group = lane >> __builtin_ctz(q.group_lanes);  // a power of two
-    return (int32_t)(group * q.per_group + (lane & (q.group_lanes - 1)) * V + place % V);
+    const uint32_t expert = group * q.per_group + (lane & (q.group_lanes - 1)) * V + place % V;
+    // Its logit is loaded: no key may lead out of the row.
+    return expert < q.num_experts ? (int32_t)expert : -1;
 }
 
 // The k best by scores of 32 bits, as whole numbers over the range of the token's scores.
@@ -313,8 +315,11 @@ __device__ inline bool choose_nearly(const Mine<V> &a, const RouteArgs &q, uint3
     high = join<L>(high, [](float p, float r) { return larger(p, r); });
     low = join<L>(low, [](float p, float r) { return fminf(p, r); });
     const bool unsure = keep_groups<L>(a, q, s, HOW == kBy32 ? off : 0.0f);
-    // Nothing but one number, or numbers too far apart: all of them are near each other.
-    const float steps = high > low ? kSteps / (high - low) : 0.0f;
+    // Nothing but one number, or numbers too near each other or too far apart to be told by
+    // finite steps: all of them count as near each other.  kSteps is below 2^25, so that steps
+    // are below 2^125 and no number comes to more than kSteps and 2, or bit 31 of a key.
+    const float range = high - low;
+    const float steps = range >= 0x1p-100f ? kSteps / range : 0.0f;
     uint32_t key[V];
     const uint32_t place = threadIdx.x % L * V;
     if (clean && !__any(steps == 0.0f)) {

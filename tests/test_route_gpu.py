@@ -191,6 +191,41 @@ def test_far_logits():
         assert bool(((w.double() - want).abs() <= off * want + 2.0 ** -126).all())
 
 
+# Ranges of scores that no finite factor spreads over the keys' whole numbers, and some above.
+@pytest.mark.parametrize("size", [1e-45, 1e-42, 1.2e-38, 1e-36, 1e-33, 1e-31, 1e-29, 1e-20, 1e-9])
+@pytest.mark.parametrize("experts", [60, 64, 256, 512, 1000])
+def test_logits_that_lie_close_together(experts, size):
+    g = gen(experts)
+    rows = [torch.randint(-1000, 1001, (9, experts), generator=g, device=DEV) * size,  # far and near
+            torch.randint(-4, 5, (9, experts), generator=g, device=DEV) * size,        # equal ones
+            torch.zeros(9, experts, device=DEV), torch.zeros(2, experts, device=DEV)]
+    rows[2][torch.arange(9), torch.arange(9) * 6] = size  # one above the others, and below
+    rows[3][0, -1], rows[3][1, 3] = size, -size
+    rows.append(logits_of(g, 9, experts, torch.float32))  # in the same waves
+    x = torch.cat(rows)[torch.randperm(38, generator=g, device=DEV)]
+    want = x.cpu().double().sort(dim=1, descending=True, stable=True).indices.int()
+    for k in (1, 8, 60):
+        for scoring in ("softmax", "sigmoid"):
+            w, e = st.route(x, k, scoring=scoring)
+            assert torch.equal(e.cpu(), want[:, :k])
+            plain = plain_weights(x, e, scoring, True, 1.0)
+            assert bool(((w.double() - plain).abs() <= 1.01 * U * plain).all())
+    # One expert ruled out: none of the others is.
+    x[:, 5] = -math.inf
+    _, e = st.route(x, 59)
+    assert torch.equal(e.cpu(), x.cpu().double().sort(dim=1, descending=True, stable=True).indices[:, :59].int())
+
+
+@pytest.mark.parametrize("experts,groups,kept", [(60, 1, 1), (64, 1, 1), (256, 8, 3), (200, 5, 2), (512, 1, 1)])
+def test_sigmoids_that_lie_close_together(experts, groups, kept):
+    g = gen(experts + 1)
+    x = -88 + 16 * torch.rand(30, experts, generator=g, device=DEV)
+    x[:5] = -104 + torch.rand(5, experts, generator=g, device=DEV)  # nothing in 32 bits
+    for bias in (torch.zeros(experts, device=DEV), 1e-40 * torch.randn(experts, generator=g, device=DEV)):
+        for k in (1, 8, 32):
+            check(x, k, scoring="sigmoid", bias=bias, groups=groups, kept=kept)
+
+
 def test_nan_and_inf():
     x = torch.randn(6, 32, generator=gen(1), device=DEV)
     x[0, 3], x[1, 0], x[2, 5] = math.nan, math.inf, math.nan
