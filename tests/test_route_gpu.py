@@ -310,6 +310,33 @@ def test_gradient(tokens, experts, k, renormalize, scoring, dtype):
     check_gradient(dw, x, e, scoring, renormalize, 1.5)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("experts,k", [(2, 1), (64, 1), (64, 8), (200, 3), (1000, 64)])
+def test_gradient_of_a_confident_router(experts, k, dtype):
+    # One expert far above the others: its gradient p (g - <g, p>) is g p times what little is
+    # left for the others.
+    g = gen(experts + k)
+    gap = torch.tensor([4.0, 8.0, 12.0, 16.0, 20.0, 24.0], device=DEV)[:, None]
+    x = torch.rand(6, experts, generator=g, device=DEV) - gap
+    at = torch.randint(0, experts, (6, 1), generator=g, device=DEV)
+    x = x.scatter_(1, at, 0.0).to(dtype)
+    _, e = st.route(x, k, renormalize=False)
+    assert torch.equal(e[:, :1].long(), at)
+    dw = torch.randn(6, k, generator=g, device=DEV)
+    dw[:, 0] += 3.0
+    d = st.route_backward(dw, x, e, renormalize=False, scale=1.5).double()
+    # g - <g, p> as the sum of p_j (g - g_j), which leaves nothing to cancel but g - g_j.
+    p = torch.softmax(x.double(), 1)
+    full = torch.zeros_like(p).scatter_(1, e.long(), 1.5 * dw.double())
+    want = p * (p[:, None, :] * (full[:, :, None] - full[:, None, :])).sum(2)
+    # In 64 bits: the softmax's sum, the mean and the difference, each of the size of g.
+    size = p * (full.abs() + (p * full.abs()).sum(1, keepdim=True))
+    inner = (experts / 64 + 12) * 2.0 ** -53 * size + 2.0 ** -48 * want.abs()
+    eps = torch.finfo(dtype).eps / 2 + U  # by way of 32 bits
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 2.0 ** -133
+    assert bool(((d - want).abs() <= eps * want.abs() + 2 * inner + tiny).all())
+
+
 def test_gradient_slots_that_are_odd():
     g = gen(6)
     x = logits_of(g, 20, 16, torch.float32)
