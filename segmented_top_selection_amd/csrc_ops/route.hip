@@ -148,9 +148,11 @@ __device__ inline float make_scores(const Mine<V> &a, const RouteArgs &q, S *s) 
     return off;
 }
 
-// A lane's scores with what is ruled out at -inf, and a NaN at the lowest number.
+// A lane's scores with what is ruled out at -inf, and a NaN at the lowest number; in 64 bits at
+// -2^1022, which no score with a bias of 32 bits reaches, so that a group's two are a number
+// still and not what marks a group without experts.
 template <int V, class S> __device__ inline void rule_out(const Mine<V> &a, S *s) {
-    constexpr S kLowest = sizeof(S) == 8 ? (S)-1.7976931348623157e308 : (S)-3.4028234663852886e38f;
+    constexpr S kLowest = sizeof(S) == 8 ? (S)-0x1p1022 : (S)-3.4028234663852886e38f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (s[j] != s[j]) s[j] = kLowest;

@@ -226,6 +226,29 @@ def test_sigmoids_that_lie_close_together(experts, groups, kept):
             check(x, k, scoring="sigmoid", bias=bias, groups=groups, kept=kept)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("experts", [16, 240, 1024])
+def test_groups_of_nan(experts, dtype):
+    # A NaN is the lowest score that is not ruled out, and so are two: its group has experts left.
+    size, none, nan = experts // 4, -math.inf, math.nan
+    x = torch.full((6, 4, size), none)
+    x[0, 1] = x[0, 3] = nan                    # two groups of NaN next to two that are ruled out
+    x[1, 3] = nan
+    x[2, 2, 1] = nan                           # one NaN alone
+    x[3, 0], x[3, 2, :2] = nan, torch.tensor([nan, -3.0])  # a number and a NaN before two NaN
+    x[4, 0], x[4, 1], x[4, 3] = nan, -9.0, 2.0
+    x[5, 1:3] = nan
+    first = [[size, size + 1], [3 * size, 3 * size + 1], [2 * size + 1, -1],
+             [2 * size + 1, 2 * size], [3 * size, 3 * size + 1], [size, size + 1]]
+    x = x.view(6, experts).to(DEV, dtype)
+    for bias in (None, torch.zeros(experts, device=DEV)):
+        for best in (1, 2):
+            _, e = st.route(x, 2, scoring="sigmoid", bias=bias, groups=4, kept_groups=1, group_best=best)
+            assert e.tolist() == first
+            _, e = st.route(x, 2, scoring="sigmoid", bias=bias, groups=4, kept_groups=3, group_best=best)
+            assert bool((e[:, 0] >= 0).all()) and bool((e[[0, 1, 3, 4, 5], 1] >= 0).all())
+
+
 def test_nan_and_inf():
     x = torch.randn(6, 32, generator=gen(1), device=DEV)
     x[0, 3], x[1, 0], x[2, 5] = math.nan, math.inf, math.nan
