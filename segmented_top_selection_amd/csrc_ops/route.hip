@@ -175,6 +175,7 @@ template <int L> __device__ inline double score_of(double score, uint32_t lane) 
 template <int L, int V, class S>
 __device__ inline bool keep_groups(const Mine<V> &a, const RouteArgs &q, S *s, float off) {
     constexpr S kNone = (S)-INFINITY;
+    constexpr float kMost = 3.4028234663852886e38f;
     if (q.kept >= q.groups) return false;
     Best<S> b{kNone, kNone};
 #pragma unroll
@@ -192,6 +193,9 @@ __device__ inline bool keep_groups(const Mine<V> &a, const RouteArgs &q, S *s, f
     }
     S score = b.first;
     if (q.best > 1 && b.second != kNone) score += b.second;
+    // Scores of 32 bits whose sum leaves them stay at their end, where they are near each other:
+    // -inf marks a group without experts, and nothing is near an infinity.
+    if (off > 0.0f && b.first != kNone) score = larger((S)-kMost, score < (S)kMost ? score : (S)kMost);
     uint32_t before = 0;
     bool unsure = false;
     if (off > 0.0f) {

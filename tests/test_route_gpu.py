@@ -249,6 +249,38 @@ def test_groups_of_nan(experts, dtype):
             assert bool((e[:, 0] >= 0).all()) and bool((e[[0, 1, 3, 4, 5], 1] >= 0).all())
 
 
+def test_groups_of_biases_whose_sums_leave_32_bits():
+    x = torch.randn(9, 32, generator=gen(21), device=DEV)
+    far = [[3e38, 3e38, 0, 0], [3.2e38, 3.1e38, 0, 0], [0, 0, 0, 0], [3.3e38, 0, 1, 2],
+           [-3.1e38, -3.2e38, -3.3e38, -3.4e38], [-3e38] * 4, [-math.inf] * 4, [-3.05e38, -math.inf, 0, 0]]
+    # Apart from each other, so that nothing but the groups' sums is in doubt.
+    above = [[3e38 - 1e36 * i, 2e38 + 1.1e37 * (i % 3) + 2e35 * i, 1e38 - 1e36 * i, 1e37 - 1e36 * i]
+             for i in range(8)]
+    below = [[-1.8e38 - 1e36 * i, -2e38 - 1.1e37 * (i % 3) - 2e35 * i, -3e38 - 1e36 * i, -3.2e38 - 1e36 * i]
+             for i in range(7)] + [[0, -1e37, -2e37, -3e37]]
+    order = torch.randperm(8, generator=gen(22), device=DEV).tolist()
+    for groups in (far, far[::-1], [far[i] for i in order], far[4:7] * 2 + far[4:6], far[4:7][::-1] * 2 + far[4:6],
+                   above, above[::-1], below, below[::-1], [below[i] for i in order]):
+        bias = torch.tensor(groups, device=DEV).view(32)
+        for kept in (1, 2, 3):
+            for scoring in ("sigmoid", "softmax"):
+                check(x, 4 * kept, scoring=scoring, bias=bias, groups=8, kept=kept)
+                check(x, 4, scoring=scoring, bias=bias, groups=8, kept=kept, best=1)
+
+
+def test_groups_by_an_infinite_logit():
+    most = torch.finfo(torch.float32).max
+    x = torch.tensor([[most, 0, 1, 2, math.inf, 3, 4, 5, -most, -1, -2, -3]], device=DEV)
+    for kept, want in ((1, [4, 7, 6, 5]), (2, [4, 0, 7, 6])):
+        _, e = st.route(x, 4, scoring="sigmoid", groups=3, kept_groups=kept, group_best=1)
+        assert e[0].tolist() == want
+    # The same by a bias, where sums of two are compared.
+    bias = x[0].clone()
+    for best in (1, 2):
+        _, e = st.route(torch.zeros_like(x), 4, bias=bias, scoring="sigmoid", groups=3, kept_groups=1, group_best=best)
+        assert e[0].tolist() == [4, 7, 6, 5]
+
+
 def test_nan_and_inf():
     x = torch.randn(6, 32, generator=gen(1), device=DEV)
     x[0, 3], x[1, 0], x[2, 5] = math.nan, math.inf, math.nan
