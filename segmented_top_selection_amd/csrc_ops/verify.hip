@@ -576,11 +576,13 @@ struct Cut {
 };
 
 // Chunks of 65536 elements, or less where there are few rows (4096 workgroups, two rounds of
-// them, 73 us on the above, 2048 77, 8192 77).  Parts of 1024 elements, or more where there are
-// many requests, since each workgroup finds out for itself where the drafts stop: by 512, 1024,
-// 2048 workgroups at most 16 requests of 131072 29, 35, 45 us, 22 of 60179 18, 21, 27, 256 of
-// 32000 60, 67, 88, but 64 of 131072 77, 73, 74: two rounds of 64 elements a thread leave more
-// of the device idle at the end.
+// them, 73 us on the above, 2048 77, 8192 77).  Parts of 1024 elements, or up to 8192 where there
+// are many requests, since each workgroup finds out for itself where the drafts stop.  By 512 and
+// 1024 workgroups before they grow: 8 requests of 131072 entries, up to 7 drafts, 26 and 30 us, 16
+// 32 and 39, 32 of 65536 37 and 41, 128 of 32000 47 and 58, 64 of 65536 53 and 50.  By parts of up
+// to 4096, 8192, 16384: 64 of 131072 69, 71, 73, 128 with up to 3 drafts 91, 88, 121, 256 with up
+// to one 136, 121, 164, 512 of 50257 169, 171, 232, 256 of 32000 98, 69, 66.  Past that only
+// where a launch would not hold them.
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
     int64_t chunk = 65536;
@@ -591,8 +593,7 @@ Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     };
     chunk = least(chunk, kMostChunks, 2048);
     int64_t part = kPart;
-    while (part < 16384 && requests * ((vocab + part - 1) / part) > (part < 8192 ? 512 : 1024))
-        part *= 2;
+    while (requests * ((vocab + part - 1) / part) > (part < 8192 ? 512 : kMostBlocks)) part *= 2;
     part = least(part, kMostParts, kPart);
     return {(uint32_t)chunk, (uint32_t)((vocab + chunk - 1) / chunk), (uint32_t)part,
             (uint32_t)((vocab + part - 1) / part)};

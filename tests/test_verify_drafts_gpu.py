@@ -111,6 +111,15 @@ def test_verify(lengths, vocab, drafted, dtype):
     check(inputs(g, lengths, vocab, dtype, drafted, ids=torch.int32 if drafted else torch.int64))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=NAMES.get)
+@pytest.mark.parametrize("requests,vocab", [(40, 12000), (60, 16400), (130, 8200), (130, 20000), (300, 8191),
+                                            (300, 16385), (600, 1025)])
+def test_rows_drawn_from_in_larger_parts(requests, vocab, dtype):
+    # The more requests, the fewer workgroups share a row.
+    g = gen(requests + vocab)
+    check(inputs(g, [r % 3 % 2 for r in range(requests)], vocab, dtype))
+
+
 @pytest.mark.parametrize("temperature", [0.0, 0.05, 0.7, 1.0, 30.0])
 @pytest.mark.parametrize("drafted", [False, True])
 def test_temperatures(temperature, drafted):
