@@ -575,18 +575,20 @@ struct Cut {
     uint32_t chunk, chunks, part, parts;
 };
 
-// Chunks of 65536 elements, or less where there are few rows (4096 workgroups, two rounds of
-// them, 73 us on the above, 2048 77, 8192 77).  Parts of 1024 elements, or up to 8192 where there
-// are many requests, since each workgroup finds out for itself where the drafts stop.  By 512 and
-// 1024 workgroups before they grow: 8 requests of 131072 entries, up to 7 drafts, 26 and 30 us, 16
-// 32 and 39, 32 of 65536 37 and 41, 128 of 32000 47 and 58, 64 of 65536 53 and 50.  By parts of up
-// to 4096, 8192, 16384: 64 of 131072 69, 71, 73, 128 with up to 3 drafts 91, 88, 121, 256 with up
-// to one 136, 121, 164, 512 of 50257 169, 171, 232, 256 of 32000 98, 69, 66.  Past that only
-// where a launch would not hold them.
+// Chunks of 65536 elements, or less where there are few rows.  By 1024, 2048, 4096, 8192
+// workgroups: 32 requests of 131072 entries and up to 7 drafts 45, 45, 47, 47 us, 64 of them 74,
+// 72, 71, 79, 48 of 100000 56, 52, 55, 55, 64 of 65536 51, 50, 53, 55, 128 of 131072 and up to 3
+// 92, 90, 88, 97, 512 of 32000 and up to 2 113, 111, 116, 119, 1024 of 8000 78, 78, 85, 89.
+// Parts of 1024 elements, or up to 8192 where there are many requests, since each workgroup finds
+// out for itself where the drafts stop.  By 512 and 1024 workgroups before they grow: 8 requests of
+// 131072 entries, up to 7 drafts, 26 and 30 us, 16 32 and 39, 32 of 65536 37 and 41, 128 of 32000
+// 47 and 58, 64 of 65536 53 and 50.  By parts of up to 4096, 8192, 16384: 64 of 131072 69, 71,
+// 73, 128 with up to 3 drafts 91, 88, 121, 256 with up to one 136, 121, 164, 512 of 50257 169,
+// 171, 232, 256 of 32000 98, 69, 66.  Past that only where a launch would not hold them.
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
     int64_t chunk = 65536;
-    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 4096) chunk /= 2;
+    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 2048) chunk /= 2;
     const auto least = [&](int64_t size, int64_t most, int64_t unit) {
         const int64_t n = (vocab + most - 1) / most;
         return size < n ? (n + unit - 1) / unit * unit : size;
