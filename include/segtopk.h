@@ -572,7 +572,7 @@ int segtopk_expert_dweights(const segtopk_expert_dweights_args *args, void *work
  * stand.  A row with NaN or +inf, or nothing but -inf, has no distribution: the draft
  * does not stand if its target row or its draft row is such a one, and the token
  * drawn from such a row (or from one whose draft row is) is -1.
- * Probabilities and sums are in 64 bits.  Offsets do not decrease, from 0 to
+ * Probabilities and sums are in 64 bits (powers within 2^-43).  Offsets do not decrease, from 0 to
  * num_drafts.  num_drafts + num_requests < 2^22, 1 <= vocab < 2^31.
  * SEGTOPK_NOT_SUPPORTED: more parts of 65536 elements (16 a row at most) than 2^24 - 1.
  */

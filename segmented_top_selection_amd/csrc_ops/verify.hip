@@ -10,9 +10,9 @@
 // The running sum passes a border at each of some 10^5 tokens, a few 10^-6 of the
 // whole apart: sums of 32 bits, 10^-7 off, would pick another token once in a
 // hundred calls.  All is in 64 bits, whose vector rate is that of 32 here: 2^t is
-// one of 32 roots in LDS, a polynomial of degree 3 on [-1/64, 1/64], 7e-11 off, and
-// an addition to the exponent, some 13 instructions for an element that takes as long
-// to load.  (Without roots it is a polynomial of degree 7 and 15 instructions.)
+// one of 32 roots in LDS, a polynomial of degree 4 on [-1/64, 1/64], 8e-14 off, and
+// an addition to the exponent, some 14 instructions for an element that takes as long
+// to load.  (Without roots it is a polynomial of degree 9.)
 //
 //   stats_kernel  every row in chunks: the maximum, the sum of 2^(x - max) (the
 //                 place of the maximum, for temperature 0)
@@ -114,8 +114,9 @@ __device__ inline double between(float from, float to, double factor) {
     return __hiloint2double((1023 + e) << 20, 0);
 }
 // Its exponent is n + j / 32 + f: an addition that leaves 32nds the last bit has n and j in the
-// low word, f is what is over, and 2^f the polynomial of degree 3 that goes through it at the
-// Chebyshev points of [-1/64, 1/64].  The whole low word goes 15 bits up to the root's high
+// low word, f is what is over, and 2^f the polynomial of degree 4 that goes through it at the
+// Chebyshev points of [-1/64, 1/64], 8e-14 off: as near as a running sum of 10^5 numbers in 64
+// bits is.  (Degree 3, 7e-11 off: 64 requests 71.7 against 72.9 us.)  The whole low word goes 15 bits up to the root's high
 // word, n into the exponent, and takes back j << 15.
 struct Factors {
     double root, poly;  // their product is the power
@@ -124,9 +125,10 @@ __device__ inline Factors factors(const Power &a, double x, const Roots &roots) 
     const double s = fma(x, a.factor, a.round), f = fma(x, a.factor, a.round - s);
     const uint32_t k = (uint32_t)__double2loint(s);
     const uint2 r = roots.of[k % 32];
-    double p = fma(f, 0.055504434191939005, 0.24022885514318595);
-    p = fma(p, f, 0.693147180550011);
-    p = fma(p, f, 0.9999999999283391);
+    double p = fma(f, 0.009618176115571158, 0.055504515573860415);
+    p = fma(p, f, 0.24022650695623157);
+    p = fma(p, f, 0.6931471805351095);
+    p = fma(p, f, 1.0);
     return {__hiloint2double((int)(r.y + (k << 15)), (int)r.x), p};
 }
 // The sum so far and one power more.

@@ -136,6 +136,31 @@ def test_a_temperature_for_each_request():
     check(s)
 
 
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 2.5])
+def test_borders_that_34_bits_would_miss(temperature):
+    # Two tokens, and uniform numbers nearer than 3e-11 to the first one's probability.  In 64
+    # bits a power is 1e-13 off at most, and so is a probability p0 (the largest power is exact up
+    # to that too): p0 (1 - p0) 2e-13 <= 5e-14, and some 2^-52.
+    n = 1 << 22
+    x = 5 * torch.randn(n, generator=gen(15), device=DEV)
+    p = 1 / (1 + torch.exp(x.double() / temperature))
+    u = p.float()
+    away = (p - u.double()).abs()
+    at = ((away > 2e-13) & (away < 3e-11) & (u < 1)).nonzero()[:, 0]
+    assert at.numel() > 500
+    x, p, u = x[at], p[at], u[at]
+    target = torch.stack([torch.zeros_like(x), x], 1)
+    n = at.numel()
+    none = torch.zeros(0, device=DEV)
+    zeros = torch.zeros(n + 1, dtype=torch.int64, device=DEV)
+    tokens, _ = st.verify_drafts(target, zeros[:0], zeros, none, u, temperature=temperature)
+    assert torch.equal(tokens, (p <= u.double()).long())
+    # A certain draft of the first token stands if u < p.
+    _, counts = st.verify_drafts(target.repeat_interleave(2, 0), zeros[:n], torch.arange(n + 1, device=DEV), u, u,
+                                 temperature=temperature)
+    assert torch.equal(counts == 2, u.double() < p)
+
+
 def test_all_stand_and_none_stands():
     g = gen(6)
     for near in (0.0, 8.0):  # the draft is the target; it is far from it
