@@ -508,7 +508,9 @@ int segtopk_quantize_blocks(const segtopk_matrices *x, const segtopk_matrices *q
  * matrices of width x depth, both SEGTOPK_E4M3; out is num_rows x width.  Offsets do
  * not decrease and are within [0, num_rows].  Sums are held in 32 bits; for a result
  * of 16, each eight products are added up with the smaller cut off at 2^-13 of the
- * largest, as the 8-bit matrix instruction does.
+ * largest, as the 8-bit matrix instruction does.  The product of a row's and a weight's
+ * scale is one number of 32 bits: results below some 2^-100 lose bits to it, and one of
+ * 2^128 or more is inf.
  * With the weights (and their scales) transposed this is the gradient of the rows.
  * num_rows < 2^31 - 1025, 1 <= num_experts <= 65535.  SEGTOPK_NOT_SUPPORTED: a row
  * stride of 2^24 or more, or 2^24 tiles or more (16 x 16 results at the least, 256 x
@@ -572,8 +574,8 @@ int segtopk_expert_dweights(const segtopk_expert_dweights_args *args, void *work
  * stand.  A row with NaN or +inf, or nothing but -inf, has no distribution: the draft
  * does not stand if its target row or its draft row is such a one, and the token
  * drawn from such a row (or from one whose draft row is) is -1.
- * Probabilities and sums are in 64 bits (powers within 2^-43).  Offsets do not decrease, from 0 to
- * num_drafts.  num_drafts + num_requests < 2^22, 1 <= vocab < 2^31.
+ * Probabilities and sums are in 64 bits (powers within 2^-43).  Offsets do not decrease,
+ * from 0 to num_drafts.  num_drafts + num_requests < 2^22, 1 <= vocab < 2^31.
  * SEGTOPK_NOT_SUPPORTED: more parts of 65536 elements (16 a row at most) than 2^24 - 1.
  */
 typedef struct segtopk_verify_args {

@@ -107,7 +107,8 @@ __device__ inline double factor_of(double temperature) {
     return fmin(kLog2e / temperature, 0x1p830);
 }
 // What a sum by one maximum is multiplied by to become one by a larger: a power of two.
-// (A sum by -inf is zero, and stays so.)
+// (A sum by -inf is n 2^-1000 for n elements, and what it is multiplied by is never above one: beside
+// a row's sum, of which the largest element alone is 2^-0.5 or more, it is nothing.)
 __device__ inline double between(float from, float to, double factor) {
     const double d = shift_of(from, factor) - shift_of(to, factor);
     const int e = d > 0.0 ? 0 : d < -1020.0 ? -1020 : (int)d;
