@@ -504,13 +504,13 @@ int segtopk_quantize_blocks(const segtopk_matrices *x, const segtopk_matrices *q
  *   out[r][n] = sum_b row_scales[r][b] weight_scales[e][n / 128][b]
  *                     sum over block b's c of rows[r][c] weights[e][n][c]
  * for the rows offsets[e] .. offsets[e + 1] of expert e; rows from
- * offsets[num_experts] on are zero.  rows is num_rows x depth, weights num_experts
- * matrices of width x depth, both SEGTOPK_E4M3; out is num_rows x width.  Offsets do
- * not decrease and are within [0, num_rows].  Sums are held in 32 bits; for a result
- * of 16, each eight products are added up with the smaller cut off at 2^-13 of the
- * largest, as the 8-bit matrix instruction does.  The product of a row's and a weight's
- * scale is one number of 32 bits: results below some 2^-100 lose bits to it, and one of
- * 2^128 or more is inf.
+ * offsets[num_experts] on are zero, those before offsets[0] are not written.  rows is
+ * num_rows x depth, weights num_experts matrices of width x depth, both SEGTOPK_E4M3; out
+ * is num_rows x width.  Offsets do not decrease and are within [0, num_rows].  Sums are
+ * held in 32 bits; for a result of 16, each eight products are added up with the smaller
+ * cut off at 2^-13 of the largest, as the 8-bit matrix instruction does.  The product of a
+ * row's and a weight's scale is one number of 32 bits: results below some 2^-100 lose bits
+ * to it, and one of 2^128 or more is inf.
  * With the weights (and their scales) transposed this is the gradient of the rows.
  * num_rows < 2^31 - 1025, 1 <= num_experts <= 65535.  SEGTOPK_NOT_SUPPORTED: a row
  * stride of 2^24 or more, or 2^24 tiles or more (16 x 16 results at the least, 256 x

@@ -117,7 +117,7 @@ __device__ inline double between(float from, float to, double factor) {
 // Its exponent is n + j / 32 + f: an addition that leaves 32nds the last bit has n and j in the
 // low word, f is what is over, and 2^f the polynomial of degree 4 that goes through it at the
 // Chebyshev points of [-1/64, 1/64], 8e-14 off: as near as a running sum of 10^5 numbers in 64
-// bits is.  (Degree 3, 7e-11 off: 64 requests 71.7 against 72.9 us.)  The whole low word goes 15 bits up to the root's high
+// bits is.  (Degree 3, 7e-11 off: 64 requests 76 against 77 us.)  The whole low word goes 15 bits up to the root's high
 // word, n into the exponent, and takes back j << 15.
 struct Factors {
     double root, poly;  // their product is the power
@@ -579,15 +579,16 @@ struct Cut {
 };
 
 // Chunks of 65536 elements, or less where there are few rows.  By 1024, 2048, 4096, 8192
-// workgroups: 32 requests of 131072 entries and up to 7 drafts 45, 45, 47, 47 us, 64 of them 74,
-// 72, 71, 79, 48 of 100000 56, 52, 55, 55, 64 of 65536 51, 50, 53, 55, 128 of 131072 and up to 3
-// 92, 90, 88, 97, 512 of 32000 and up to 2 113, 111, 116, 119, 1024 of 8000 78, 78, 85, 89.
+// workgroups, new inputs in turn: 32 requests of 131072 entries and up to 7 drafts 48, 48, 50,
+// 50 us, 64 of them 77, 76, 74, 80, 48 of 100000 60, 53, 57, 57, 64 of 65536 52, 52, 54, 56, 128 of
+// 131072 and up to 3 97, 95, 92, 98, 512 of 32000 and up to 2 115, 113, 117, 120, 1024 of 8000 81,
+// 81, 87, 91.
 // Parts of 1024 elements, or up to 8192 where there are many requests, since each workgroup finds
-// out for itself where the drafts stop.  By 512 and 1024 workgroups before they grow: 8 requests of
-// 131072 entries, up to 7 drafts, 26 and 30 us, 16 32 and 39, 32 of 65536 37 and 41, 128 of 32000
-// 47 and 58, 64 of 65536 53 and 50.  By parts of up to 4096, 8192, 16384: 64 of 131072 69, 71,
-// 73, 128 with up to 3 drafts 91, 88, 121, 256 with up to one 136, 121, 164, 512 of 50257 169,
-// 171, 232, 256 of 32000 98, 69, 66.  Past that only where a launch would not hold them.
+// out for itself where the drafts stop.  By 512 and 1024 workgroups before they grow: 8 requests
+// of 131072 entries, up to 7 drafts, 27 and 31 us, 16 35 and 41, 32 of 65536 39 and 43, 128 of
+// 32000 49 and 60, 64 of 65536 54 and 51.  By parts of up to 4096, 8192, 16384: 64 of 131072 76,
+// 74, 79, 128 with up to 3 drafts 96, 92, 115, 256 with up to one 132, 123, 176, 512 of 50257 164,
+// 166, 222, 256 of 32000 96, 70, 67.  Past that only where a launch would not hold them.
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
     int64_t chunk = 65536;

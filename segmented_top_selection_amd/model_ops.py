@@ -7,8 +7,8 @@ top-k picks the next token: ``embedding`` looks it up, ``policy_loss`` scores
 sampled tokens under the model's logits.  ``route`` is a router's whole selection, from
 scores to gate weights; ``dispatch_quantized`` and ``expert_matmul`` are the experts'
 products in 8 bits; ``verify_drafts`` says which tokens of a draft model stand.  The
-gradients are calls of their own
-(``*_backward``, ``policy_loss_grad``, ``expert_matmul_dweights``); none of them records an autograd graph.
+gradients are calls of their own (``*_backward``, ``policy_loss_grad``,
+``expert_matmul_dweights``); none of them records an autograd graph.
 
 Like ``batched_topk`` these only marshal arguments, in ``_binding`` (built from
 csrc_ops/binding.cpp): tensor metadata is checked before anything is queued,
@@ -412,7 +412,9 @@ def expert_matmul(rows: torch.Tensor, row_scales: torch.Tensor, weights: torch.T
     dtype          of the result: bfloat16 (default), float16 or float32
     Sums are held in 32 bits; for a result of 16 each eight products are added up with
     the smaller cut off at 2^-13 of the largest, as the 8-bit matrix instruction does.
-    Returns (rows, width); rows from offsets[-1] on are zero.  Operands whose rows do not begin at multiples of 16 bytes are copied first.
+    Returns (rows, width); rows from offsets[-1] on are zero, those before offsets[0]
+    are not written.  Operands whose rows do not begin at multiples of 16 bytes are
+    copied first.
 
     The gradient of the rows is the same call on quantize_rows' of the result's
     gradient, and the weights transposed:
