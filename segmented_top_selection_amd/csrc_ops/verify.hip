@@ -117,7 +117,7 @@ __device__ inline double between(float from, float to, double factor) {
 // Its exponent is n + j / 32 + f: an addition that leaves 32nds the last bit has n and j in the
 // low word, f is what is over, and 2^f the polynomial of degree 4 that goes through it at the
 // Chebyshev points of [-1/64, 1/64], 8e-14 off: as near as a running sum of 10^5 numbers in 64
-// bits is.  (Degree 3, 7e-11 off: 64 requests 76 against 77 us.)  The whole low word goes 15 bits up to the root's high
+// bits is.  (Degree 3, 7e-11 off: 64 requests 73.8 against 74.7 us.)  The whole low word goes 15 bits up to the root's high
 // word, n into the exponent, and takes back j << 15.
 struct Factors {
     double root, poly;  // their product is the power
@@ -578,11 +578,11 @@ struct Cut {
     uint32_t chunk, chunks, part, parts;
 };
 
-// Chunks of 65536 elements, or less where there are few rows.  By 1024, 2048, 4096, 8192
-// workgroups, new inputs in turn: 32 requests of 131072 entries and up to 7 drafts 48, 48, 50,
-// 50 us, 64 of them 77, 76, 74, 80, 48 of 100000 60, 53, 57, 57, 64 of 65536 52, 52, 54, 56, 128 of
-// 131072 and up to 3 97, 95, 92, 98, 512 of 32000 and up to 2 115, 113, 117, 120, 1024 of 8000 81,
-// 81, 87, 91.
+// Chunks of 65536 elements, or less where there are few rows.  By 2048, 4096, 8192 workgroups, new
+// inputs in turn: 64 requests of 131072 entries and up to 7 drafts 78, 74, 80 us, 128 and up to 3
+// 95, 91, 97, 1024 of 32000 and one 188, 184, 187; but 32 of 131072 45, 48, 50, 48 of 100000 52, 57,
+// 57, 64 of 65536 51, 54, 56, 64 of 128256 and up to 5 65, 70: neither of the first two is ahead
+// everywhere.
 // Parts of 1024 elements, or up to 8192 where there are many requests, since each workgroup finds
 // out for itself where the drafts stop.  By 512 and 1024 workgroups before they grow: 8 requests
 // of 131072 entries, up to 7 drafts, 27 and 31 us, 16 35 and 41, 32 of 65536 39 and 43, 128 of
@@ -592,7 +592,7 @@ struct Cut {
 Cut cut_of(int64_t drafts, int64_t requests, int64_t vocab) {
     const int64_t rows = 2 * drafts + requests;
     int64_t chunk = 65536;
-    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 2048) chunk /= 2;
+    while (chunk > 2048 && rows * ((vocab + chunk - 1) / chunk) < 4096) chunk /= 2;
     const auto least = [&](int64_t size, int64_t most, int64_t unit) {
         const int64_t n = (vocab + most - 1) / most;
         return size < n ? (n + unit - 1) / unit * unit : size;
