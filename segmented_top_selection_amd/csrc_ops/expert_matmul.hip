@@ -10,9 +10,9 @@
 // The 8-bit instruction adds up 8 products at a time with the smaller ones cut off
 // 2^-13 below the largest (the exponents' sum): 1.5e-5 of a sum of random values,
 // far below the 2^-9 and 2^-12 that a result in bf16 or f16 is rounded by, and taken
-// there for its rate: loops of nothing else reach 4870 TFLOP/s against 2080.  A result in 32 bits is held to them:
-// its operands are widened to bf16, which holds e4m3 whole, and multiplied by the
-// bf16 instruction, whose sums are right to 32 bits.
+// there for its rate: loops of nothing else reach 4870 TFLOP/s against 2080.  A result
+// in 32 bits is held to them: its operands are widened to bf16, which holds e4m3 whole,
+// and multiplied by the bf16 instruction, whose sums are right to 32 bits.
 //
 // The operand whose index is the result's fast one ("columns": n) is the
 // instruction's first, so that a lane holds neighbouring columns of one row: it
@@ -722,11 +722,12 @@ extern "C" int segtopk_expert_matmul(const segtopk_expert_matmul_args *args, hip
         // to 2048, 256 rows (48) 17 and 15; 1024 to 1024, 512 rows (40) 10 and 10, 8 experts to
         // 256, 128 rows each (32) 7 and 10.  In f32, whose products take twice as long, 192 squares
         // 56 and 36, 72 35 and 34, 64 17 and 20; 16 experts of 2048 to 768, 40 rows each (126) 17
-        // and 19.  All of this is for depths of 1024 and more.  In shallow products the waves that share
-        // an expert's blocks have few or none, and where they are wide tiles of 64 x 128 would be
-        // quicker: 64 experts to 2048, 16 rows each, by what is taken here and by those, a depth of
-        // 128 14.5 and 7.4, 512 22 and 15, 1024 33 and 23; 128 to 1024, 8 rows each, 128 11.4 and
-        // 7.6; where there are less than 200 squares the two are within a third of each other.
+        // and 19.  All of this is for depths of 1024 and more.  In shallower products the waves that
+        // share an expert's blocks have few or none, and of many experts tiles of 64 x 128 would be
+        // quicker: 64 to 2048, 16 rows each, weights in the last cache, by what is taken here and by
+        // those, a depth of 128 14.5 and 7.4, 512 22 and 15, 1024 33 and 23; 128 to 1024, 8 rows
+        // each, a depth of 128 11.4 and 7.6.  Under 200 squares all forms but those of 128 x 128 are
+        // within a third of each other there.
         const int64_t each = (q.num_rows + q.num_experts - 1) / q.num_experts;
         const int64_t squares =
             tiles_most(q.num_rows, q.num_experts, 128) * ((a.width + 127) / 128);

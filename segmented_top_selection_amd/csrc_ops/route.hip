@@ -17,11 +17,11 @@
 // and the lower index is the lower lane and the lower place in it.  The k best are
 // taken one after the other, each by the largest of a lane's V and a butterfly.
 //
-// Bound by the vector units, 88% busy: a wave's four tokens take some 1100 instructions,
+// Bound by the vector units, 90% busy: a wave's four tokens take some 1100 instructions,
 // 400 of them for eight picks and 200 for the gates in 64 bits.  32768 tokens, 8 of 256
 // experts in 4 of 8 groups, f32 by the sigmoid with a bias: 21.9 us, 1.6 TB/s, against 45.5
 // with all scores in 64 bits; 18.4 if no token were left for them, since all waves run at once
-// and wait for the one that has such a token.  One token of 64 experts: 5.5 us a call, 4.4 of it the kernel.
+// and wait for the one that has such a token.  One token of 64 experts: 5.5 us a call, 4.0 of it the kernel.
 #include <cmath>
 #include <type_traits>
 

@@ -20,9 +20,9 @@
 //                 which drafts stand, and adds up its chunk of the one row that is
 //                 drawn from; the last of a request to arrive finds the token
 //
-// 64 requests of up to seven drafts over 131072 entries in bf16: 72 us, of which 44 are the
-// statistics (27 without the powers; by the polynomial of degree 7 48, and then 38 without the
-// loads) and 30 the pick.  One request of 32003: 12.4 us, two launches and the pick's chain of
+// 64 requests of up to seven drafts over 131072 entries in bf16: 75 us, of which 45 are the
+// statistics (27 without the powers; without roots, by a polynomial of degree 7, 48, and then 38
+// without the loads) and 31 the pick.  One request of 32003: 12.4 us, two launches and the pick's chain of
 // offsets, drafts, statistics, parts and places.
 #include <cmath>
 #include <type_traits>
@@ -107,8 +107,8 @@ __device__ inline double factor_of(double temperature) {
     return fmin(kLog2e / temperature, 0x1p830);
 }
 // What a sum by one maximum is multiplied by to become one by a larger: a power of two.
-// (A sum by -inf is n 2^-1000 for n elements, and what it is multiplied by is never above one: beside
-// a row's sum, of which the largest element alone is 2^-0.5 or more, it is nothing.)
+// (A sum by -inf is n 2^-1000 for n elements, and what it is multiplied by is never above one:
+// beside a row's sum, of which the largest element alone is 2^-0.5 or more, it is nothing.)
 __device__ inline double between(float from, float to, double factor) {
     const double d = shift_of(from, factor) - shift_of(to, factor);
     const int e = d > 0.0 ? 0 : d < -1020.0 ? -1020 : (int)d;
@@ -117,8 +117,8 @@ __device__ inline double between(float from, float to, double factor) {
 // Its exponent is n + j / 32 + f: an addition that leaves 32nds the last bit has n and j in the
 // low word, f is what is over, and 2^f the polynomial of degree 4 that goes through it at the
 // Chebyshev points of [-1/64, 1/64], 8e-14 off: as near as a running sum of 10^5 numbers in 64
-// bits is.  (Degree 3, 7e-11 off: 64 requests 73.8 against 74.7 us.)  The whole low word goes 15 bits up to the root's high
-// word, n into the exponent, and takes back j << 15.
+// bits is.  (Degree 3, 7e-11 off: 64 requests 73.8 against 74.7 us.)  The whole low word goes 15
+// bits up to the root's high word, n into the exponent, and takes back j << 15.
 struct Factors {
     double root, poly;  // their product is the power
 };
